@@ -41,7 +41,8 @@
  *    ran out, a sparse-output overflow) never trap: the offending work is
  *    skipped and a sticky per-device status word records the first one; read
  *    and clear it with pkm_get_device_error.
- *  - dtype applies to query, sub-keys, values, x, W1, W2, dy and out.
+ *  - dtype applies to query, sub-keys, values, x, W1, W2, dy and out unless
+ *    an entry point says otherwise.
  *    Row ids are int32, weights and gradients fp32.
  */
 #ifndef PKM_H
@@ -429,6 +430,141 @@ typedef struct {
 } pkm_engram_args;
 
 PKM_API pkm_status pkm_engram_forward(const pkm_engram_args *args, pkm_stream_t stream);
+
+/*
+ * Activations in 8 bits.  A row of d columns is cut into groups of
+ * PKM_Q8_GROUP columns (the last may be shorter); a group has one fp32 scale,
+ * the smallest power of two s >= 2^-100 with max |v| <= s * M (M = 448 for
+ * PKM_Q8_E4M3, 127 for PKM_Q8_INT8), and its elements are stored as v / s
+ * rounded to the format (nearest even; the division by a power of two is
+ * exact).  q * s has at most 8 significant bits: read back as bf16 it is
+ * exact.  A group holding a NaN or an infinity gets the scale NaN and reads
+ * back as NaN throughout; a magnitude within rounding of the largest fp32
+ * value may read back as infinity.
+ *   q [T, d] bytes (e4m3 or two's complement), scales fp32
+ *   [T, ceil(d / PKM_Q8_GROUP)].
+ * Limits everywhere: d a multiple of 8.
+ */
+typedef enum { PKM_Q8_NONE = 0, PKM_Q8_E4M3 = 1, PKM_Q8_INT8 = 2 } pkm_q8;
+#define PKM_Q8_GROUP 128
+
+/* x [T, d] (dtype) -> q, scales; and q, scales -> out [T, d] (dtype). */
+PKM_API pkm_status pkm_act8_store(const void *x, int64_t T, int32_t d, pkm_dtype dtype, pkm_q8 fmt,
+                                  void *q, float *scales, pkm_stream_t stream);
+PKM_API pkm_status pkm_act8_load(const void *q, const float *scales, int64_t T, int32_t d,
+                                 pkm_q8 fmt, void *out, pkm_dtype dtype, pkm_stream_t stream);
+
+/*
+ * The residual's addition and the root-mean-square norm that feed a memory
+ * layer.  Per row:
+ *   h = x + residual, rounded to dtype (x itself when residual is NULL)
+ *   rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight
+ *   x, residual [T, d], weight [d] (dtype; residual and weight may be NULL)
+ *   sum   [T, d] out (dtype): h, or NULL.  May be x or residual itself.
+ *   y     [T, d] out (dtype), or NULL.  May be x or residual itself, but not sum.
+ *   y8, scales: the 8-bit copy of y (fmt PKM_Q8_E4M3 or PKM_Q8_INT8, rounded
+ *         once, from the fp32 y), or y8 NULL with fmt PKM_Q8_NONE
+ *   rstd  [T] out (fp32), or NULL; the backward reads it.
+ * At least one of y and y8.  No other overlap between arguments.  fp32 sums
+ * in a fixed order.
+ * Limits: d a multiple of 8, d <= 16384; T < 2^31 - 64 (PKM_ERR_UNSUPPORTED
+ * above either); eps >= 0.
+ */
+typedef struct {
+    int64_t T;
+    int32_t d;
+    pkm_dtype dtype;
+    float eps;
+    pkm_q8 fmt;
+    const void *x;
+    const void *residual;
+    const void *weight;
+    void *sum;
+    void *y;
+    void *y8;
+    float *scales;
+    float *rstd;
+} pkm_norm_args;
+
+PKM_API pkm_status pkm_add_rmsnorm_forward(const pkm_norm_args *args, pkm_stream_t stream);
+
+/*
+ * Its backward.  With n = h * rstd and g = dy * weight:
+ *   dx      [T, d] out (dtype) = rstd * (g - n * mean(g * n)) + dsum: the
+ *           gradient of x and of residual alike.  May be dsum itself, or dy
+ *           where dy_dtype is dtype.
+ *   dweight [d] out (fp32) = sum over the rows of dy * n, or NULL
+ *   dy [T, d] (dy_dtype), dsum [T, d] (dtype; the gradient that reaches the
+ *           stored sum from elsewhere) or NULL, weight [d] (dtype) or NULL
+ *   sum     h [T, d] in dtype with fmt PKM_Q8_NONE, or its 8-bit copy with
+ *           scales and fmt
+ *   workspace of pkm_add_rmsnorm_backward_workspace_size bytes (only read
+ *           and written when dweight is given).
+ * Every sum runs in a fixed order.  Limits as in the forward; T = 0 writes
+ * a zero dweight.
+ */
+typedef struct {
+    int64_t T;
+    int32_t d;
+    pkm_dtype dtype;
+    pkm_dtype dy_dtype;
+    pkm_q8 fmt;
+    const void *dy;
+    const void *sum;
+    const float *scales;
+    const void *weight;
+    const float *rstd;
+    const void *dsum;
+    void *dx;
+    float *dweight;
+    void *workspace;
+    size_t workspace_bytes;
+} pkm_norm_bwd_args;
+
+PKM_API size_t pkm_add_rmsnorm_backward_workspace_size(const pkm_norm_bwd_args *args);
+PKM_API pkm_status pkm_add_rmsnorm_backward(const pkm_norm_bwd_args *args, pkm_stream_t stream);
+
+/*
+ * Token embedding with a scale, and its gradient by sorted tokens.
+ *   forward:   out[t] = scale * table[ids[t]]               (one rounding)
+ *   backward:  grad[r] = scale * sum of dout[t] over the t with ids[t] = r,
+ *              every row of grad written (zeros where no token reads it); with
+ *              accumulate != 0, added to grad instead, other rows left as
+ *              they are.  fp32 sums in token order cut at fixed places:
+ *              bitwise reproducible; one rounding.
+ *   table [n_rows, d], out and dout [T, d] (dtype), ids [T] int32 (device),
+ *   grad [n_rows, d] (grad_dtype).
+ * With has_pad != 0 positions whose id is pad_id are no token: a zero row in
+ * out, nothing in grad.  Any other id outside [0, n_rows) is treated the same
+ * and sets the device status.  The forward reads table and out, the backward
+ * dout, grad and a workspace of pkm_embed_workspace_size bytes.
+ * T = 0 is a valid empty call (the backward then zeroes grad unless it
+ * accumulates).
+ * Limits: d a multiple of 8, d <= 65536; T < 2^31 - 64 (PKM_ERR_UNSUPPORTED
+ * above either); 1 <= n_rows < 2^31; scale not NaN.
+ */
+typedef struct {
+    int64_t T;
+    int64_t n_rows;
+    int32_t d;
+    pkm_dtype dtype;
+    pkm_dtype grad_dtype;
+    float scale;
+    int32_t has_pad;
+    int32_t pad_id;
+    int32_t accumulate;
+    const int32_t *ids;
+    const void *table;
+    void *out;
+    const void *dout;
+    void *grad;
+    void *workspace;
+    size_t workspace_bytes;
+} pkm_embed_args;
+
+PKM_API size_t pkm_embed_workspace_size(const pkm_embed_args *args);
+PKM_API pkm_status pkm_embed_forward(const pkm_embed_args *args, pkm_stream_t stream);
+PKM_API pkm_status pkm_embed_backward(const pkm_embed_args *args, pkm_stream_t stream);
 
 /*
  * Failure-path check of the bounded waits (no counterpart on the pages; a

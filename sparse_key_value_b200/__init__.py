@@ -15,11 +15,14 @@ from typing import Optional
 
 import torch
 
-from ._lib import (PKM_BF16, PKM_F32, PKMError, BwdArgs, FwdArgs, check, load)
+from . import _lib
+from ._lib import (PKM_BF16, PKM_F32, PKM_Q8_E4M3, PKM_Q8_INT8, PKM_Q8_NONE, Q8_GROUP, PKMError,
+                   BwdArgs, FwdArgs, check, load)
 
 __all__ = ["PKMError", "load", "pkm_forward", "pkm_backward", "embbag_forward",
            "embbag_backward", "forward_workspace_size", "backward_workspace_size",
-           "device_error", "fwd_args"]
+           "device_error", "fwd_args", "embedding_forward", "embedding_backward",
+           "add_rmsnorm_forward", "add_rmsnorm_backward", "act8_store", "act8_load"]
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -380,3 +383,222 @@ def check_wait_timeout(polls: int = 4096, device=None, stream=None) -> int:
     if int(done.item()) != 1:
         raise RuntimeError(f"the waiting kernel did not finish as expected ({int(done.item())})")
     return code
+
+
+def _same_device(dev: torch.device, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {t.device} and {dev}")
+
+
+def _shape(name: str, t: Optional[torch.Tensor], shape, dtype=None):
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+
+
+def _enqueue(fn: str, args, dev: torch.device, stream):
+    """Call the entry point with ``args`` on the tensors' device and stream."""
+    f = getattr(load(), fn)
+    if torch.cuda.current_device() == dev.index:
+        check(f(*args, _stream(dev, stream)), fn)
+    else:
+        with torch.cuda.device(dev):
+            check(f(*args, _stream(dev, stream)), fn)
+
+
+def _workspace(workspace, need: int, dev: torch.device):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _need_cuda(workspace)
+    _same_device(dev, workspace)
+    return workspace
+
+
+def _embed_args(ids, n_rows, d, dtype, scale, pad_id) -> "_lib.EmbedArgs":
+    _need_cuda(ids)
+    if ids.dtype != torch.int32:
+        raise TypeError("ids must be int32")
+    a = _lib.EmbedArgs()
+    a.T, a.n_rows, a.d, a.dtype, a.scale = ids.numel(), n_rows, d, dtype, scale
+    if pad_id is not None:
+        if not -2 ** 31 <= pad_id < 2 ** 31:  # ctypes would cut it silently
+            raise ValueError(f"pad_id {pad_id} is not an int32")
+        a.has_pad, a.pad_id = 1, pad_id
+    a.ids = _p(ids)
+    return a
+
+
+def embedding_forward(table, ids, scale: float = 1.0, pad_id: Optional[int] = None, out=None,
+                      stream=None):
+    """out[t] = scale * table[ids[t]] (see pkm_embed_forward in include/pkm.h).
+
+    table [n_rows, d], ids int32 of any shape; out [*ids.shape, d].
+    Positions holding ``pad_id`` give a zero row."""
+    _need_cuda(table, out)
+    n_rows, d = table.shape
+    dev = table.device
+    a = _embed_args(ids, n_rows, d, _dt(table), scale, pad_id)
+    if out is None:
+        out = torch.empty(*ids.shape, d, dtype=table.dtype, device=dev)
+    _shape("out", out, (*ids.shape, d), table.dtype)
+    _same_device(dev, ids, out)
+    a.table, a.out = _p(table), _p(out)
+    _enqueue("pkm_embed_forward", (ctypes.byref(a),), dev, stream)
+    return out
+
+
+def embedding_backward(dout, ids, n_rows: int, scale: float = 1.0, pad_id: Optional[int] = None,
+                       grad=None, accumulate: bool = False, grad_dtype=torch.float32,
+                       workspace=None, stream=None):
+    """Gradient of embedding_forward's table (see pkm_embed_backward in
+    include/pkm.h): grad[r] = scale * the sum of dout over the positions of r.
+
+    dout [*ids.shape, d]; returns grad [n_rows, d] (``grad_dtype``, or the
+    given tensor), every row written, or added to with ``accumulate``."""
+    _need_cuda(dout, grad)
+    d = dout.shape[-1]
+    dev = dout.device
+    _shape("dout", dout, (*ids.shape, d))
+    if accumulate and grad is None:
+        raise ValueError("accumulate needs grad")
+    a = _embed_args(ids, n_rows, d, _dt(dout), scale, pad_id)
+    if grad is None:
+        grad = torch.empty(n_rows, d, dtype=grad_dtype, device=dev)
+    _shape("grad", grad, (n_rows, d))
+    a.grad_dtype, a.accumulate = _dt(grad), 1 if accumulate else 0
+    need = int(load().pkm_embed_workspace_size(ctypes.byref(a)))
+    workspace = _workspace(workspace, need, dev)
+    _same_device(dev, ids, grad)
+    a.dout, a.grad, a.workspace, a.workspace_bytes = _p(dout), _p(grad), _p(workspace), \
+        workspace.numel() * workspace.element_size()
+    _enqueue("pkm_embed_backward", (ctypes.byref(a),), dev, stream)
+    return grad
+
+
+_Q8 = {"e4m3": (PKM_Q8_E4M3, torch.float8_e4m3fn), "int8": (PKM_Q8_INT8, torch.int8)}
+
+
+def _q8_fmt(q: torch.Tensor) -> int:
+    for fmt, dtype in _Q8.values():
+        if q.dtype == dtype:
+            return fmt
+    raise TypeError(f"8-bit values must be float8_e4m3fn or int8, not {q.dtype}")
+
+
+def _q8_name(fmt: str):
+    if fmt not in _Q8:
+        raise ValueError(f"fmt {fmt!r}: 'e4m3' or 'int8'")
+    return _Q8[fmt]
+
+
+def _q8_empty(T: int, d: int, dtype, dev):
+    return (torch.empty(T, d, dtype=dtype, device=dev),
+            torch.empty(T, (d + Q8_GROUP - 1) // Q8_GROUP, dtype=torch.float32, device=dev))
+
+
+def _q8_check(name: str, q, scales):
+    """Checks an 8-bit activation and its scales; returns (T, d, fmt)."""
+    _need_cuda(q, scales)
+    fmt = _q8_fmt(q)
+    T, d = q.shape
+    _shape(f"{name} scales", scales, (T, (d + Q8_GROUP - 1) // Q8_GROUP), torch.float32)
+    _same_device(q.device, scales)
+    return T, d, fmt
+
+
+def act8_store(x, fmt: str = "int8", stream=None):
+    """x [T, d] in 8 bits (see pkm_act8_store in include/pkm.h): returns
+    (q [T, d] float8_e4m3fn or int8, scales fp32 [T, ceil(d / 128)])."""
+    _need_cuda(x)
+    code, dtype = _q8_name(fmt)
+    T, d = x.shape
+    q, scales = _q8_empty(T, d, dtype, x.device)
+    _enqueue("pkm_act8_store", (_p(x), T, d, _dt(x), code, _p(q), _p(scales)), x.device, stream)
+    return q, scales
+
+
+def act8_load(q, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """The values act8_store's (or add_rmsnorm_forward's) 8 bits stand for,
+    exact in bf16."""
+    T, d, fmt = _q8_check("act8", q, scales)
+    _need_cuda(out)
+    if out is None:
+        out = torch.empty(T, d, dtype=dtype, device=q.device)
+    _shape("out", out, (T, d))
+    _same_device(q.device, out)
+    _enqueue("pkm_act8_load", (_p(q), _p(scales), T, d, fmt, _p(out), _dt(out)), q.device, stream)
+    return out
+
+
+def add_rmsnorm_forward(x, weight=None, residual=None, eps: float = 1e-6,
+                        fmt: Optional[str] = None, want_y: bool = True, sum_out=None,
+                        stream=None):
+    """h = x + residual, y = h / rms(h) * weight (see pkm_add_rmsnorm_forward
+    in include/pkm.h).
+
+    x, residual [T, d], weight [d].  Returns dict(sum (x itself without a
+    residual), y (None unless ``want_y``), rstd fp32 [T], and with ``fmt``
+    ('e4m3' or 'int8') q8, scales: y in 8 bits).  ``sum_out`` may be x or
+    residual, to add in place."""
+    _need_cuda(x, weight, residual, sum_out)
+    T, d = x.shape
+    dev, dt = x.device, x.dtype
+    _shape("residual", residual, (T, d), dt)
+    _shape("weight", weight, (d,), dt)
+    _shape("sum_out", sum_out, (T, d), dt)
+    _same_device(dev, weight, residual, sum_out)
+    h = sum_out
+    if h is None and residual is not None:
+        h = torch.empty_like(x)
+    y = torch.empty_like(x) if want_y else None
+    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    q = scales = None
+    code = PKM_Q8_NONE
+    if fmt is not None:
+        code, qdt = _q8_name(fmt)
+        q, scales = _q8_empty(T, d, qdt, dev)
+    a = _lib.NormArgs(T, d, _dt(x), eps, code, _p(x), _p(residual), _p(weight), _p(h), _p(y),
+                      _p(q), _p(scales), _p(rstd))
+    _enqueue("pkm_add_rmsnorm_forward", (ctypes.byref(a),), dev, stream)
+    return dict(sum=x if h is None else h, y=y, rstd=rstd, q8=q, scales=scales)
+
+
+def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, scales=None, want_dweight: bool = True,
+                         workspace=None, stream=None):
+    """Backward of add_rmsnorm_forward (see pkm_add_rmsnorm_backward in
+    include/pkm.h).
+
+    dy [T, d] (bf16 or fp32); ``sum`` the forward's h [T, d], or its 8-bit
+    copy together with ``scales`` (act8_store); dsum the gradient that
+    reaches the stored sum from elsewhere.  Returns dict(dx: the gradient of
+    x and of the residual, in the type of dsum, weight or dy; dweight fp32 [d])."""
+    _need_cuda(dy, sum, weight, rstd, dsum)
+    T, d = dy.shape
+    dev = dy.device
+    fmt = PKM_Q8_NONE
+    if scales is not None:
+        _, _, fmt = _q8_check("sum", sum, scales)
+        like = dsum if dsum is not None else weight if weight is not None else dy
+        dt = like.dtype
+    else:
+        dt = sum.dtype
+    _shape("sum", sum, (T, d))
+    _shape("weight", weight, (d,), dt)
+    _shape("rstd", rstd, (T,), torch.float32)
+    _shape("dsum", dsum, (T, d), dt)
+    _same_device(dev, sum, scales, weight, rstd, dsum)
+    dx = torch.empty(T, d, dtype=dt, device=dev)
+    dweight = torch.empty(d, dtype=torch.float32, device=dev) if want_dweight else None
+    a = _lib.NormBwdArgs(T, d, _dt(dx), _dt(dy), fmt, _p(dy), _p(sum), _p(scales), _p(weight),
+                         _p(rstd), _p(dsum), _p(dx), _p(dweight), None, 0)
+    if want_dweight:
+        need = int(load().pkm_add_rmsnorm_backward_workspace_size(ctypes.byref(a)))
+        workspace = _workspace(workspace, need, dev)
+        a.workspace, a.workspace_bytes = _p(workspace), \
+            workspace.numel() * workspace.element_size()
+    _enqueue("pkm_add_rmsnorm_backward", (ctypes.byref(a),), dev, stream)
+    return dict(dx=dx, dweight=dweight)

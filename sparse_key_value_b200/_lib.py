@@ -17,6 +17,8 @@ PKM_OK = 0
 STATUS = {0: "PKM_OK", 1: "PKM_ERR_INVALID_ARG", 2: "PKM_ERR_UNSUPPORTED", 3: "PKM_ERR_CUDA",
           4: "PKM_ERR_DEVICE", 5: "PKM_ERR_TIMEOUT", 6: "PKM_ERR_WORKSPACE"}
 PKM_F32, PKM_BF16 = 0, 1
+PKM_Q8_NONE, PKM_Q8_E4M3, PKM_Q8_INT8 = 0, 1, 2
+Q8_GROUP = 128
 
 P = ctypes.c_void_p
 I32, I64, SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
@@ -73,13 +75,36 @@ class EngramArgs(ctypes.Structure):
                 ("e", P)]
 
 
+class NormArgs(ctypes.Structure):
+    _fields_ = [("T", I64), ("d", I32), ("dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("fmt", ctypes.c_int), ("x", P), ("residual", P), ("weight", P), ("sum", P),
+                ("y", P), ("y8", P), ("scales", P), ("rstd", P)]
+
+
+class NormBwdArgs(ctypes.Structure):
+    _fields_ = [("T", I64), ("d", I32), ("dtype", ctypes.c_int), ("dy_dtype", ctypes.c_int),
+                ("fmt", ctypes.c_int), ("dy", P), ("sum", P), ("scales", P), ("weight", P),
+                ("rstd", P), ("dsum", P), ("dx", P), ("dweight", P), ("workspace", P),
+                ("workspace_bytes", SZ)]
+
+
+class EmbedArgs(ctypes.Structure):
+    _fields_ = [("T", I64), ("n_rows", I64), ("d", I32), ("dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("scale", ctypes.c_float), ("has_pad", I32),
+                ("pad_id", I32), ("accumulate", I32), ("ids", P), ("table", P), ("out", P),
+                ("dout", P), ("grad", P), ("workspace", P), ("workspace_bytes", SZ)]
+
+
 EXPORTS = ("pkm_forward_workspace_size", "pkm_forward", "pkm_backward_workspace_size",
            "pkm_backward", "embbag_forward", "embbag_backward_workspace_size",
            "embbag_backward", "pkm_get_device_error", "pkm_status_string", "pkm_version",
            "pkm_launch_count", "pkm_forward_noalloc", "pkm_memplus_backward_workspace_size",
            "pkm_memplus_backward", "pkm_qproj_workspace_size", "pkm_qproj_forward",
            "pkm_qproj_backward", "pkm_sparse_optimizer_step", "pkm_engram_forward",
-           "pkm_select", "embbag_forward_range", "pkm_check_wait_timeout")
+           "pkm_select", "embbag_forward_range", "pkm_check_wait_timeout", "pkm_act8_store",
+           "pkm_act8_load", "pkm_add_rmsnorm_forward", "pkm_add_rmsnorm_backward_workspace_size",
+           "pkm_add_rmsnorm_backward", "pkm_embed_workspace_size", "pkm_embed_forward",
+           "pkm_embed_backward")
 
 _lib = None
 
@@ -139,6 +164,19 @@ def load(path: str = LIB_PATH):
     lib.pkm_engram_forward.restype = ctypes.c_int
     lib.pkm_sparse_optimizer_step.argtypes = [ctypes.POINTER(SparseOptArgs), P]
     lib.pkm_sparse_optimizer_step.restype = ctypes.c_int
+    CI = ctypes.c_int
+    for name, args in (("pkm_act8_store", [P, I64, I32, CI, CI, P, P, P]),
+                       ("pkm_act8_load", [P, P, I64, I32, CI, P, CI, P]),
+                       ("pkm_add_rmsnorm_forward", [ctypes.POINTER(NormArgs), P]),
+                       ("pkm_add_rmsnorm_backward", [ctypes.POINTER(NormBwdArgs), P]),
+                       ("pkm_embed_forward", [ctypes.POINTER(EmbedArgs), P]),
+                       ("pkm_embed_backward", [ctypes.POINTER(EmbedArgs), P])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = CI
+    for name, arg in (("pkm_add_rmsnorm_backward_workspace_size", NormBwdArgs),
+                      ("pkm_embed_workspace_size", EmbedArgs)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(arg)]
+        getattr(lib, name).restype = SZ
     if path == LIB_PATH:
         _lib = lib
     return lib

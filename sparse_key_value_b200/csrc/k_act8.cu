@@ -1,0 +1,124 @@
+// k_act8.cu -- activations stored in 8 bits and read back (formats and scale
+// rule in q8.cuh).
+//
+// A half-warp holds a group of 128 columns, one 8-column unit per lane, so
+// the group's maximum is four shuffles and every row access is a contiguous
+// 16-byte (8-byte for the 8-bit side) load or store per lane.  Bound by
+// memory: b bytes read and one written per element, four bytes per group for
+// the scale.
+#include "kernels.h"
+#include "q8.cuh"
+
+namespace pkm {
+
+namespace {
+constexpr int kThreads = 256;
+
+template <pkm_dtype DT>
+__global__ void __launch_bounds__(kThreads) act8_store_kernel(
+    const typename Elem<DT>::T* __restrict__ x, int64_t n_groups, int groups, int d, pkm_q8 fmt,
+    uint8_t* __restrict__ q, float* __restrict__ scales) {
+  const int64_t gi = (int64_t)blockIdx.x * (kThreads / kGroupLanes) + threadIdx.x / kGroupLanes;
+  const int64_t row = gi / groups;
+  const int col = (int)(gi - row * groups) * kQ8Group + (threadIdx.x % kGroupLanes) * kUnit;
+  const bool live = gi < n_groups && col < d;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (live) load8<DT>(x + row * d + col, v);
+  const float s = q8_scale(group_amax_bits(v), fmt);
+  if (live) *reinterpret_cast<uint2*>(q + row * d + col) = q8_encode(v, q8_inverse(s), fmt);
+  if (gi < n_groups && threadIdx.x % kGroupLanes == 0) scales[gi] = s;
+}
+
+template <pkm_dtype DT>
+__global__ void __launch_bounds__(kThreads) act8_load_kernel(
+    const uint8_t* __restrict__ q, const float* __restrict__ scales, int64_t n_groups, int groups,
+    int d, pkm_q8 fmt, typename Elem<DT>::T* __restrict__ out) {
+  const int64_t gi = (int64_t)blockIdx.x * (kThreads / kGroupLanes) + threadIdx.x / kGroupLanes;
+  const int64_t row = gi / groups;
+  const int col = (int)(gi - row * groups) * kQ8Group + (threadIdx.x % kGroupLanes) * kUnit;
+  if (gi >= n_groups || col >= d) return;
+  float v[8];
+  q8_decode(*reinterpret_cast<const uint2*>(q + row * d + col), scales[gi], fmt, v);
+  store8<DT>(out + row * d + col, v);
+}
+
+unsigned group_grid(int64_t n_groups) {
+  return (unsigned)((n_groups + kThreads / kGroupLanes - 1) / (kThreads / kGroupLanes));
+}
+}  // namespace
+
+cudaError_t launch_act8_store(const void* x, int64_t T, int d, pkm_dtype dt, pkm_q8 fmt, void* q,
+                              float* scales, cudaStream_t stream) {
+  const int g = q8_groups(d);
+  const int64_t n = T * g;
+  if (n <= 0) return cudaSuccess;
+  if (dt == PKM_BF16)
+    act8_store_kernel<PKM_BF16><<<group_grid(n), kThreads, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(x), n, g, d, fmt, static_cast<uint8_t*>(q), scales);
+  else
+    act8_store_kernel<PKM_F32><<<group_grid(n), kThreads, 0, stream>>>(
+        static_cast<const float*>(x), n, g, d, fmt, static_cast<uint8_t*>(q), scales);
+  note_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_act8_load(const void* q, const float* scales, int64_t T, int d, pkm_q8 fmt,
+                             void* out, pkm_dtype dt, cudaStream_t stream) {
+  const int g = q8_groups(d);
+  const int64_t n = T * g;
+  if (n <= 0) return cudaSuccess;
+  if (dt == PKM_BF16)
+    act8_load_kernel<PKM_BF16><<<group_grid(n), kThreads, 0, stream>>>(
+        static_cast<const uint8_t*>(q), scales, n, g, d, fmt, static_cast<__nv_bfloat16*>(out));
+  else
+    act8_load_kernel<PKM_F32><<<group_grid(n), kThreads, 0, stream>>>(
+        static_cast<const uint8_t*>(q), scales, n, g, d, fmt, static_cast<float*>(out));
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace pkm
+
+using namespace pkm;
+
+namespace {
+bool aligned(const void* p, uintptr_t a) {
+  return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+pkm_status act8_validate(const void* x, int64_t T, int32_t d, pkm_dtype dtype, pkm_q8 fmt,
+                         const void* q, const float* scales) {
+  if (T < 0 || d < 8 || d % 8 || (dtype != PKM_F32 && dtype != PKM_BF16) ||
+      (fmt != PKM_Q8_E4M3 && fmt != PKM_Q8_INT8))
+    return PKM_ERR_INVALID_ARG;
+  // the grid holds 16 groups per block
+  if (T > kMaxTokens || T > ((int64_t(1) << 31) - 1) * 16 / q8_groups(d))
+    return PKM_ERR_UNSUPPORTED;
+  if (T > 0 && (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, 16)))
+    return PKM_ERR_INVALID_ARG;
+  return PKM_OK;
+}
+}  // namespace
+
+extern "C" {
+
+PKM_API pkm_status pkm_act8_store(const void* x, int64_t T, int32_t d, pkm_dtype dtype, pkm_q8 fmt,
+                                  void* q, float* scales, pkm_stream_t stream) {
+  const pkm_status s = act8_validate(x, T, d, dtype, fmt, q, scales);
+  if (s != PKM_OK || T == 0) return s;
+  return launch_act8_store(x, T, d, dtype, fmt, q, scales,
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKM_OK
+             : PKM_ERR_CUDA;
+}
+
+PKM_API pkm_status pkm_act8_load(const void* q, const float* scales, int64_t T, int32_t d,
+                                 pkm_q8 fmt, void* out, pkm_dtype dtype, pkm_stream_t stream) {
+  const pkm_status s = act8_validate(out, T, d, dtype, fmt, q, scales);
+  if (s != PKM_OK || T == 0) return s;
+  return launch_act8_load(q, scales, T, d, fmt, out, dtype,
+                          reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKM_OK
+             : PKM_ERR_CUDA;
+}
+
+}  // extern "C"

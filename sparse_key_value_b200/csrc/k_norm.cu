@@ -1,0 +1,385 @@
+// k_norm.cu -- the residual's addition and the root-mean-square norm in front
+// of a memory layer, with its output in 16 (or 32) and in 8 bits, and its
+// backward.
+//
+// Forward, per row: h = x + r rounded to the storage type (the value the rest
+// of the network sees, so the backward differentiates the same one),
+// rstd = (mean h^2 + eps)^-1/2, y = h rstd w.  The 8-bit copy is rounded from
+// the fp32 y, not from its 16-bit rounding.
+// Backward: n = h rstd, g = dy w, dx = rstd (g - n mean(g n)) + dsum,
+// dweight = sum over rows of dy n.
+//
+// Both are bound by memory: every tensor is read or written once, a row stays
+// in registers between its sum and its outputs.  A row belongs to WPR warps,
+// each lane holding NU units of 8 columns; 16 consecutive lanes hold a
+// quantisation group.
+#include <type_traits>
+
+#include "kernels.h"
+#include "q8.cuh"
+
+namespace pkm {
+
+namespace {
+
+constexpr int kNormThreads = 256;
+
+constexpr int block_threads(int wpr) { return wpr * 32 > kNormThreads ? wpr * 32 : kNormThreads; }
+
+// Sum over the row's WPR warps (the warps of a row are consecutive); every
+// thread of the block calls it.  Fixed order: the same bits every run.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if constexpr (WPR > 1) {
+    const int warp = threadIdx.x >> 5;
+    __syncthreads();  // the previous use of `red` has been read
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) v += red[warp / WPR * WPR + w];
+  }
+  return v;
+}
+
+struct NormFwd {
+  int64_t T;
+  int d;
+  float eps;
+  pkm_q8 fmt;
+  const void *x, *r, *w;
+  void *sum, *y;
+  uint8_t* y8;
+  float *scales, *rstd;
+};
+
+template <pkm_dtype DT, int NU, int WPR>
+__global__ void __launch_bounds__(block_threads(WPR)) norm_fwd_kernel(const NormFwd p) {
+  using E = typename Elem<DT>::T;
+  __shared__ float red[block_threads(WPR) / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kRows = block_threads(WPR) / 32 / WPR;
+  const int64_t row = (int64_t)blockIdx.x * kRows + warp / WPR;
+  const bool live = row < p.T;
+  const int col0 = ((warp % WPR) * 32 + lane) * kUnit;
+  const int64_t base = row * p.d;
+  float h[NU][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < NU; ++c) {
+    const int col = col0 + c * (WPR * 32 * kUnit);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[c][e] = 0.f;
+    if (live && col < p.d) load8<DT>(static_cast<const E*>(p.x) + base + col, h[c]);
+  }
+  if (p.r) {
+    float r[NU][8];
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      const int col = col0 + c * (WPR * 32 * kUnit);
+      if (live && col < p.d) {
+        load8<DT>(static_cast<const E*>(p.r) + base + col, r[c]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[c][e] += r[c][e];
+        round8<DT>(h[c]);
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NU; ++c) {
+    const int col = col0 + c * (WPR * 32 * kUnit);
+    if (p.sum && live && col < p.d) store8<DT>(static_cast<E*>(p.sum) + base + col, h[c]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(h[c][e], h[c][e], ss);
+  }
+  ss = row_sum<WPR>(ss, red);
+  const float rstd = 1.0f / sqrtf(ss / (float)p.d + p.eps);
+  if (live && p.rstd && col0 == 0) p.rstd[row] = rstd;
+  const int groups = q8_groups(p.d);
+#pragma unroll
+  for (int c = 0; c < NU; ++c) {
+    const int col = col0 + c * (WPR * 32 * kUnit);
+    const bool in = live && col < p.d;
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.f;
+    if (p.w && in) load8<DT>(static_cast<const E*>(p.w) + col, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[c][e] = h[c][e] * rstd * w[e];
+    if (p.y && in) store8<DT>(static_cast<E*>(p.y) + base + col, h[c]);
+    if (p.y8) {
+      if (!in) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[c][e] = 0.f;
+      }
+      const float s = q8_scale(group_amax_bits(h[c]), p.fmt);
+      if (in) {
+        *reinterpret_cast<uint2*>(p.y8 + base + col) = q8_encode(h[c], q8_inverse(s), p.fmt);
+        if (lane % kGroupLanes == 0) p.scales[row * groups + col / kQ8Group] = s;
+      }
+    }
+  }
+}
+
+struct NormBwd {
+  int64_t T;
+  int d;
+  pkm_q8 fmt;  // PKM_Q8_NONE: h in the storage type
+  const void *dy, *h, *w, *dsum;
+  const float *scales, *rstd;
+  void* dx;
+  float* part;  // [blocks, d] weight-gradient partials, or null
+};
+
+// DY: type of dy; DT: type of h (when not 8-bit), weight, dsum and dx.
+template <pkm_dtype DT, pkm_dtype DY, int NU, int WPR>
+__global__ void __launch_bounds__(block_threads(WPR)) norm_bwd_kernel(const NormBwd p) {
+  using E = typename Elem<DT>::T;
+  using Ey = typename Elem<DY>::T;
+  constexpr int kWarps = block_threads(WPR) / 32;
+  constexpr int kTeams = kWarps / WPR;  // rows in flight per block
+  __shared__ float red[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = warp / WPR;
+  const int col0 = ((warp % WPR) * 32 + lane) * kUnit;
+  const int groups = q8_groups(p.d);
+  float dw[NU][8];
+#pragma unroll
+  for (int c = 0; c < NU; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[c][e] = 0.f;
+  // every team of the block makes the same number of rounds (row_sum syncs)
+  for (int64_t r0 = (int64_t)blockIdx.x * kTeams; r0 < p.T; r0 += (int64_t)gridDim.x * kTeams) {
+    const int64_t row = r0 + team;
+    const bool live = row < p.T;
+    const int64_t base = row * p.d;
+    const float rstd = live ? p.rstd[row] : 0.f;
+    float g[NU][8], n[NU][8];
+    float dot = 0.f;
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      const int col = col0 + c * (WPR * 32 * kUnit);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[c][e] = n[c][e] = 0.f;
+      if (live && col < p.d) {
+        load8<DY>(static_cast<const Ey*>(p.dy) + base + col, g[c]);
+        if (p.fmt == PKM_Q8_NONE)
+          load8<DT>(static_cast<const E*>(p.h) + base + col, n[c]);
+        else
+          q8_decode(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.h) + base + col),
+                    p.scales[row * groups + col / kQ8Group], p.fmt, n[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      const int col = col0 + c * (WPR * 32 * kUnit);
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 1.f;
+      if (p.w && col < p.d) load8<DT>(static_cast<const E*>(p.w) + col, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        n[c][e] *= rstd;
+        dw[c][e] = fmaf(g[c][e], n[c][e], dw[c][e]);
+        g[c][e] *= w[e];
+        dot = fmaf(g[c][e], n[c][e], dot);
+      }
+    }
+    const float mean = row_sum<WPR>(dot, red) / (float)p.d;
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      const int col = col0 + c * (WPR * 32 * kUnit);
+      if (!(live && col < p.d)) continue;
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = 0.f;
+      if (p.dsum) load8<DT>(static_cast<const E*>(p.dsum) + base + col, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] += rstd * (g[c][e] - n[c][e] * mean);
+      store8<DT>(static_cast<E*>(p.dx) + base + col, o);
+    }
+  }
+  if (!p.part) return;
+  // the block's teams in order, then one partial row per block
+  __shared__ float acc[kTeams > 1 ? kTeams - 1 : 1][NU * WPR * 32 * kUnit];
+  if (team > 0) {
+#pragma unroll
+    for (int c = 0; c < NU; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        acc[team - 1][col0 + c * (WPR * 32 * kUnit) + e] = dw[c][e];
+  }
+  __syncthreads();
+  if (team == 0) {
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      const int col = col0 + c * (WPR * 32 * kUnit);
+      if (col >= p.d) continue;
+#pragma unroll
+      for (int t = 1; t < kTeams; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[c][e] += acc[t - 1][col + e];
+      store8<PKM_F32>(p.part + (int64_t)blockIdx.x * p.d + col, dw[c]);
+    }
+  }
+}
+
+// dweight[c] = sum over blocks of part[block][c]: 32 columns per block, 8
+// row strides, joined in order
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int blocks,
+                                                      int d, float* __restrict__ dw) {
+  __shared__ float s[8][32];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+  float v = 0.f;
+  if (col < d)
+    for (int b = r; b < blocks; b += 8) v += part[(int64_t)b * d + col];
+  s[r][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (r == 0 && col < d) {
+    for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x];
+    dw[col] = v;
+  }
+}
+
+constexpr int kMaxD = 16384;
+constexpr int kBwdBlocks = 148 * 2;
+
+int rows_per_block(int wpr) { return wpr >= 8 ? 1 : 8 / wpr; }
+
+// Warps per row and units per lane: as few warps as hold the row with four
+// units a lane (no block barrier up to 1024 columns).
+template <typename F>
+cudaError_t norm_shape(int d, F&& f) {
+  if (d <= 256) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+  if (d <= 512) return f(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
+  if (d <= 1024) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+  if (d <= 2048) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+  if (d <= 4096) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+  if (d <= 8192) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 16>{});
+}
+
+int bwd_blocks(int64_t T, int d) {
+  int rows = 1;
+  norm_shape(d, [&](auto, auto wpr) {
+    rows = rows_per_block(decltype(wpr)::value);
+    return cudaSuccess;
+  });
+  const int64_t b = (T + rows - 1) / rows;
+  return (int)(b < kBwdBlocks ? b : kBwdBlocks);
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool need16(const void* p) { return p && al16(p); }
+
+template <pkm_dtype DT>
+cudaError_t fwd_launch(const NormFwd& p, cudaStream_t st) {
+  return norm_shape(p.d, [&](auto nu, auto wpr) {
+    constexpr int NU = decltype(nu)::value, WPR = decltype(wpr)::value;
+    const int rows = rows_per_block(WPR);
+    norm_fwd_kernel<DT, NU, WPR>
+        <<<(unsigned)((p.T + rows - 1) / rows), block_threads(WPR), 0, st>>>(p);
+    note_launch();
+    return cudaGetLastError();
+  });
+}
+
+template <pkm_dtype DT, pkm_dtype DY>
+cudaError_t bwd_launch(const NormBwd& p, float* dweight, cudaStream_t st) {
+  const int blocks = bwd_blocks(p.T, p.d);
+  const cudaError_t e = norm_shape(p.d, [&](auto nu, auto wpr) {
+    constexpr int NU = decltype(nu)::value, WPR = decltype(wpr)::value;
+    norm_bwd_kernel<DT, DY, NU, WPR><<<blocks, block_threads(WPR), 0, st>>>(p);
+    note_launch();
+    return cudaGetLastError();
+  });
+  if (e != cudaSuccess || !dweight) return e;
+  norm_dw_kernel<<<(p.d + 31) / 32, 256, 0, st>>>(p.part, blocks, p.d, dweight);
+  note_launch();
+  return cudaGetLastError();
+}
+
+pkm_status fwd_validate(const pkm_norm_args* a) {
+  if (!a || a->T < 0 || a->d < 8 || a->d % 8 || !(a->eps >= 0.f) ||
+      (a->dtype != PKM_F32 && a->dtype != PKM_BF16) ||
+      (a->fmt != PKM_Q8_NONE && a->fmt != PKM_Q8_E4M3 && a->fmt != PKM_Q8_INT8))
+    return PKM_ERR_INVALID_ARG;
+  if (a->d > kMaxD || a->T > (int64_t(1) << 31) - 64) return PKM_ERR_UNSUPPORTED;
+  if (a->T == 0) return PKM_OK;
+  if (!need16(a->x) || !al16(a->residual) || !al16(a->weight) || !al16(a->sum) || !al16(a->y) ||
+      !al16(a->y8) || !al16(a->rstd))
+    return PKM_ERR_INVALID_ARG;
+  if ((a->y8 != nullptr) != (a->fmt != PKM_Q8_NONE)) return PKM_ERR_INVALID_ARG;
+  if (a->y8 && !need16(a->scales)) return PKM_ERR_INVALID_ARG;
+  if (!a->y && !a->y8) return PKM_ERR_INVALID_ARG;
+  return PKM_OK;
+}
+
+size_t bwd_bytes(const pkm_norm_bwd_args* a) {
+  if (a->T <= 0 || a->d < 8 || a->d > kMaxD) return 0;
+  return (size_t)bwd_blocks(a->T, a->d) * (size_t)a->d * 4;
+}
+
+pkm_status bwd_validate(const pkm_norm_bwd_args* a) {
+  if (!a || a->T < 0 || a->d < 8 || a->d % 8 || (a->dtype != PKM_F32 && a->dtype != PKM_BF16) ||
+      (a->dy_dtype != PKM_F32 && a->dy_dtype != PKM_BF16) ||
+      (a->fmt != PKM_Q8_NONE && a->fmt != PKM_Q8_E4M3 && a->fmt != PKM_Q8_INT8))
+    return PKM_ERR_INVALID_ARG;
+  if (a->d > kMaxD || a->T > (int64_t(1) << 31) - 64) return PKM_ERR_UNSUPPORTED;
+  if (!al16(a->dweight)) return PKM_ERR_INVALID_ARG;
+  if (a->T == 0) return PKM_OK;
+  if (!need16(a->dy) || !need16(a->sum) || !need16(a->rstd) || !need16(a->dx) ||
+      !al16(a->weight) || !al16(a->dsum))
+    return PKM_ERR_INVALID_ARG;
+  if (a->fmt != PKM_Q8_NONE && !need16(a->scales)) return PKM_ERR_INVALID_ARG;
+  if (a->dweight && (!need16(a->workspace) || a->workspace_bytes < bwd_bytes(a)))
+    return PKM_ERR_WORKSPACE;
+  return PKM_OK;
+}
+
+}  // namespace
+}  // namespace pkm
+
+using namespace pkm;
+
+extern "C" {
+
+PKM_API pkm_status pkm_add_rmsnorm_forward(const pkm_norm_args* a, pkm_stream_t stream) {
+  const pkm_status s = fwd_validate(a);
+  if (s != PKM_OK || a->T == 0) return s;
+  const NormFwd p{a->T,   a->d, a->eps, a->fmt, a->x, a->residual, a->weight, a->sum,
+                  a->y,   static_cast<uint8_t*>(a->y8), a->scales, a->rstd};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      a->dtype == PKM_BF16 ? fwd_launch<PKM_BF16>(p, st) : fwd_launch<PKM_F32>(p, st);
+  return e == cudaSuccess ? PKM_OK : PKM_ERR_CUDA;
+}
+
+PKM_API size_t pkm_add_rmsnorm_backward_workspace_size(const pkm_norm_bwd_args* a) {
+  return a ? bwd_bytes(a) : 0;
+}
+
+PKM_API pkm_status pkm_add_rmsnorm_backward(const pkm_norm_bwd_args* a, pkm_stream_t stream) {
+  const pkm_status s = bwd_validate(a);
+  if (s != PKM_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (a->T == 0)
+    return a->dweight && cudaMemsetAsync(a->dweight, 0, sizeof(float) * (size_t)a->d, st) !=
+                             cudaSuccess
+               ? PKM_ERR_CUDA
+               : PKM_OK;
+  const NormBwd p{a->T, a->d,      a->fmt,  a->dy, a->sum, a->weight, a->dsum,
+                  a->scales, a->rstd, a->dx,
+                  a->dweight ? static_cast<float*>(a->workspace) : nullptr};
+  cudaError_t e;
+  if (a->dtype == PKM_BF16)
+    e = a->dy_dtype == PKM_BF16 ? bwd_launch<PKM_BF16, PKM_BF16>(p, a->dweight, st)
+                                : bwd_launch<PKM_BF16, PKM_F32>(p, a->dweight, st);
+  else
+    e = a->dy_dtype == PKM_BF16 ? bwd_launch<PKM_F32, PKM_BF16>(p, a->dweight, st)
+                                : bwd_launch<PKM_F32, PKM_F32>(p, a->dweight, st);
+  return e == cudaSuccess ? PKM_OK : PKM_ERR_CUDA;
+}
+
+}  // extern "C"

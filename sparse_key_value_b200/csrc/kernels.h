@@ -162,6 +162,12 @@ cudaError_t launch_sparse_opt(void* table, pkm_dtype dt, int64_t n_rows, int d,
                               float b2, float eps, int64_t step, int32_t* status,
                               cudaStream_t stream);
 
+// Activations in 8 bits (k_act8.cu; formats in q8.cuh).
+cudaError_t launch_act8_store(const void* x, int64_t T, int d, pkm_dtype dt, pkm_q8 fmt, void* q,
+                              float* scales, cudaStream_t stream);
+cudaError_t launch_act8_load(const void* q, const float* scales, int64_t T, int d, pkm_q8 fmt,
+                             void* out, pkm_dtype dt, cudaStream_t stream);
+
 // ---------------------------------------------------------------- backward
 // dw[t,j] = <dy[t], table[idx[t,j]]>; with H>0 also dS = w (dw - sum w dw)
 // per (t, h) group of k.

@@ -1,0 +1,117 @@
+"""Refusals of the operators around a memory layer, on the host: an invalid
+call returns its error and launches nothing (no GPU is needed)."""
+
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_key_value_b200 import build
+    build.build()
+    from sparse_key_value_b200 import _lib
+    return _lib.load()
+
+
+F = ctypes.c_void_p(1 << 20)         # 16-byte aligned, never dereferenced on the host
+ODD = ctypes.c_void_p((1 << 20) + 8)
+
+
+def _norm(**kw):
+    from sparse_key_value_b200 import _lib
+    base = dict(T=4, d=64, dtype=1, eps=1e-6, fmt=1, x=F, residual=F, weight=F, sum=F, y=F, y8=F,
+                scales=F, rstd=F)
+    return _lib.NormArgs(**{**base, **kw})
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(T=-1), 1), (dict(d=0), 1), (dict(d=60), 1), (dict(dtype=2), 1), (dict(eps=-1.0), 1),
+    (dict(eps=float("nan")), 1), (dict(fmt=0), 1), (dict(fmt=3), 1), (dict(y8=None), 1),
+    (dict(x=None), 1), (dict(x=ODD), 1), (dict(residual=ODD), 1), (dict(weight=ODD), 1),
+    (dict(sum=ODD), 1), (dict(y=ODD), 1), (dict(y8=ODD), 1), (dict(scales=None), 1),
+    (dict(rstd=ODD), 1), (dict(y=None, y8=None, fmt=0), 1), (dict(d=16392), 2),
+    (dict(T=2 ** 31), 2)])
+def test_norm_forward_refuses(lib, bad, code):
+    assert lib.pkm_add_rmsnorm_forward(ctypes.byref(_norm(**bad)), None) == code
+    assert lib.pkm_add_rmsnorm_forward(None, None) == 1
+
+
+def _norm_bwd(**kw):
+    from sparse_key_value_b200 import _lib
+    base = dict(T=4, d=64, dtype=1, dy_dtype=0, fmt=0, dy=F, sum=F, scales=None, weight=F, rstd=F,
+                dsum=F, dx=F, dweight=F, workspace=F, workspace_bytes=1 << 40)
+    return _lib.NormBwdArgs(**{**base, **kw})
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(T=-1), 1), (dict(d=4), 1), (dict(dtype=5), 1), (dict(dy_dtype=2), 1), (dict(fmt=7), 1),
+    (dict(dy=None), 1), (dict(sum=None), 1), (dict(rstd=None), 1), (dict(dx=None), 1),
+    (dict(dx=ODD), 1), (dict(dweight=ODD), 1), (dict(fmt=1), 1), (dict(fmt=2, scales=ODD), 1),
+    (dict(d=16392), 2), (dict(workspace=None), 6), (dict(workspace_bytes=64 * 4 - 1), 6)])
+def test_norm_backward_refuses(lib, bad, code):
+    assert lib.pkm_add_rmsnorm_backward(ctypes.byref(_norm_bwd(**bad)), None) == code
+
+
+def test_norm_workspace_and_empty(lib):
+    a = _norm_bwd()
+    assert lib.pkm_add_rmsnorm_backward_workspace_size(ctypes.byref(a)) >= 64 * 4
+    assert lib.pkm_add_rmsnorm_backward_workspace_size(None) == 0
+    assert lib.pkm_add_rmsnorm_forward(ctypes.byref(_norm(T=0, x=None)), None) == 0
+    # no weight gradient asked for: an empty call has nothing to do
+    assert lib.pkm_add_rmsnorm_backward(ctypes.byref(_norm_bwd(T=0, dweight=None)), None) == 0
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(T=-1), 1), (dict(d=12), 1), (dict(dtype=2), 1), (dict(fmt=0), 1), (dict(fmt=3), 1),
+    (dict(x=None), 1), (dict(x=ODD), 1), (dict(q=ODD), 1), (dict(s=ODD), 1), (dict(s=None), 1),
+    (dict(T=2 ** 36 + 1), 2), (dict(T=2 ** 36, d=1024), 2)])
+def test_act8_refuses(lib, bad, code):
+    k = {**dict(x=F, T=4, d=64, dtype=1, fmt=1, q=F, s=F), **bad}
+    assert lib.pkm_act8_store(k["x"], k["T"], k["d"], k["dtype"], k["fmt"], k["q"], k["s"],
+                              None) == code
+    assert lib.pkm_act8_load(k["q"], k["s"], k["T"], k["d"], k["fmt"], k["x"], k["dtype"],
+                             None) == code
+
+
+def _embed(**kw):
+    from sparse_key_value_b200 import _lib
+    base = dict(T=4, n_rows=10, d=64, dtype=1, grad_dtype=0, scale=1.0, has_pad=0, pad_id=0,
+                accumulate=0, ids=F, table=F, out=F, dout=F, grad=F, workspace=F,
+                workspace_bytes=1 << 40)
+    return _lib.EmbedArgs(**{**base, **kw})
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(T=-1), 1), (dict(n_rows=0), 1), (dict(n_rows=2 ** 31), 1), (dict(d=4), 1),
+    (dict(d=20), 1), (dict(dtype=9), 1), (dict(scale=float("nan")), 1), (dict(ids=None), 1),
+    (dict(ids=ODD), 1), (dict(T=2 ** 31), 2), (dict(d=65544), 2)])
+def test_embed_refuses(lib, bad, code):
+    assert lib.pkm_embed_forward(ctypes.byref(_embed(**bad)), None) == code
+    assert lib.pkm_embed_backward(ctypes.byref(_embed(**bad)), None) == code
+
+
+def test_embed_refuses_by_direction(lib):
+    fwd = lambda **k: lib.pkm_embed_forward(ctypes.byref(_embed(**k)), None)   # noqa: E731
+    bwd = lambda **k: lib.pkm_embed_backward(ctypes.byref(_embed(**k)), None)  # noqa: E731
+    assert fwd(table=None) == 1 and fwd(out=ODD) == 1
+    assert bwd(dout=None) == 1 and bwd(grad=ODD) == 1 and bwd(grad_dtype=4) == 1
+    assert bwd(T=0, grad=None) == 1
+    assert bwd(workspace=None) == 6
+    need = lib.pkm_embed_workspace_size(ctypes.byref(_embed()))
+    assert need > 0 and bwd(workspace_bytes=need - 1) == 6
+    assert fwd(T=0, ids=None) == 0
+    assert fwd(T=0) == 0 and lib.pkm_embed_workspace_size(None) == 0
+
+
+def test_binding_refuses_bad_tensors():
+    """The binding's own checks need no GPU: CPU tensors are refused."""
+    import sparse_key_value_b200 as skv
+    x = torch.zeros(4, 64)
+    ids = torch.zeros(4, dtype=torch.int32)
+    for call in (lambda: skv.act8_store(x), lambda: skv.add_rmsnorm_forward(x),
+                 lambda: skv.embedding_forward(x, ids),
+                 lambda: skv.embedding_backward(x, ids, 4)):
+        with pytest.raises(ValueError):
+            call()
