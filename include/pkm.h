@@ -567,6 +567,94 @@ PKM_API pkm_status pkm_embed_forward(const pkm_embed_args *args, pkm_stream_t st
 PKM_API pkm_status pkm_embed_backward(const pkm_embed_args *args, pkm_stream_t stream);
 
 /*
+ * Softmax cross entropy of an output layer over the vocabulary, without
+ * keeping the logits, and its gradients.
+ *   forward:  lse[t]  = log sum_v exp(<x[t], W[v]>)
+ *             loss[t] = lse[t] - <x[t], W[targets[t]]>
+ *   backward: d[t, v] = (exp(<x[t], W[v]> - lse[t]) - [v = targets[t]]) dloss[t]
+ *             dx = d W,  dW = d^T x
+ *   x [T, d], W [V, d] (bf16), targets [T] int32, lse, loss, dloss [T] fp32,
+ *   dx [T, d], dW [V, d] (grad_dtype; overwritten).
+ * A position whose target is ignore_index has no loss: loss 0 (lse is still
+ * written), a zero row of d whatever its dloss and lse hold, so a zero row of
+ * dx and nothing in dW as long as its x is finite (0 times NaN is NaN).
+ * Any other target outside [0, V) is treated the same and sets the device
+ * status in the forward.
+ * Products and sums are fp32 (exact bf16 products).  The backward recomputes
+ * the logits by pieces of the vocabulary and rounds d to bf16 once, the
+ * operand type of its products: dx and dW carry that half step per term also
+ * in fp32.  The forward reads x, W, targets; the backward also lse (the
+ * forward's) and dloss.  Each direction has its own workspace size (the
+ * backward's holds one piece of d, at most 256 MiB or 1024 columns, and fp32
+ * sums of dx).  Results are bitwise reproducible.
+ * Limits: dtype PKM_BF16 (PKM_F32: PKM_ERR_UNSUPPORTED); d a multiple of 8,
+ * d <= 65536; T <= 2^30; ceil(T / 256) * ceil(V / 256) < 2^30.  T = 0 is a
+ * valid empty call (the backward then zeroes dW).
+ */
+typedef struct {
+    int64_t T;
+    int32_t V;
+    int32_t d;
+    pkm_dtype dtype;
+    pkm_dtype grad_dtype;
+    int32_t ignore_index;
+    const void *x;
+    const void *W;
+    const int32_t *targets;
+    float *loss;
+    float *lse;
+    const float *dloss;
+    void *dx;
+    void *dW;
+    void *workspace;
+    size_t workspace_bytes;
+} pkm_xent_args;
+
+PKM_API size_t pkm_linear_xent_forward_workspace_size(const pkm_xent_args *args);
+PKM_API size_t pkm_linear_xent_backward_workspace_size(const pkm_xent_args *args);
+PKM_API pkm_status pkm_linear_xent_forward(const pkm_xent_args *args, pkm_stream_t stream);
+PKM_API pkm_status pkm_linear_xent_backward(const pkm_xent_args *args, pkm_stream_t stream);
+
+/*
+ * The Memory+ backward (pkm_memplus_backward above) from activations kept in
+ * 8 bits: x and y as pkm_act8_store or pkm_add_rmsnorm_forward wrote them,
+ * both in the format fmt.  The formulas are the same with the values that x8
+ * and y8 stand for.
+ *   x8 [T, d_model], y8 [T, d_v] and their scales; W1, W2, dout bf16
+ *   dy  [T, d_v] out (bf16)
+ *   dx  [T, d_model], dW1 [d_model, d_v], dW2 [d_v, d_model] out (grad_dtype,
+ *       overwritten)
+ * da and y ⊙ g are rounded to bf16 once as the operands of the products that
+ * give dx, dW1 and dW2.  Every sum runs in a fixed order.
+ * Limits: d_model, d_v multiples of 8 and <= 65536, T <= 2^28 and
+ * T * ceil(d_model / PKM_Q8_GROUP) < 2^34 (PKM_ERR_UNSUPPORTED above).  T = 0 is a valid empty call (dW1 and dW2 are
+ * zeroed).
+ */
+typedef struct {
+    int64_t T;
+    int32_t d_model, d_v;
+    pkm_q8 fmt;
+    pkm_dtype grad_dtype;
+    const void *x8;
+    const float *x_scales;
+    const void *W1;
+    const void *W2;
+    const void *y8;
+    const float *y_scales;
+    const void *dout;
+    void *dy;
+    void *dx;
+    void *dW1;
+    void *dW2;
+    void *workspace; /* pkm_memplus_backward_act8_workspace_size bytes */
+    size_t workspace_bytes;
+} pkm_memplus_bwd8_args;
+
+PKM_API size_t pkm_memplus_backward_act8_workspace_size(const pkm_memplus_bwd8_args *args);
+PKM_API pkm_status pkm_memplus_backward_act8(const pkm_memplus_bwd8_args *args,
+                                             pkm_stream_t stream);
+
+/*
  * Failure-path check of the bounded waits (no counterpart on the pages; a
  * service for tests and operators): one CTA waits, with the wait every
  * pipelined kernel of the library uses, on an mbarrier phase that nothing

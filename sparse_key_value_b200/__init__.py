@@ -22,7 +22,9 @@ from ._lib import (PKM_BF16, PKM_F32, PKM_Q8_E4M3, PKM_Q8_INT8, PKM_Q8_NONE, Q8_
 __all__ = ["PKMError", "load", "pkm_forward", "pkm_backward", "embbag_forward",
            "embbag_backward", "forward_workspace_size", "backward_workspace_size",
            "device_error", "fwd_args", "embedding_forward", "embedding_backward",
-           "add_rmsnorm_forward", "add_rmsnorm_backward", "act8_store", "act8_load"]
+           "add_rmsnorm_forward", "add_rmsnorm_backward", "act8_store", "act8_load",
+           "linear_xent_forward", "linear_xent_backward",
+           "memplus_backward_act8"]
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -602,3 +604,96 @@ def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, scales=None, want_dwe
             workspace.numel() * workspace.element_size()
     _enqueue("pkm_add_rmsnorm_backward", (ctypes.byref(a),), dev, stream)
     return dict(dx=dx, dweight=dweight)
+
+
+def _xent_args(x, W, targets, ignore_index: int) -> "_lib.XentArgs":
+    _need_cuda(x, W, targets)
+    T, d = x.shape
+    _shape("W", W, (W.shape[0], d), x.dtype)
+    _shape("targets", targets, (T,), torch.int32)
+    _same_device(x.device, W, targets)
+    if not -2 ** 31 <= ignore_index < 2 ** 31:
+        raise ValueError(f"ignore_index {ignore_index} is not an int32")
+    a = _lib.XentArgs()
+    a.T, a.V, a.d, a.dtype, a.ignore_index = T, W.shape[0], d, _dt(x), ignore_index
+    a.x, a.W, a.targets = _p(x), _p(W), _p(targets)
+    return a
+
+
+def linear_xent_forward(x, W, targets, ignore_index: int = -100, workspace=None, stream=None):
+    """Cross entropy of the output layer without keeping the logits (see
+    pkm_linear_xent_forward in include/pkm.h).
+
+    x [T, d], W [V, d] bf16, targets int32 [T].  Returns (loss, lse) fp32
+    [T]; positions whose target is ``ignore_index`` have loss 0."""
+    a = _xent_args(x, W, targets, ignore_index)
+    dev = x.device
+    loss = torch.empty(a.T, dtype=torch.float32, device=dev)
+    lse = torch.empty(a.T, dtype=torch.float32, device=dev)
+    a.loss, a.lse = _p(loss), _p(lse)
+    need = int(load().pkm_linear_xent_forward_workspace_size(ctypes.byref(a)))
+    workspace = _workspace(workspace, need, dev)
+    a.workspace, a.workspace_bytes = _p(workspace), workspace.numel() * workspace.element_size()
+    _enqueue("pkm_linear_xent_forward", (ctypes.byref(a),), dev, stream)
+    return loss, lse
+
+
+def linear_xent_backward(x, W, targets, lse, dloss, ignore_index: int = -100,
+                         grad_dtype=torch.float32, dx=None, dW=None, workspace=None, stream=None):
+    """Gradients of linear_xent_forward (see pkm_linear_xent_backward in
+    include/pkm.h): lse as the forward gave it, dloss fp32 [T] the upstream
+    gradient of each position's loss.  Returns (dx [T, d], dW [V, d]) in
+    ``grad_dtype`` (or the given tensors, overwritten)."""
+    a = _xent_args(x, W, targets, ignore_index)
+    dev = x.device
+    _need_cuda(lse, dloss, dx, dW)
+    _shape("lse", lse, (a.T,), torch.float32)
+    _shape("dloss", dloss, (a.T,), torch.float32)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=grad_dtype if dW is None else dW.dtype, device=dev)
+    if dW is None:
+        dW = torch.empty(W.shape, dtype=dx.dtype, device=dev)
+    _shape("dx", dx, x.shape)
+    _shape("dW", dW, W.shape, dx.dtype)
+    _same_device(dev, lse, dloss, dx, dW)
+    a.grad_dtype = _dt(dx)
+    a.lse, a.dloss, a.dx, a.dW = _p(lse), _p(dloss), _p(dx), _p(dW)
+    need = int(load().pkm_linear_xent_backward_workspace_size(ctypes.byref(a)))
+    workspace = _workspace(workspace, need, dev)
+    a.workspace, a.workspace_bytes = _p(workspace), workspace.numel() * workspace.element_size()
+    _enqueue("pkm_linear_xent_backward", (ctypes.byref(a),), dev, stream)
+    return dx, dW
+
+
+def memplus_backward_act8(x8, x_scales, W1, W2, y8, y_scales, dout, grad_dtype=torch.float32,
+                          workspace=None, stream=None):
+    """Backward of the Memory+ block from 8-bit activations (see
+    pkm_memplus_backward_act8 in include/pkm.h).
+
+    x8, x_scales and y8, y_scales: the gate's input [T, d_model] and the bag
+    output [T, d_v] as act8_store (or add_rmsnorm_forward) wrote them, in one
+    format; W1 [d_model, d_v], W2 [d_v, d_model], dout [T, d_model] bf16.
+    Returns dict(dy (bf16), dx, dW1, dW2 (``grad_dtype``))."""
+    T, dm, fmt = _q8_check("x8", x8, x_scales)
+    T2, dv, fmt2 = _q8_check("y8", y8, y_scales)
+    if T2 != T or fmt2 != fmt:
+        raise ValueError("x8 and y8: one number of rows and one format")
+    _need_cuda(W1, W2, dout)
+    bf = torch.bfloat16
+    _shape("W1", W1, (dm, dv), bf)
+    _shape("W2", W2, (dv, dm), bf)
+    _shape("dout", dout, (T, dm), bf)
+    dev = x8.device
+    _same_device(dev, y8, W1, W2, dout)
+    dy = torch.empty(T, dv, dtype=bf, device=dev)
+    dx = torch.empty(T, dm, dtype=grad_dtype, device=dev)
+    dW1 = torch.empty(dm, dv, dtype=grad_dtype, device=dev)
+    dW2 = torch.empty(dv, dm, dtype=grad_dtype, device=dev)
+    a = _lib.MemplusBwd8Args(T, dm, dv, fmt, _dt(dx), _p(x8), _p(x_scales), _p(W1), _p(W2),
+                             _p(y8), _p(y_scales), _p(dout), _p(dy), _p(dx), _p(dW1), _p(dW2),
+                             None, 0)
+    need = int(load().pkm_memplus_backward_act8_workspace_size(ctypes.byref(a)))
+    workspace = _workspace(workspace, need, dev)
+    a.workspace, a.workspace_bytes = _p(workspace), workspace.numel() * workspace.element_size()
+    _enqueue("pkm_memplus_backward_act8", (ctypes.byref(a),), dev, stream)
+    return dict(dy=dy, dx=dx, dW1=dW1, dW2=dW2)

@@ -95,6 +95,20 @@ class EmbedArgs(ctypes.Structure):
                 ("dout", P), ("grad", P), ("workspace", P), ("workspace_bytes", SZ)]
 
 
+class XentArgs(ctypes.Structure):
+    _fields_ = [("T", I64), ("V", I32), ("d", I32), ("dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("ignore_index", I32), ("x", P), ("W", P),
+                ("targets", P), ("loss", P), ("lse", P), ("dloss", P), ("dx", P), ("dW", P),
+                ("workspace", P), ("workspace_bytes", SZ)]
+
+
+class MemplusBwd8Args(ctypes.Structure):
+    _fields_ = [("T", I64), ("d_model", I32), ("d_v", I32), ("fmt", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("x8", P), ("x_scales", P), ("W1", P), ("W2", P),
+                ("y8", P), ("y_scales", P), ("dout", P), ("dy", P), ("dx", P), ("dW1", P),
+                ("dW2", P), ("workspace", P), ("workspace_bytes", SZ)]
+
+
 EXPORTS = ("pkm_forward_workspace_size", "pkm_forward", "pkm_backward_workspace_size",
            "pkm_backward", "embbag_forward", "embbag_backward_workspace_size",
            "embbag_backward", "pkm_get_device_error", "pkm_status_string", "pkm_version",
@@ -104,7 +118,10 @@ EXPORTS = ("pkm_forward_workspace_size", "pkm_forward", "pkm_backward_workspace_
            "pkm_select", "embbag_forward_range", "pkm_check_wait_timeout", "pkm_act8_store",
            "pkm_act8_load", "pkm_add_rmsnorm_forward", "pkm_add_rmsnorm_backward_workspace_size",
            "pkm_add_rmsnorm_backward", "pkm_embed_workspace_size", "pkm_embed_forward",
-           "pkm_embed_backward")
+           "pkm_embed_backward", "pkm_linear_xent_forward_workspace_size",
+           "pkm_linear_xent_backward_workspace_size", "pkm_linear_xent_forward",
+           "pkm_linear_xent_backward", "pkm_memplus_backward_act8_workspace_size",
+           "pkm_memplus_backward_act8")
 
 _lib = None
 
@@ -170,11 +187,17 @@ def load(path: str = LIB_PATH):
                        ("pkm_add_rmsnorm_forward", [ctypes.POINTER(NormArgs), P]),
                        ("pkm_add_rmsnorm_backward", [ctypes.POINTER(NormBwdArgs), P]),
                        ("pkm_embed_forward", [ctypes.POINTER(EmbedArgs), P]),
-                       ("pkm_embed_backward", [ctypes.POINTER(EmbedArgs), P])):
+                       ("pkm_embed_backward", [ctypes.POINTER(EmbedArgs), P]),
+                       ("pkm_linear_xent_forward", [ctypes.POINTER(XentArgs), P]),
+                       ("pkm_linear_xent_backward", [ctypes.POINTER(XentArgs), P]),
+                       ("pkm_memplus_backward_act8", [ctypes.POINTER(MemplusBwd8Args), P])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = CI
     for name, arg in (("pkm_add_rmsnorm_backward_workspace_size", NormBwdArgs),
-                      ("pkm_embed_workspace_size", EmbedArgs)):
+                      ("pkm_embed_workspace_size", EmbedArgs),
+                      ("pkm_linear_xent_forward_workspace_size", XentArgs),
+                      ("pkm_linear_xent_backward_workspace_size", XentArgs),
+                      ("pkm_memplus_backward_act8_workspace_size", MemplusBwd8Args)):
         getattr(lib, name).argtypes = [ctypes.POINTER(arg)]
         getattr(lib, name).restype = SZ
     if path == LIB_PATH:

@@ -1,0 +1,286 @@
+// k_memplus8.cu -- the Memory+ backward from activations kept in 8 bits
+// ("Memory Layers at Scale" digest, "Memory+ 블록": out = (y ⊙ silu(x W1)) W2).
+//
+//   a = x W1, dz = dout W2^T, g = silu(a):
+//   dy = dz g, da = dz y silu'(a), z = y g, dx = da W1^T, dW1 = x^T da,
+//   dW2 = z^T dout
+//
+// x is read back to bf16 (exact: 8 significant bits) for the tensor cores; y
+// is decoded where it is used.  dz is kept in fp32; the epilogue of a's
+// product reads it and writes dy, da and z, so neither a nor an elementwise
+// pass touches HBM.  da and z are rounded to bf16 once, the operand type of
+// the three products that follow; those run in one launch, the weight
+// gradients (few tiles, a long contraction over the tokens) cut into slices
+// that are summed in order.
+// Bound by the tensor cores for long batches (10 T d_model d_v operations),
+// by launches for short ones.
+#include <math.h>
+
+#include "gemm_pair.cuh"
+#include "kernels.h"
+#include "q8.cuh"
+
+namespace pkm {
+
+namespace {
+
+// dz, fp32
+struct Memplus8Dz {
+  int64_t T;
+  int dv;
+  float* dz;
+
+  __device__ __forceinline__ void tile(int, int64_t m, int n0, int half, int,
+                                       uint32_t tmem) const {
+#pragma unroll 1
+    for (int q = 0; q < gp::kNh / 32; ++q) {
+      const int col = n0 + half * gp::kNh + q * 32;
+      if (col >= dv) break;
+      uint32_t r[32];
+      __syncwarp();  // the load is warp-aligned
+      tmem_ld_32x32b_x32(tmem + q * 32, r);
+      tmem_ld_wait();
+      if (m < T) store_cols_f32(dz + m * dv, col, dv, r, false);
+    }
+  }
+};
+
+// a in TMEM, dz and y from memory -> dy, da, z
+struct Memplus8Gate {
+  int64_t T;
+  int dv;
+  pkm_q8 fmt;
+  const float* dz;
+  const uint8_t* y8;
+  const float* y_scales;
+  __nv_bfloat16 *dy, *da, *z;
+
+  __device__ __forceinline__ void tile(int, int64_t m, int n0, int half, int,
+                                       uint32_t tmem) const {
+    const int c0 = n0 + half * gp::kNh;  // one quantisation group
+    const float s =
+        m < T && c0 < dv ? y_scales[m * q8_groups(dv) + c0 / kQ8Group] : 0.f;
+#pragma unroll 1
+    for (int q = 0; q < gp::kNh / 16; ++q) {
+      const int col = c0 + q * 16;
+      if (col >= dv) break;
+      uint32_t r[16];
+      __syncwarp();  // the load is warp-aligned
+      tmem_ld_32x32b_x16(tmem + q * 16, r);
+      tmem_ld_wait();
+      if (m >= T) continue;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c = col + 8 * u;
+        if (c >= dv) break;
+        const int64_t at = m * dv + c;
+        float y[8], d[8], o[3][8];
+        q8_decode(*reinterpret_cast<const uint2*>(y8 + at), s, fmt, y);
+        load8<PKM_F32>(dz + at, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = __uint_as_float(r[8 * u + e]);
+          const float sg = 1.0f / (1.0f + __expf(-a));
+          const float g = a * sg;
+          o[0][e] = d[e] * g;
+          o[1][e] = d[e] * y[e] * (sg + g * (1.0f - sg));
+          o[2][e] = y[e] * g;
+        }
+        store8<PKM_BF16>(dy + at, o[0]);
+        store8<PKM_BF16>(da + at, o[1]);
+        store8<PKM_BF16>(z + at, o[2]);
+      }
+    }
+  }
+};
+
+// Problems 0 and 1: slices of dW1 and dW2 (fp32, or the output itself when
+// there is one slice and it is fp32).  Problem 2: dx.
+struct Memplus8Grads {
+  int64_t T;
+  int dm, dv;
+  float *w1, *w2;
+  void* dx;
+  int dx_bf16;
+
+  __device__ __forceinline__ void tile(int prob, int64_t m, int n0, int half, int z,
+                                       uint32_t tmem) const {
+    const int64_t rows = prob == 0 ? dm : prob == 1 ? dv : T;
+    const int cols = prob == 0 ? dv : dm;
+#pragma unroll 1
+    for (int q = 0; q < gp::kNh / 32; ++q) {
+      const int col = n0 + half * gp::kNh + q * 32;
+      if (col >= cols) break;
+      uint32_t r[32];
+      __syncwarp();  // the load is warp-aligned
+      tmem_ld_32x32b_x32(tmem + q * 32, r);
+      tmem_ld_wait();
+      if (m >= rows) continue;
+      if (prob == 2 && dx_bf16) {
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
+        store_cols_bf16(static_cast<__nv_bfloat16*>(dx) + m * dm, col, dm, f);
+      } else {
+        float* out = prob == 2 ? static_cast<float*>(dx)
+                               : (prob == 0 ? w1 : w2) + (int64_t)z * dm * dv;
+        store_cols_f32(out + m * cols, col, cols, r, false);
+      }
+    }
+  }
+};
+
+bool need16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t rup(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Mp8Layout {
+  size_t xb, dz, da, z, w1, w2, total;
+  int nz;
+};
+
+// Slices of the weight gradients: their tiles should give most pairs of SMs
+// one item that is not much longer than the pair's share of all products, and
+// a slice has at least 4 k-blocks.
+int weight_slices(int64_t T, int dm, int dv) {
+  const int64_t kbT = (T + gp::kKB - 1) / gp::kKB;
+  const int64_t tw = (int64_t)((dm + 255) / 256) * ((dv + 255) / 256);
+  const int64_t share = (2 * tw * kbT + (T + 255) / 256 * ((dm + 255) / 256) *
+                                            ((dv + gp::kKB - 1) / gp::kKB)) / 74 + 1;
+  int64_t nz = (kbT + share - 1) / share;
+  if (nz > kbT / 4) nz = kbT / 4;
+  if (nz < 1) nz = 1;
+  return pair_prob(dm, dv, (int)T, true, true, (int)(nz > 64 ? 64 : nz)).nz;
+}
+
+Mp8Layout mp8_layout(const pkm_memplus_bwd8_args* g) {
+  Mp8Layout L{};
+  const size_t T = (size_t)g->T, dm = (size_t)g->d_model, dv = (size_t)g->d_v;
+  size_t off = 0;
+  auto take = [&](size_t b) {
+    const size_t o = off;
+    off += rup(b);
+    return o;
+  };
+  L.nz = weight_slices(g->T, g->d_model, g->d_v);
+  L.xb = take(T * dm * 2);
+  L.dz = take(T * dv * 4);
+  L.da = take(T * dv * 2);
+  L.z = take(T * dv * 2);
+  const bool direct = L.nz == 1 && g->grad_dtype == PKM_F32;
+  L.w1 = direct ? 0 : take((size_t)L.nz * dm * dv * 4);
+  L.w2 = direct ? 0 : take((size_t)L.nz * dm * dv * 4);
+  L.total = off;
+  return L;
+}
+
+pkm_status mp8_sizes(const pkm_memplus_bwd8_args* g) {
+  if (!g || g->T < 0 || g->d_model < 8 || g->d_model % 8 || g->d_v < 8 || g->d_v % 8 ||
+      (g->fmt != PKM_Q8_E4M3 && g->fmt != PKM_Q8_INT8) ||
+      (g->grad_dtype != PKM_F32 && g->grad_dtype != PKM_BF16))
+    return PKM_ERR_INVALID_ARG;
+  // tile counts and the 8-bit load's grid stay in 31 bits
+  if (g->T > (int64_t(1) << 28) || g->d_model > 65536 || g->d_v > 65536 ||
+      g->T * q8_groups(g->d_model) >= (int64_t(1) << 34))
+    return PKM_ERR_UNSUPPORTED;
+  return PKM_OK;
+}
+
+pkm_status mp8_validate(const pkm_memplus_bwd8_args* g) {
+  const pkm_status s = mp8_sizes(g);
+  if (s != PKM_OK) return s;
+  if (!need16(g->dW1) || !need16(g->dW2)) return PKM_ERR_INVALID_ARG;
+  if (g->T == 0) return PKM_OK;
+  const void* need[] = {g->x8, g->x_scales, g->W1, g->W2, g->y8, g->y_scales, g->dout, g->dy, g->dx};
+  for (const void* p : need)
+    if (!need16(p)) return PKM_ERR_INVALID_ARG;
+  if (!need16(g->workspace) || g->workspace_bytes < mp8_layout(g).total)
+    return PKM_ERR_WORKSPACE;
+  return PKM_OK;
+}
+
+#define PKM_TRY(expr)                 \
+  do {                                \
+    const cudaError_t e_ = (expr);    \
+    if (e_ != cudaSuccess) return e_; \
+    note_launch();                    \
+  } while (0)
+
+cudaError_t memplus8_backward(const pkm_memplus_bwd8_args* g, int32_t* status, cudaStream_t st) {
+  const Mp8Layout L = mp8_layout(g);
+  char* ws = static_cast<char*>(g->workspace);
+  const int64_t T = g->T;
+  const int dm = g->d_model, dv = g->d_v;
+  auto* xb = reinterpret_cast<__nv_bfloat16*>(ws + L.xb);
+  auto* dz = reinterpret_cast<float*>(ws + L.dz);
+  auto* da = reinterpret_cast<__nv_bfloat16*>(ws + L.da);
+  auto* z = reinterpret_cast<__nv_bfloat16*>(ws + L.z);
+  cudaError_t e = launch_act8_load(g->x8, g->x_scales, T, dm, g->fmt, xb, PKM_BF16, st);
+  if (e != cudaSuccess) return e;
+  {  // dz = dout W2^T
+    PairMaps<1> m;
+    if (!pair_map(&m.a[0], g->dout, T, dm, dm, false) ||
+        !pair_map(&m.b[0], g->W2, dv, dm, dm, false))
+      return cudaErrorInvalidValue;
+    const PairProbs<1> p{{pair_prob(T, dv, dm, false, false)}, 1, {}};
+    PKM_TRY((launch_pair_gemm<1>(m, p, Memplus8Dz{T, dv, dz}, status, st)));
+  }
+  {  // a = x W1 and everything elementwise
+    PairMaps<1> m;
+    if (!pair_map(&m.a[0], xb, T, dm, dm, false) || !pair_map(&m.b[0], g->W1, dv, dm, dv, true))
+      return cudaErrorInvalidValue;
+    const PairProbs<1> p{{pair_prob(T, dv, dm, false, true)}, 1, {}};
+    const Memplus8Gate epi{T,  dv, g->fmt, dz, static_cast<const uint8_t*>(g->y8),
+                           g->y_scales, static_cast<__nv_bfloat16*>(g->dy), da, z};
+    PKM_TRY((launch_pair_gemm<1>(m, p, epi, status, st)));
+  }
+  const bool gb = g->grad_dtype == PKM_BF16;
+  const bool direct = L.nz == 1 && !gb;
+  float* w1 = direct ? static_cast<float*>(g->dW1) : reinterpret_cast<float*>(ws + L.w1);
+  float* w2 = direct ? static_cast<float*>(g->dW2) : reinterpret_cast<float*>(ws + L.w2);
+  {  // dW1 = x^T da, dW2 = z^T dout, dx = da W1^T
+    PairMaps<3> m;
+    if (!pair_map(&m.a[0], xb, dm, (int)T, dm, true) || !pair_map(&m.b[0], da, dv, (int)T, dv, true) ||
+        !pair_map(&m.a[1], z, dv, (int)T, dv, true) ||
+        !pair_map(&m.b[1], g->dout, dm, (int)T, dm, true) ||
+        !pair_map(&m.a[2], da, T, dv, dv, false) || !pair_map(&m.b[2], g->W1, dm, dv, dv, false))
+      return cudaErrorInvalidValue;
+    const PairProbs<3> p{{pair_prob(dm, dv, (int)T, true, true, L.nz),
+                          pair_prob(dv, dm, (int)T, true, true, L.nz),
+                          pair_prob(T, dm, dv, false, false)}, 2, {}};
+    PKM_TRY((launch_pair_gemm<3>(m, p, Memplus8Grads{T, dm, dv, w1, w2, g->dx, gb}, status, st)));
+  }
+  if (direct) return cudaSuccess;
+  PKM_TRY(launch_slice_sum(w1, L.nz, (int64_t)dm * dv, g->dW1, g->grad_dtype, st));
+  PKM_TRY(launch_slice_sum(w2, L.nz, (int64_t)dm * dv, g->dW2, g->grad_dtype, st));
+  return cudaSuccess;
+}
+
+}  // namespace
+}  // namespace pkm
+
+using namespace pkm;
+
+extern "C" {
+
+PKM_API size_t pkm_memplus_backward_act8_workspace_size(const pkm_memplus_bwd8_args* g) {
+  return mp8_sizes(g) == PKM_OK ? mp8_layout(g).total : 0;
+}
+
+PKM_API pkm_status pkm_memplus_backward_act8(const pkm_memplus_bwd8_args* g,
+                                             pkm_stream_t stream) {
+  const pkm_status s = mp8_validate(g);
+  if (s != PKM_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (g->T == 0) {
+    const size_t b = (size_t)g->d_model * g->d_v * (g->grad_dtype == PKM_F32 ? 4 : 2);
+    return cudaMemsetAsync(g->dW1, 0, b, st) == cudaSuccess &&
+                   cudaMemsetAsync(g->dW2, 0, b, st) == cudaSuccess
+               ? PKM_OK
+               : PKM_ERR_CUDA;
+  }
+  int32_t* status = status_ptr();
+  if (!status) return PKM_ERR_CUDA;
+  return memplus8_backward(g, status, st) == cudaSuccess ? PKM_OK : PKM_ERR_CUDA;
+}
+
+}  // extern "C"

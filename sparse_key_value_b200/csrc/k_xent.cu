@@ -1,0 +1,374 @@
+// k_xent.cu -- softmax cross entropy of an output layer over a large
+// vocabulary, without keeping the logits, and its gradients.
+//
+//   logit[t, v] = <x[t], W[v]>,  lse[t] = log sum_v exp(logit[t, v]),
+//   loss[t] = lse[t] - logit[t, target[t]]          (0 where there is none)
+//   d[t, v] = (exp(logit[t, v] - lse[t]) - [v = target[t]]) dloss[t]
+//   dx = d W,  dW = d^T x
+//
+// Forward: the logits live in TMEM only.  Each 256 x 256 tile's epilogue
+// reduces its columns to a running maximum and sum per row (two column halves
+// of 128), a small kernel joins the partials.  Base 2 throughout: with
+// s = logit log2(e), a term is 2^(s - max) -- one multiply-add and one ex2 --
+// and the rounding of log2(e) scales every term alike (1.3e-8 of the logit).
+// Backward: d for a piece of the vocabulary (recomputed logits, rounded to
+// bf16 once: the operand type of the products that read it, half a step of
+// each d), then both products in one launch; dx is summed over the pieces in
+// fp32, in piece order.
+// Bound by the tensor cores: 2 T V d operations forward, 6 T V d backward.
+#include <math.h>
+
+#include "gemm_pair.cuh"
+#include "kernels.h"
+
+namespace pkm {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Row maximum and sum of a tile's column half -> part[slot][row], and the
+// target's logit.
+struct XentStats {
+  int64_t T;
+  int V;
+  const int32_t* target;
+  float2* part;  // [2 * tiles_n][T]: maximum (base 2) and sum
+  float* picked;
+
+  __device__ __forceinline__ void tile(int, int64_t m, int n0, int half, int,
+                                       uint32_t tmem) const {
+    const bool live = m < T;
+    const int t = live ? target[m] : -1;
+    float mx = -INFINITY, sum = 0.f;
+    const int c0 = n0 + half * gp::kNh;
+#pragma unroll 1
+    for (int g = 0; g < gp::kNh / 32; ++g) {
+      const int col = c0 + g * 32;
+      if (col >= V) break;
+      uint32_t r[32];
+      __syncwarp();  // the load is warp-aligned
+      tmem_ld_32x32b_x32(tmem + g * 32, r);
+      tmem_ld_wait();
+      if (col + 32 > V) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (col + j >= V) r[j] = 0xff800000u;  // -inf: no such column
+      }
+      float top = __uint_as_float(r[0]);
+#pragma unroll
+      for (int j = 1; j < 32; ++j) top = fmaxf(top, __uint_as_float(r[j]));
+      const float nm = fmaxf(mx, top * kLog2e);
+      const float ref = nm == -INFINITY ? 0.f : nm;  // all -inf so far: every term is 0
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
+      sum = fmaf(sum, ex2(mx - ref), (s[0] + s[1]) + (s[2] + s[3]));
+      mx = nm;
+      const uint32_t at = (uint32_t)t - (uint32_t)col;
+      if (at < 32u) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (at == j) picked[m] = __uint_as_float(r[j]);
+      }
+    }
+    if (live) part[(int64_t)(c0 / gp::kNh) * T + m] = make_float2(mx, sum);
+  }
+};
+
+// lse and loss from the partials: 32 rows per block, 16 strips of partials
+constexpr int kJoinStrips = 16;
+
+__global__ void __launch_bounds__(32 * kJoinStrips) xent_join_kernel(
+    const float2* __restrict__ part, int slots, int64_t T, int V,
+    const int32_t* __restrict__ target, int32_t ignore, const float* __restrict__ picked,
+    float* __restrict__ loss, float* __restrict__ lse, int32_t* status) {
+  __shared__ float2 sm[kJoinStrips][32];
+  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
+  const int64_t m = (int64_t)blockIdx.x * 32 + lane;
+  float mx = -INFINITY, sum = 0.f;
+  auto join = [&](float2 q) {
+    const float nm = fmaxf(mx, q.x);
+    const float ref = nm == -INFINITY ? 0.f : nm;
+    sum = sum * ex2(mx - ref) + q.y * ex2(q.x - ref);
+    mx = nm;
+  };
+  if (m < T) {
+#pragma unroll 4
+    for (int s = strip; s < slots; s += kJoinStrips) join(part[(int64_t)s * T + m]);
+  }
+  sm[strip][lane] = make_float2(mx, sum);
+  __syncthreads();
+  if (strip != 0 || m >= T) return;
+  for (int s = 1; s < kJoinStrips; ++s) join(sm[s][lane]);
+  const float l = (mx + log2f(sum)) * kLn2;
+  lse[m] = l;
+  const int32_t t = target[m];
+  const bool counted = t != ignore && t >= 0 && t < V;
+  if (!counted && t != ignore) set_status(status, PKM_ERR_DEVICE);
+  loss[m] = counted ? l - picked[m] : 0.f;
+}
+
+// d of one vocabulary piece, bf16
+struct XentDelta {
+  int64_t T;
+  int Vp, v0, V;  // piece columns, first column, vocabulary
+  const int32_t* target;
+  int32_t ignore;
+  const float *lse, *dloss;
+  __nv_bfloat16* out;  // [T][ld]
+  int64_t ld;
+
+  __device__ __forceinline__ void tile(int, int64_t m, int n0, int half, int,
+                                       uint32_t tmem) const {
+    const bool live = m < T;
+    const int t = live ? target[m] : ignore;
+    const bool counted = t != ignore && t >= 0 && t < V;
+    const float g = counted ? dloss[m] : 0.f;
+    const float l2 = counted ? lse[m] * kLog2e : 0.f;
+    const int c0 = n0 + half * gp::kNh;
+#pragma unroll 1
+    for (int q = 0; q < gp::kNh / 32; ++q) {
+      const int col = c0 + q * 32;
+      if (col >= Vp) break;
+      uint32_t r[32];
+      __syncwarp();  // the load is warp-aligned
+      tmem_ld_32x32b_x32(tmem + q * 32, r);
+      tmem_ld_wait();
+      if (!live) continue;
+      float p[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) p[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -l2));
+      const uint32_t at = (uint32_t)t - (uint32_t)(v0 + col);
+      if (at < 32u) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (at == j) p[j] -= 1.f;
+      }
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        w[j] = counted ? pack_bf16x2(p[2 * j] * g, p[2 * j + 1] * g) : 0u;
+      __nv_bfloat16* dst = out + m * ld + col;  // ld covers whole groups of 32 columns
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        reinterpret_cast<uint4*>(dst)[j] =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    }
+  }
+};
+
+// Problem 0: dx partials, fp32 (overwritten or added to), one [T, d] slice per
+// z.  Problem 1: rows of dW.
+struct XentGrads {
+  int64_t T;
+  int Vp, d;
+  float* dx;
+  int add;
+  void* dW;  // at the piece's first row
+  int dw_bf16;
+
+  __device__ __forceinline__ void tile(int prob, int64_t m, int n0, int half, int z,
+                                       uint32_t tmem) const {
+    const int c0 = n0 + half * gp::kNh;
+    const bool live = m < (prob ? (int64_t)Vp : T);
+#pragma unroll 1
+    for (int q = 0; q < gp::kNh / 32; ++q) {
+      const int col = c0 + q * 32;
+      if (col >= d) break;
+      uint32_t r[32];
+      __syncwarp();  // the load is warp-aligned
+      tmem_ld_32x32b_x32(tmem + q * 32, r);
+      tmem_ld_wait();
+      if (!live) continue;
+      if (prob && dw_bf16) {
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
+        store_cols_bf16(static_cast<__nv_bfloat16*>(dW) + m * d, col, d, f);
+      } else {
+        store_cols_f32((prob ? static_cast<float*>(dW) : dx + (int64_t)z * T * d) + m * d, col, d,
+                       r, !prob && add);
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------ host side
+
+bool need16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t rup(size_t x) { return (x + 255) / 256 * 256; }
+
+constexpr int64_t kPieceBytes = int64_t(256) << 20;  // most that a piece's d may take
+constexpr int kMinPiece = 1024;
+
+struct XentLayout {
+  size_t part, picked, fwd_total;  // forward
+  int piece, ld, nz;
+  size_t delta, dx, bwd_total;     // backward
+};
+
+int fwd_slots(int V) { return 2 * ((V + gp::kN - 1) / gp::kN); }
+
+XentLayout xent_layout(const pkm_xent_args* a) {
+  XentLayout L{};
+  const size_t T = (size_t)a->T;
+  L.part = 0;
+  L.picked = rup((size_t)fwd_slots(a->V) * T * sizeof(float2));
+  L.fwd_total = L.picked + rup(T * 4);
+  // columns of a piece: as many as kPieceBytes holds, whole tiles
+  int64_t piece = kPieceBytes / 2 / (a->T > 0 ? a->T : 1) / gp::kN * gp::kN;
+  if (piece < kMinPiece) piece = kMinPiece;
+  if (piece > a->V) piece = a->V;
+  L.piece = (int)piece;
+  L.ld = (int)((piece + 63) / 64 * 64);
+  // few tiles of dx: slices of the piece, so that every pair of SMs has some
+  const int64_t tiles = (a->T + 255) / 256 * ((a->d + 255) / 256);
+  int64_t nz = 74 / (tiles > 0 ? tiles : 1);
+  const int64_t most = (piece + 511) / 512;
+  if (nz > most) nz = most;
+  if (nz > 16) nz = 16;
+  L.nz = pair_prob(a->T, a->d, L.piece, false, true, nz < 1 ? 1 : (int)nz).nz;
+  L.delta = 0;
+  L.dx = rup(T * (size_t)L.ld * 2);
+  const bool direct = L.nz == 1 && a->grad_dtype == PKM_F32;
+  L.bwd_total = L.dx + (direct ? 0 : rup((size_t)L.nz * T * (size_t)a->d * 4));
+  return L;
+}
+
+pkm_status xent_sizes(const pkm_xent_args* a) {
+  if (!a || a->T < 0 || a->V < 1 || a->d < 8 || a->d % 8) return PKM_ERR_INVALID_ARG;
+  if (a->dtype != PKM_BF16)
+    return a->dtype == PKM_F32 ? PKM_ERR_UNSUPPORTED : PKM_ERR_INVALID_ARG;
+  if (a->grad_dtype != PKM_F32 && a->grad_dtype != PKM_BF16) return PKM_ERR_INVALID_ARG;
+  // tile counts and tensor-map coordinates stay in 31 bits
+  if (a->T > (int64_t(1) << 30) || a->d > 65536 ||
+      ((a->T + 255) / 256) * (((int64_t)a->V + 255) / 256) >= (int64_t(1) << 30))
+    return PKM_ERR_UNSUPPORTED;
+  return PKM_OK;
+}
+
+pkm_status xent_validate(const pkm_xent_args* a, bool backward) {
+  const pkm_status s = xent_sizes(a);
+  if (s != PKM_OK) return s;
+  if (backward && !need16(a->dW)) return PKM_ERR_INVALID_ARG;
+  if (a->T == 0) return PKM_OK;
+  if (!need16(a->x) || !need16(a->W) || !need16(a->targets) || !need16(a->lse))
+    return PKM_ERR_INVALID_ARG;
+  if (!backward && !need16(a->loss)) return PKM_ERR_INVALID_ARG;
+  if (backward && (!need16(a->dloss) || !need16(a->dx))) return PKM_ERR_INVALID_ARG;
+  const XentLayout L = xent_layout(a);
+  if (!need16(a->workspace) || a->workspace_bytes < (backward ? L.bwd_total : L.fwd_total))
+    return PKM_ERR_WORKSPACE;
+  return PKM_OK;
+}
+
+#define PKM_TRY(expr)                         \
+  do {                                        \
+    const cudaError_t e_ = (expr);            \
+    if (e_ != cudaSuccess) return e_;         \
+    note_launch();                            \
+  } while (0)
+
+cudaError_t xent_forward(const pkm_xent_args* a, int32_t* status, cudaStream_t st) {
+  const XentLayout L = xent_layout(a);
+  char* ws = static_cast<char*>(a->workspace);
+  auto* part = reinterpret_cast<float2*>(ws + L.part);
+  auto* picked = reinterpret_cast<float*>(ws + L.picked);
+  PairMaps<1> maps;
+  if (!pair_map(&maps.a[0], a->x, a->T, a->d, a->d, false) ||
+      !pair_map(&maps.b[0], a->W, a->V, a->d, a->d, false))
+    return cudaErrorInvalidValue;
+  const PairProbs<1> p{{pair_prob(a->T, a->V, a->d, false, false, 1, 8)}, 1, {}};
+  const XentStats epi{a->T, a->V, a->targets, part, picked};
+  PKM_TRY((launch_pair_gemm<1>(maps, p, epi, status, st)));
+  xent_join_kernel<<<(unsigned)((a->T + 31) / 32), 32 * kJoinStrips, 0, st>>>(
+      part, fwd_slots(a->V), a->T, a->V, a->targets, a->ignore_index, picked, a->loss, a->lse,
+      status);
+  PKM_TRY(cudaGetLastError());
+  return cudaSuccess;
+}
+
+cudaError_t xent_backward(const pkm_xent_args* a, int32_t* status, cudaStream_t st) {
+  const XentLayout L = xent_layout(a);
+  char* ws = static_cast<char*>(a->workspace);
+  auto* delta = reinterpret_cast<__nv_bfloat16*>(ws + L.delta);
+  const bool direct = L.nz == 1 && a->grad_dtype == PKM_F32;
+  float* dx = direct ? static_cast<float*>(a->dx) : reinterpret_cast<float*>(ws + L.dx);
+  const bool gb = a->grad_dtype == PKM_BF16;
+  for (int v0 = 0; v0 < a->V; v0 += L.piece) {
+    const int Vp = a->V - v0 < L.piece ? a->V - v0 : L.piece;
+    const char* Wp = static_cast<const char*>(a->W) + (size_t)v0 * a->d * 2;
+    PairMaps<1> m1;
+    if (!pair_map(&m1.a[0], a->x, a->T, a->d, a->d, false) ||
+        !pair_map(&m1.b[0], Wp, Vp, a->d, a->d, false))
+      return cudaErrorInvalidValue;
+    const PairProbs<1> p{{pair_prob(a->T, Vp, a->d, false, false, 1, 8)}, 1, {}};
+    const XentDelta de{a->T,  Vp,    v0,    a->V, a->targets, a->ignore_index, a->lse, a->dloss,
+                       delta, L.ld};
+    PKM_TRY((launch_pair_gemm<1>(m1, p, de, status, st)));
+    PairMaps<2> m2;
+    if (!pair_map(&m2.a[0], delta, a->T, Vp, L.ld, false) ||
+        !pair_map(&m2.b[0], Wp, a->d, Vp, a->d, true) ||
+        !pair_map(&m2.a[1], delta, Vp, (int)a->T, L.ld, true) ||
+        !pair_map(&m2.b[1], a->x, a->d, (int)a->T, a->d, true))
+      return cudaErrorInvalidValue;
+    // a shorter last piece may fill fewer slices: the others keep their sums
+    const PairProbs<2> q{{pair_prob(a->T, a->d, Vp, false, true, L.nz),
+                          pair_prob(Vp, a->d, (int)a->T, true, true)}, 1, {}};
+    const XentGrads ge{a->T, Vp, a->d, dx, v0 > 0,
+                       static_cast<char*>(a->dW) + (size_t)v0 * a->d * (gb ? 2 : 4), gb};
+    PKM_TRY((launch_pair_gemm<2>(m2, q, ge, status, st)));
+  }
+  if (direct) return cudaSuccess;
+  PKM_TRY(launch_slice_sum(dx, L.nz, a->T * a->d, a->dx, a->grad_dtype, st));
+  return cudaSuccess;
+}
+
+}  // namespace
+}  // namespace pkm
+
+using namespace pkm;
+
+extern "C" {
+
+PKM_API size_t pkm_linear_xent_forward_workspace_size(const pkm_xent_args* a) {
+  return xent_sizes(a) == PKM_OK ? xent_layout(a).fwd_total : 0;
+}
+
+PKM_API size_t pkm_linear_xent_backward_workspace_size(const pkm_xent_args* a) {
+  return xent_sizes(a) == PKM_OK ? xent_layout(a).bwd_total : 0;
+}
+
+PKM_API pkm_status pkm_linear_xent_forward(const pkm_xent_args* a, pkm_stream_t stream) {
+  const pkm_status s = xent_validate(a, false);
+  if (s != PKM_OK || a->T == 0) return s;
+  int32_t* status = status_ptr();
+  if (!status) return PKM_ERR_CUDA;
+  return xent_forward(a, status, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKM_OK
+             : PKM_ERR_CUDA;
+}
+
+PKM_API pkm_status pkm_linear_xent_backward(const pkm_xent_args* a, pkm_stream_t stream) {
+  const pkm_status s = xent_validate(a, true);
+  if (s != PKM_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (a->T == 0)
+    return cudaMemsetAsync(a->dW, 0, (size_t)a->V * a->d * (a->grad_dtype == PKM_F32 ? 4 : 2),
+                           st) == cudaSuccess
+               ? PKM_OK
+               : PKM_ERR_CUDA;
+  int32_t* status = status_ptr();
+  if (!status) return PKM_ERR_CUDA;
+  return xent_backward(a, status, st) == cudaSuccess ? PKM_OK : PKM_ERR_CUDA;
+}
+
+}  // extern "C"

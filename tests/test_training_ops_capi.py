@@ -115,3 +115,69 @@ def test_binding_refuses_bad_tensors():
                  lambda: skv.embedding_backward(x, ids, 4)):
         with pytest.raises(ValueError):
             call()
+
+
+def _xent(**kw):
+    from sparse_key_value_b200 import _lib
+    base = dict(T=4, V=10, d=64, dtype=1, grad_dtype=0, ignore_index=-100, x=F, W=F, targets=F,
+                loss=F, lse=F, dloss=F, dx=F, dW=F, workspace=F, workspace_bytes=1 << 40)
+    return _lib.XentArgs(**{**base, **kw})
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(T=-1), 1), (dict(V=0), 1), (dict(d=4), 1), (dict(d=60), 1), (dict(dtype=3), 1),
+    (dict(dtype=0), 2), (dict(grad_dtype=2), 1), (dict(x=None), 1), (dict(x=ODD), 1),
+    (dict(W=ODD), 1), (dict(targets=None), 1), (dict(lse=ODD), 1), (dict(d=65544), 2),
+    (dict(T=2 ** 30 + 1), 2), (dict(T=2 ** 28, V=2 ** 20), 2), (dict(workspace=None), 6)])
+def test_xent_refuses(lib, bad, code):
+    assert lib.pkm_linear_xent_forward(ctypes.byref(_xent(**bad)), None) == code
+    assert lib.pkm_linear_xent_backward(ctypes.byref(_xent(**bad)), None) == code
+
+
+def test_xent_refuses_by_direction(lib):
+    fwd = lambda **k: lib.pkm_linear_xent_forward(ctypes.byref(_xent(**k)), None)   # noqa: E731
+    bwd = lambda **k: lib.pkm_linear_xent_backward(ctypes.byref(_xent(**k)), None)  # noqa: E731
+    assert fwd(loss=None) == 1 and bwd(dloss=None) == 1 and bwd(dx=ODD) == 1 and bwd(dW=None) == 1
+    assert bwd(T=0, dW=None) == 1
+    for call, size in ((fwd, lib.pkm_linear_xent_forward_workspace_size),
+                       (bwd, lib.pkm_linear_xent_backward_workspace_size)):
+        need = size(ctypes.byref(_xent()))
+        assert need > 0 and call(workspace_bytes=need - 1) == 6
+        assert size(None) == 0 and size(ctypes.byref(_xent(d=60))) == 0
+    assert fwd(T=0, x=None) == 0
+    # the piece of d stays within 256 MiB (or 1024 columns) however large the vocabulary
+    big = _xent(T=16384, V=262144, d=1024)
+    need = lib.pkm_linear_xent_backward_workspace_size(ctypes.byref(big))
+    assert need <= (256 << 20) + 16384 * 1024 * 4 + 1024
+
+
+def _mp8(**kw):
+    from sparse_key_value_b200 import _lib
+    base = dict(T=4, d_model=64, d_v=32, fmt=2, grad_dtype=0, x8=F, x_scales=F, W1=F, W2=F, y8=F,
+                y_scales=F, dout=F, dy=F, dx=F, dW1=F, dW2=F, workspace=F,
+                workspace_bytes=1 << 40)
+    return _lib.MemplusBwd8Args(**{**base, **kw})
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(T=-1), 1), (dict(d_model=60), 1), (dict(d_v=0), 1), (dict(fmt=0), 1), (dict(fmt=3), 1),
+    (dict(grad_dtype=2), 1), (dict(x8=None), 1), (dict(x_scales=ODD), 1), (dict(W1=ODD), 1),
+    (dict(W2=None), 1), (dict(y8=ODD), 1), (dict(y_scales=None), 1), (dict(dout=None), 1),
+    (dict(dy=ODD), 1), (dict(dx=None), 1), (dict(dW1=ODD), 1), (dict(dW2=None), 1),
+    (dict(T=2 ** 28 + 1), 2), (dict(d_v=65544), 2), (dict(T=2 ** 28, d_model=65536), 2),
+    (dict(workspace=None), 6)])
+def test_memplus_act8_refuses(lib, bad, code):
+    assert lib.pkm_memplus_backward_act8(ctypes.byref(_mp8(**bad)), None) == code
+
+
+def test_memplus_act8_workspace(lib):
+    need = lib.pkm_memplus_backward_act8_workspace_size(ctypes.byref(_mp8()))
+    assert need > 0
+    a = _mp8(workspace_bytes=need - 1)
+    assert lib.pkm_memplus_backward_act8(ctypes.byref(a), None) == 6
+    assert lib.pkm_memplus_backward_act8_workspace_size(None) == 0
+    for T in (0, 1, 2 ** 28):  # any batch has a size, the empty one too
+        lib.pkm_memplus_backward_act8_workspace_size(ctypes.byref(_mp8(T=T)))
+        lib.pkm_linear_xent_backward_workspace_size(ctypes.byref(_xent(T=T)))
+        lib.pkm_linear_xent_forward_workspace_size(ctypes.byref(_xent(T=T)))
+    assert lib.pkm_memplus_backward_act8(ctypes.byref(_mp8(T=0, dW1=None)), None) == 1
