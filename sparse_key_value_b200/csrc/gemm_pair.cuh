@@ -4,7 +4,7 @@
 //   acc[M, N] = A[M, K] B[N, K]^T, fp32 accumulation, 256 x 256 tiles per pair
 //
 // through tcgen05.mma.cta_group::2: each CTA of a cluster of two loads its own
-// 128 rows of A and its own half of B (a ring of 6 stages of 32 KiB), one
+// 128 rows of A and its own half of B (a ring of up to 6 stages of 32 KiB), one
 // instruction multiplies both, each CTA's epilogue reads its 128 rows from
 // TMEM while the next tile's products fill the other accumulator.  A or B may
 // be held K-major ([M][K]) or MN-major ([K][M]); one launch takes up to three
@@ -28,12 +28,17 @@
 namespace pkm {
 
 namespace gp {
-constexpr int kM = 128, kN = 256, kNh = kN / 2, kKB = 64, kStages = 6, kAcc = 2, kBox = 64;
+constexpr int kM = 128, kN = 256, kNh = kN / 2, kKB = 64, kMaxStages = 6, kAcc = 2, kBox = 64;
 constexpr int kABytes = kM * kKB * 2, kBBytes = kNh * kKB * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 256;
+// ring, staging of the epilogue warps, control words; the first kilobyte
+// aligns the ring (the swizzle goes by the address)
+template <class E>
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)E::kStages * kStageBytes + (size_t)kEpiWarps * E::kWarpBytes + 256;
+}
 }  // namespace gp
 
 struct PairProb {
@@ -114,55 +119,149 @@ __device__ __forceinline__ PairTile pair_tile(const PairProb& p, int idx) {
 }
 
 struct PairCtl {
-  uint64_t full[gp::kStages];   // leader: both CTAs' copies of a stage landed
-  uint64_t empty[gp::kStages];  // each CTA: the MMAs are done with a stage
-  uint64_t accf[gp::kAcc];      // each CTA: an accumulator is ready
-  uint64_t acce[gp::kAcc];      // leader: both epilogues drained an accumulator
+  uint64_t full[gp::kMaxStages];   // leader: both CTAs' copies of a stage landed
+  uint64_t empty[gp::kMaxStages];  // each CTA: the MMAs are done with a stage
+  uint64_t accf[gp::kAcc];         // each CTA: an accumulator is ready
+  uint64_t acce[gp::kAcc];         // leader: both epilogues drained an accumulator
+  uint64_t epi[gp::kEpiWarps];     // an epilogue warp's own copies
   uint64_t drain;
   uint32_t tmem;
   volatile int abort;
 };
 
-// 32 accumulator columns of one row -> columns col .. of a row-major output
-// with d columns (d % 8 == 0), stored or added to.
-__device__ __forceinline__ void store_cols_f32(float* row, int col, int d, const uint32_t* r,
-                                               bool add) {
-  const int n4 = min(8, (d - col) / 4);
-  float* dst = row + col;
+// ---- staging: an epilogue warp's 32 rows in shared memory, in the swizzled
+// layout of a tensor copy, so that a lane writes its own row's 16-byte pieces
+// without bank conflicts and the copy writes whole lines.  (Row-per-lane
+// stores to global memory touch 32 lines an instruction: for a 128 x 256 fp32
+// tile that alone took as long as the products of K = 1024.)
+
+// 32 fp32 columns, rows of 128 bytes
+__device__ __forceinline__ void stage_f32(unsigned char* buf, int lane, const uint32_t* r) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (j < n4) {
-      float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                             __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-      if (add) {
-        const float4 o = reinterpret_cast<const float4*>(dst)[j];
-        v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-      }
-      reinterpret_cast<float4*>(dst)[j] = v;
-    }
+    *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+        make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
 }
-__device__ __forceinline__ void store_cols_bf16(__nv_bfloat16* row, int col, int d,
-                                                const float* f) {
-  const int n8 = min(4, (d - col) / 8);
+// columns 32 h .. + 31 of 64 bf16 columns, rows of 128 bytes
+__device__ __forceinline__ void stage_bf16(unsigned char* buf, int lane, int h,
+                                           const uint32_t* w) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (j < n8) reinterpret_cast<uint4*>(row + col)[j] = pack16<PKM_BF16>(f + 8 * j);
+    *reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+// piece j (of 4) of 32 bf16 columns, rows of 64 bytes
+__device__ __forceinline__ unsigned char* stage64_at(unsigned char* buf, int lane, int j) {
+  return buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
 }
 
+__device__ __forceinline__ void tma_store_3d(const void* map, const void* smem, int c0, int c1,
+                                             int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+      ::"l"(map), "r"(smem_u32(smem)), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const void* map, const void* smem, int c0, int c1,
+                                           int c2) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];"
+      ::"l"(map), "r"(smem_u32(smem)), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// this thread's tensor stores have read their shared memory
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// The warp's staging buffer may be written again (lane 0 issues the stores).
+__device__ __forceinline__ void stage_free(int lane) {
+  if (lane == 0) bulk_wait_read();
+  __syncwarp();
+}
+// The warp's writes are visible to the copy that lane 0 issues next.
+__device__ __forceinline__ void stage_ready() {
+  fence_async_smem();
+  __syncwarp();
+}
+
+struct EpiWarp {
+  int lane, half;         // half: columns 128 half .. + 127 of the tile
+  unsigned char* stage;   // E::kWarpBytes of shared memory, 1024-byte aligned
+  uint64_t* bar;          // a barrier of the warp's own, one arrival
+  volatile int* abort;
+  int32_t* status;
+};
+
 // E: a trivially copyable epilogue with
-//   __device__ void tile(int prob, int64_t m, int n0, int half, int z, uint32_t tmem) const
-// called by a whole warp: `m` the lane's row, columns n0 + 128 half .. + 127 of
-// the problem at TMEM address `tmem` (its lane quarter and column included).
+//   kStages, kWarpBytes   ring stages; staging bytes per epilogue warp
+//   struct State          a warp's state over its tiles, zero-initialised
+//   begin(State&, w, prob, row0, n0, z)        before the accumulator is ready
+//   tile(State&, w, prob, row0, n0, z, tmem)   by a whole warp: rows row0 + lane,
+//       columns n0 + 128 half .. + 127 at TMEM address `tmem` (lane quarter
+//       and column included)
+//   abandon(State&, w)    after an abort: lets copies in flight land
+// The accumulator itself -> the problem's output map: fp32 (stored or added
+// to; slice z is the map's third coordinate) or bf16.
+struct StoreOut {
+  int64_t rows;
+  int cols;
+  int bf16, add;
+};
+
+__device__ __forceinline__ void store_tile(const StoreOut& o, const CUtensorMap* map,
+                                           const EpiWarp& w, int64_t row0, int n0, int z,
+                                           uint32_t tmem) {
+  if (row0 >= o.rows) return;  // the whole warp
+  const int c0 = n0 + w.half * gp::kNh;
+  const int step = o.bf16 ? 64 : 32;
+  for (int q = 0; q < gp::kNh; q += step) {
+    if (c0 + q >= o.cols) break;
+    stage_free(w.lane);
+#pragma unroll 1
+    for (int h = 0; h < step / 32; ++h) {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tmem + q + 32 * h, r);
+      tmem_ld_wait();
+      if (o.bf16) {
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          p[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        stage_bf16(w.stage, w.lane, h, p);
+      } else {
+        stage_f32(w.stage, w.lane, r);
+      }
+    }
+    stage_ready();
+    if (w.lane == 0) {
+      if (o.add)
+        tma_add_3d(map, w.stage, c0 + q, (int)row0, z);
+      else
+        tma_store_3d(map, w.stage, c0 + q, (int)row0, z);
+      bulk_commit();
+    }
+    __syncwarp();
+  }
+}
+
 template <int NP, class E>
 __global__ void __launch_bounds__(gp::kThreads, 1)
     pair_gemm_kernel(const __grid_constant__ PairMaps<NP> maps,
                      const __grid_constant__ PairProbs<NP> probs, const __grid_constant__ E epi,
                      int32_t* status) {
   using namespace gp;
+  constexpr int kStages = E::kStages;
+  static_assert(kStages <= kMaxStages && E::kWarpBytes % 1024 == 0, "shared memory layout");
+  static_assert(sizeof(PairCtl) <= 256 && smem_bytes<E>() <= 227 * 1024, "shared memory size");
   extern __shared__ unsigned char smem_raw[];
   unsigned char* stages = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  PairCtl* ctl = reinterpret_cast<PairCtl*>(stages + kStages * kStageBytes);
+  unsigned char* staging = stages + kStages * kStageBytes;
+  PairCtl* ctl = reinterpret_cast<PairCtl*>(staging + kEpiWarps * E::kWarpBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
@@ -177,6 +276,7 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
       mbar_init(&ctl->accf[b], 1);
       mbar_init(&ctl->acce[b], 2 * kEpiWarps);
     }
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&ctl->epi[w], 1);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     fence_barrier_init();
@@ -311,22 +411,31 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
     }
   } else {
     // ----------------------------------------------------------- epilogue
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3;
+    const EpiWarp w{lane, (warp - 2) >> 2, staging + (warp - 2) * E::kWarpBytes,
+                    &ctl->epi[warp - 2], &ctl->abort, status};
+    typename E::State state{};
     for (int iter = 0;; ++iter) {
       const PairItem it = pair_item(probs, pair, pairs, iter);
       if (it.prob < 0) break;
       const PairTile tc = pair_tile(probs.p[it.prob], it.idx);
+      const int64_t row0 = tc.m0 + (int64_t)rank * kM + quarter * 32;
       const int buf = iter & 1;
+      epi.begin(state, w, it.prob, row0, tc.n0, tc.z);
       const bool got =
           mbar_wait_or_abort(&ctl->accf[buf], (iter >> 1) & 1, &ctl->abort, status);
-      if (!__all_sync(0xffffffffu, got)) break;
+      if (!__all_sync(0xffffffffu, got)) {
+        epi.abandon(state, w);
+        break;
+      }
       tc_fence_after();
-      epi.tile(it.prob, tc.m0 + (int64_t)rank * kM + quarter * 32 + lane, tc.n0, half, tc.z,
-               tmem + ((uint32_t)(quarter * 32) << 16) + buf * kN + half * kNh);
+      epi.tile(state, w, it.prob, row0, tc.n0, tc.z,
+               tmem + ((uint32_t)(quarter * 32) << 16) + buf * kN + w.half * kNh);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) remote_arrive(map_to(&ctl->acce[buf], 0));
     }
+    if (E::kWarpBytes > 0) stage_free(lane);  // no store reads shared memory any more
   }
 
   // both CTAs finished: the leader's MMAs no longer read either CTA's shared
@@ -387,6 +496,24 @@ inline bool pair_map(CUtensorMap* m, const void* base, int64_t rows, int K, int6
   return make_tmap_bf16(m, base, 2, dims, strides, box);
 }
 
+// Tensor map of an output (or fp32 input) of an epilogue: [slices][rows][cols]
+// with `ld` elements from row to row; boxes of 32 rows and 128 bytes (64 with
+// half) of columns.
+inline bool pair_out_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows,
+                         int64_t slices, int64_t ld, pkm_dtype dt, bool half = false) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  const int b = dt == PKM_F32 ? 4 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)slices};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * b, (cuuint64_t)(ld * rows) * b};
+  const cuuint32_t box[3] = {(cuuint32_t)((half ? 64 : 128) / b), 32, 1}, one[3] = {1, 1, 1};
+  return enc(m, dt == PKM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline PairProb pair_prob(int64_t M, int N, int K, bool amn, bool bmn, int nz = 1,
                           int group_m = 1) {
   const int kb = (K + gp::kKB - 1) / gp::kKB;
@@ -416,12 +543,12 @@ int pair_slots() {
   if (cached[dev]) return cached[dev];
   auto kern = pair_gemm_kernel<NP, E>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)gp::kSmemBytes) != cudaSuccess)
+                           (int)gp::smem_bytes<E>()) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(gp::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = gp::kSmemBytes;
+  cfg.dynamicSmemBytes = gp::smem_bytes<E>();
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -455,7 +582,7 @@ cudaError_t launch_pair_gemm(const PairMaps<NP>& maps, PairProbs<NP> probs, cons
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
   cfg.blockDim = dim3(gp::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = gp::kSmemBytes;
+  cfg.dynamicSmemBytes = gp::smem_bytes<E>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -13,37 +13,70 @@ namespace pkm {
 
 namespace {
 constexpr int kThreads = 256;
+constexpr int kHalves = kThreads / kGroupLanes;  // groups a block handles at a time
+constexpr int kAtOnce = 4;                       // groups in flight per half-warp
+
+// Element offset of this lane's unit of group gi, or -1 past the row's end.
+__device__ __forceinline__ int64_t unit_at(int64_t gi, int64_t n_groups, int groups, int d) {
+  const int in = (threadIdx.x % kGroupLanes) * kUnit;
+  if (gi >= n_groups) return -1;
+  if (d % kQ8Group == 0) return gi * kQ8Group + in;  // no division
+  const int64_t row = gi / groups;
+  const int col = (int)(gi - row * groups) * kQ8Group + in;
+  return col < d ? row * d + col : -1;
+}
 
 template <pkm_dtype DT>
 __global__ void __launch_bounds__(kThreads) act8_store_kernel(
     const typename Elem<DT>::T* __restrict__ x, int64_t n_groups, int groups, int d, pkm_q8 fmt,
     uint8_t* __restrict__ q, float* __restrict__ scales) {
-  const int64_t gi = (int64_t)blockIdx.x * (kThreads / kGroupLanes) + threadIdx.x / kGroupLanes;
-  const int64_t row = gi / groups;
-  const int col = (int)(gi - row * groups) * kQ8Group + (threadIdx.x % kGroupLanes) * kUnit;
-  const bool live = gi < n_groups && col < d;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live) load8<DT>(x + row * d + col, v);
-  const float s = q8_scale(group_amax_bits(v), fmt);
-  if (live) *reinterpret_cast<uint2*>(q + row * d + col) = q8_encode(v, q8_inverse(s), fmt);
-  if (gi < n_groups && threadIdx.x % kGroupLanes == 0) scales[gi] = s;
+  const int64_t g0 = (int64_t)blockIdx.x * (kHalves * kAtOnce) + threadIdx.x / kGroupLanes;
+  int64_t at[kAtOnce];
+  Raw8<DT> raw[kAtOnce];
+#pragma unroll
+  for (int u = 0; u < kAtOnce; ++u) {
+    at[u] = unit_at(g0 + u * kHalves, n_groups, groups, d);
+    raw[u].zero();
+    if (at[u] >= 0) raw[u].load(x + at[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kAtOnce; ++u) {
+    float v[8];
+    raw[u].unpack(v);
+    const float s = q8_scale(group_amax_bits(v), fmt);
+    if (at[u] >= 0) *reinterpret_cast<uint2*>(q + at[u]) = q8_encode(v, q8_inverse(s), fmt);
+    const int64_t gi = g0 + u * kHalves;
+    if (gi < n_groups && threadIdx.x % kGroupLanes == 0) scales[gi] = s;
+  }
 }
 
 template <pkm_dtype DT>
 __global__ void __launch_bounds__(kThreads) act8_load_kernel(
     const uint8_t* __restrict__ q, const float* __restrict__ scales, int64_t n_groups, int groups,
     int d, pkm_q8 fmt, typename Elem<DT>::T* __restrict__ out) {
-  const int64_t gi = (int64_t)blockIdx.x * (kThreads / kGroupLanes) + threadIdx.x / kGroupLanes;
-  const int64_t row = gi / groups;
-  const int col = (int)(gi - row * groups) * kQ8Group + (threadIdx.x % kGroupLanes) * kUnit;
-  if (gi >= n_groups || col >= d) return;
-  float v[8];
-  q8_decode(*reinterpret_cast<const uint2*>(q + row * d + col), scales[gi], fmt, v);
-  store8<DT>(out + row * d + col, v);
+  const int64_t g0 = (int64_t)blockIdx.x * (kHalves * kAtOnce) + threadIdx.x / kGroupLanes;
+  int64_t at[kAtOnce];
+  uint2 raw[kAtOnce];
+  float s[kAtOnce];
+#pragma unroll
+  for (int u = 0; u < kAtOnce; ++u) {
+    at[u] = unit_at(g0 + u * kHalves, n_groups, groups, d);
+    if (at[u] >= 0) {
+      raw[u] = *reinterpret_cast<const uint2*>(q + at[u]);
+      s[u] = scales[g0 + u * kHalves];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kAtOnce; ++u)
+    if (at[u] >= 0) {
+      float v[8];
+      q8_decode(raw[u], s[u], fmt, v);
+      store8<DT>(out + at[u], v);
+    }
 }
 
 unsigned group_grid(int64_t n_groups) {
-  return (unsigned)((n_groups + kThreads / kGroupLanes - 1) / (kThreads / kGroupLanes));
+  return (unsigned)((n_groups + kHalves * kAtOnce - 1) / (kHalves * kAtOnce));
 }
 }  // namespace
 
@@ -90,8 +123,8 @@ pkm_status act8_validate(const void* x, int64_t T, int32_t d, pkm_dtype dtype, p
   if (T < 0 || d < 8 || d % 8 || (dtype != PKM_F32 && dtype != PKM_BF16) ||
       (fmt != PKM_Q8_E4M3 && fmt != PKM_Q8_INT8))
     return PKM_ERR_INVALID_ARG;
-  // the grid holds 16 groups per block
-  if (T > kMaxTokens || T > ((int64_t(1) << 31) - 1) * 16 / q8_groups(d))
+  // the grid holds 64 groups per block
+  if (T > kMaxTokens || T > ((int64_t(1) << 31) - 1) * 64 / q8_groups(d))
     return PKM_ERR_UNSUPPORTED;
   if (T > 0 && (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, 16)))
     return PKM_ERR_INVALID_ARG;

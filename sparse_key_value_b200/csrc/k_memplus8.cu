@@ -26,107 +26,143 @@ namespace {
 
 // dz, fp32
 struct Memplus8Dz {
-  int64_t T;
-  int dv;
-  float* dz;
+  CUtensorMap map;
+  StoreOut out;
 
-  __device__ __forceinline__ void tile(int, int64_t m, int n0, int half, int,
+  static constexpr int kStages = 6, kWarpBytes = 4096;
+  struct State {};
+  __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
+  __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
+  __device__ __forceinline__ void tile(State&, const EpiWarp& w, int, int64_t row0, int n0, int z,
                                        uint32_t tmem) const {
-#pragma unroll 1
-    for (int q = 0; q < gp::kNh / 32; ++q) {
-      const int col = n0 + half * gp::kNh + q * 32;
-      if (col >= dv) break;
-      uint32_t r[32];
-      __syncwarp();  // the load is warp-aligned
-      tmem_ld_32x32b_x32(tmem + q * 32, r);
-      tmem_ld_wait();
-      if (m < T) store_cols_f32(dz + m * dv, col, dv, r, false);
-    }
+    store_tile(out, &map, w, row0, n0, z, tmem);
   }
 };
 
-// a in TMEM, dz and y from memory -> dy, da, z
+// a in TMEM, dz and y from memory -> dy, da, z.  A warp takes 32 columns at a
+// time: dz comes by tensor copies and the lane's bytes of y by loads, the next
+// 32 columns' as soon as these are in registers, the tile's first before its
+// products are done; the three results go out by tensor copies.  A half of
+// the tile is one quantisation group, so a lane has one scale.
 struct Memplus8Gate {
+  CUtensorMap dz_map, dy_map, da_map, z_map;
   int64_t T;
   int dv;
   pkm_q8 fmt;
-  const float* dz;
   const uint8_t* y8;
   const float* y_scales;
-  __nv_bfloat16 *dy, *da, *z;
 
-  __device__ __forceinline__ void tile(int, int64_t m, int n0, int half, int,
-                                       uint32_t tmem) const {
-    const int c0 = n0 + half * gp::kNh;  // one quantisation group
-    const float s =
-        m < T && c0 < dv ? y_scales[m * q8_groups(dv) + c0 / kQ8Group] : 0.f;
-#pragma unroll 1
-    for (int q = 0; q < gp::kNh / 16; ++q) {
-      const int col = c0 + q * 16;
-      if (col >= dv) break;
-      uint32_t r[16];
-      __syncwarp();  // the load is warp-aligned
-      tmem_ld_32x32b_x16(tmem + q * 16, r);
-      tmem_ld_wait();
-      if (m >= T) continue;
+  static constexpr int kStages = 4, kWarpBytes = 4096 + 3 * 2048;  // 10 KiB
+  struct State {
+    uint2 y[4];     // the lane's 32 bytes of the next columns
+    float scale;
+    uint32_t phase;
+    bool waiting;   // a copy of dz is in flight
+    bool dead;      // a wait ran out: no more copies
+  };
+
+  __device__ __forceinline__ void fetch(State& s, const EpiWarp& w, int64_t row0, int col) const {
+    if (w.lane == 0) {
+      mbar_arrive_expect_tx(w.bar, 4096);
+      tma_load_3d(w.stage, &dz_map, w.bar, col, (int)row0, 0);
+    }
+    s.waiting = true;
+    const int64_t m = row0 + w.lane;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int c = col + 8 * u;
-        if (c >= dv) break;
-        const int64_t at = m * dv + c;
-        float y[8], d[8], o[3][8];
-        q8_decode(*reinterpret_cast<const uint2*>(y8 + at), s, fmt, y);
-        load8<PKM_F32>(dz + at, d);
+    for (int u = 0; u < 4; ++u)
+      if (m < T && col + 8 * u < dv)
+        s.y[u] = *reinterpret_cast<const uint2*>(y8 + m * dv + col + 8 * u);
+  }
+  __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int n0,
+                                        int) const {
+    const int c0 = n0 + w.half * gp::kNh;
+    if (row0 >= T || c0 >= dv || s.dead) return;
+    fetch(s, w, row0, c0);
+    const int64_t m = row0 + w.lane;
+    if (m < T) s.scale = y_scales[m * q8_groups(dv) + c0 / kQ8Group];
+  }
+  __device__ __forceinline__ void abandon(State& s, const EpiWarp& w) const {
+    if (s.waiting)
+      for (unsigned long long i = 0; i < kSpinLimit; ++i)
+        if (mbar_try_wait(w.bar, s.phase)) break;
+    s.waiting = false;
+    s.dead = true;
+  }
+
+  __device__ __forceinline__ void tile(State& s, const EpiWarp& w, int, int64_t row0, int n0, int,
+                                       uint32_t tmem) const {
+    const int c0 = n0 + w.half * gp::kNh;
+    if (row0 >= T || c0 >= dv || s.dead) return;  // the whole warp
+    unsigned char* const outs = w.stage + 4096;
+#pragma unroll 1
+    for (int q = 0; q < gp::kNh / 32; ++q) {
+      const int col = c0 + q * 32;
+      if (col >= dv) break;
+      const bool got = mbar_wait_or_abort(w.bar, s.phase, w.abort, w.status);  // dz
+      if (!__all_sync(0xffffffffu, got)) {
+        abandon(s, w);
+        return;
+      }
+      s.phase ^= 1;
+      s.waiting = false;
+      uint2 yq[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) yq[u] = s.y[u];
+      uint4 d[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        d[j] = *reinterpret_cast<const uint4*>(w.stage + w.lane * 128 + ((j ^ (w.lane & 7)) << 4));
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tmem + q * 32, r);
+      tmem_ld_wait();
+      __syncwarp();  // every lane has its dz: the buffer may be filled again
+      if (q + 1 < gp::kNh / 32 && col + 32 < dv) fetch(s, w, row0, col + 32);
+      stage_free(w.lane);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float y[8], o[3][8];
+        q8_decode(yq[u], s.scale, fmt, y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
+          const uint4& dq = d[2 * u + (e >> 2)];
+          const float dzv = __uint_as_float((e & 3) == 0 ? dq.x : (e & 3) == 1 ? dq.y
+                                                                : (e & 3) == 2 ? dq.z : dq.w);
           const float a = __uint_as_float(r[8 * u + e]);
-          const float sg = 1.0f / (1.0f + __expf(-a));
+          const float sg = __fdividef(1.0f, 1.0f + __expf(-a));
           const float g = a * sg;
-          o[0][e] = d[e] * g;
-          o[1][e] = d[e] * y[e] * (sg + g * (1.0f - sg));
+          o[0][e] = dzv * g;
+          o[1][e] = dzv * y[e] * fmaf(g, 1.0f - sg, sg);
           o[2][e] = y[e] * g;
         }
-        store8<PKM_BF16>(dy + at, o[0]);
-        store8<PKM_BF16>(da + at, o[1]);
-        store8<PKM_BF16>(z + at, o[2]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint4*>(stage64_at(outs + k * 2048, w.lane, u)) =
+              pack16<PKM_BF16>(o[k]);
       }
+      stage_ready();
+      if (w.lane == 0) {
+        tma_store_3d(&dy_map, outs, col, (int)row0, 0);
+        tma_store_3d(&da_map, outs + 2048, col, (int)row0, 0);
+        tma_store_3d(&z_map, outs + 4096, col, (int)row0, 0);
+        bulk_commit();
+      }
+      __syncwarp();
     }
   }
 };
 
-// Problems 0 and 1: slices of dW1 and dW2 (fp32, or the output itself when
-// there is one slice and it is fp32).  Problem 2: dx.
+// Problems 0 and 1: slices of dW1 and dW2 (fp32).  Problem 2: dx.
 struct Memplus8Grads {
-  int64_t T;
-  int dm, dv;
-  float *w1, *w2;
-  void* dx;
-  int dx_bf16;
+  CUtensorMap map[3];
+  StoreOut out[3];
 
-  __device__ __forceinline__ void tile(int prob, int64_t m, int n0, int half, int z,
-                                       uint32_t tmem) const {
-    const int64_t rows = prob == 0 ? dm : prob == 1 ? dv : T;
-    const int cols = prob == 0 ? dv : dm;
-#pragma unroll 1
-    for (int q = 0; q < gp::kNh / 32; ++q) {
-      const int col = n0 + half * gp::kNh + q * 32;
-      if (col >= cols) break;
-      uint32_t r[32];
-      __syncwarp();  // the load is warp-aligned
-      tmem_ld_32x32b_x32(tmem + q * 32, r);
-      tmem_ld_wait();
-      if (m >= rows) continue;
-      if (prob == 2 && dx_bf16) {
-        float f[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
-        store_cols_bf16(static_cast<__nv_bfloat16*>(dx) + m * dm, col, dm, f);
-      } else {
-        float* out = prob == 2 ? static_cast<float*>(dx)
-                               : (prob == 0 ? w1 : w2) + (int64_t)z * dm * dv;
-        store_cols_f32(out + m * cols, col, cols, r, false);
-      }
-    }
+  static constexpr int kStages = 6, kWarpBytes = 4096;
+  struct State {};
+  __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
+  __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
+  __device__ __forceinline__ void tile(State&, const EpiWarp& w, int prob, int64_t row0, int n0,
+                                       int z, uint32_t tmem) const {
+    store_tile(out[prob], &map[prob], w, row0, n0, z, tmem);
   }
 };
 
@@ -222,15 +258,22 @@ cudaError_t memplus8_backward(const pkm_memplus_bwd8_args* g, int32_t* status, c
         !pair_map(&m.b[0], g->W2, dv, dm, dm, false))
       return cudaErrorInvalidValue;
     const PairProbs<1> p{{pair_prob(T, dv, dm, false, false)}, 1, {}};
-    PKM_TRY((launch_pair_gemm<1>(m, p, Memplus8Dz{T, dv, dz}, status, st)));
+    Memplus8Dz epi{{}, {T, dv, 0, 0}};
+    if (!pair_out_map(&epi.map, dz, dv, T, 1, dv, PKM_F32)) return cudaErrorInvalidValue;
+    PKM_TRY((launch_pair_gemm<1>(m, p, epi, status, st)));
   }
   {  // a = x W1 and everything elementwise
     PairMaps<1> m;
     if (!pair_map(&m.a[0], xb, T, dm, dm, false) || !pair_map(&m.b[0], g->W1, dv, dm, dv, true))
       return cudaErrorInvalidValue;
     const PairProbs<1> p{{pair_prob(T, dv, dm, false, true)}, 1, {}};
-    const Memplus8Gate epi{T,  dv, g->fmt, dz, static_cast<const uint8_t*>(g->y8),
-                           g->y_scales, static_cast<__nv_bfloat16*>(g->dy), da, z};
+    Memplus8Gate epi{{}, {}, {}, {}, T, dv, g->fmt, static_cast<const uint8_t*>(g->y8),
+                     g->y_scales};
+    if (!pair_out_map(&epi.dz_map, dz, dv, T, 1, dv, PKM_F32) ||
+        !pair_out_map(&epi.dy_map, g->dy, dv, T, 1, dv, PKM_BF16, true) ||
+        !pair_out_map(&epi.da_map, da, dv, T, 1, dv, PKM_BF16, true) ||
+        !pair_out_map(&epi.z_map, z, dv, T, 1, dv, PKM_BF16, true))
+      return cudaErrorInvalidValue;
     PKM_TRY((launch_pair_gemm<1>(m, p, epi, status, st)));
   }
   const bool gb = g->grad_dtype == PKM_BF16;
@@ -247,7 +290,12 @@ cudaError_t memplus8_backward(const pkm_memplus_bwd8_args* g, int32_t* status, c
     const PairProbs<3> p{{pair_prob(dm, dv, (int)T, true, true, L.nz),
                           pair_prob(dv, dm, (int)T, true, true, L.nz),
                           pair_prob(T, dm, dv, false, false)}, 2, {}};
-    PKM_TRY((launch_pair_gemm<3>(m, p, Memplus8Grads{T, dm, dv, w1, w2, g->dx, gb}, status, st)));
+    Memplus8Grads epi{{}, {{dm, dv, 0, 0}, {dv, dm, 0, 0}, {T, dm, gb, 0}}};
+    if (!pair_out_map(&epi.map[0], w1, dv, dm, L.nz, dv, PKM_F32) ||
+        !pair_out_map(&epi.map[1], w2, dm, dv, L.nz, dm, PKM_F32) ||
+        !pair_out_map(&epi.map[2], g->dx, dm, T, 1, dm, g->grad_dtype))
+      return cudaErrorInvalidValue;
+    PKM_TRY((launch_pair_gemm<3>(m, p, epi, status, st)));
   }
   if (direct) return cudaSuccess;
   PKM_TRY(launch_slice_sum(w1, L.nz, (int64_t)dm * dv, g->dW1, g->grad_dtype, st));

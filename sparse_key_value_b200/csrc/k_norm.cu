@@ -66,22 +66,25 @@ __global__ void __launch_bounds__(block_threads(WPR)) norm_fwd_kernel(const Norm
   const int64_t base = row * p.d;
   float h[NU][8];
   float ss = 0.f;
-#pragma unroll
-  for (int c = 0; c < NU; ++c) {
-    const int col = col0 + c * (WPR * 32 * kUnit);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[c][e] = 0.f;
-    if (live && col < p.d) load8<DT>(static_cast<const E*>(p.x) + base + col, h[c]);
-  }
-  if (p.r) {
-    float r[NU][8];
+  {
+    Raw8<DT> x[NU], r[NU];
 #pragma unroll
     for (int c = 0; c < NU; ++c) {
       const int col = col0 + c * (WPR * 32 * kUnit);
+      x[c].zero();
       if (live && col < p.d) {
-        load8<DT>(static_cast<const E*>(p.r) + base + col, r[c]);
+        x[c].load(static_cast<const E*>(p.x) + base + col);
+        if (p.r) r[c].load(static_cast<const E*>(p.r) + base + col);
+      }
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[c][e] += r[c][e];
+    for (int c = 0; c < NU; ++c) {
+      x[c].unpack(h[c]);
+      if (p.r && live && col0 + c * (WPR * 32 * kUnit) < p.d) {
+        float f[8];
+        r[c].unpack(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[c][e] += f[e];
         round8<DT>(h[c]);
       }
     }
@@ -132,9 +135,12 @@ struct NormBwd {
   float* part;  // [blocks, d] weight-gradient partials, or null
 };
 
-// DY: type of dy; DT: type of h (when not 8-bit), weight, dsum and dx.
+// DY: type of dy; DT: type of h (when not 8-bit), weight, dsum and dx.  A
+// row's dy, h and dsum wait packed in registers, all loaded up front: two
+// blocks per SM then keep about 90 KB of loads in flight.
 template <pkm_dtype DT, pkm_dtype DY, int NU, int WPR>
-__global__ void __launch_bounds__(block_threads(WPR)) norm_bwd_kernel(const NormBwd p) {
+__global__ void __launch_bounds__(block_threads(WPR), WPR <= 16 ? 512 / block_threads(WPR) : 1)
+    norm_bwd_kernel(const NormBwd p) {
   using E = typename Elem<DT>::T;
   using Ey = typename Elem<DY>::T;
   constexpr int kWarps = block_threads(WPR) / 32;
@@ -155,48 +161,70 @@ __global__ void __launch_bounds__(block_threads(WPR)) norm_bwd_kernel(const Norm
     const bool live = row < p.T;
     const int64_t base = row * p.d;
     const float rstd = live ? p.rstd[row] : 0.f;
-    float g[NU][8], n[NU][8];
+    Raw8<DY> dy[NU];
+    Raw8<DT> h[NU], ds[NU];
+    float hs[NU];  // 8-bit h: its scale (the bytes wait in h)
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      const int col = col0 + c * (WPR * 32 * kUnit);
+      dy[c].zero();
+      h[c].zero();
+      ds[c].zero();
+      hs[c] = 0.f;
+      if (live && col < p.d) {
+        dy[c].load(static_cast<const Ey*>(p.dy) + base + col);
+        if (p.fmt == PKM_Q8_NONE) {
+          h[c].load(static_cast<const E*>(p.h) + base + col);
+        } else {
+          const uint2 q =
+              *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.h) + base + col);
+          h[c].v[0].x = q.x;
+          h[c].v[0].y = q.y;
+          hs[c] = p.scales[row * groups + col / kQ8Group];
+        }
+        if (p.dsum) ds[c].load(static_cast<const E*>(p.dsum) + base + col);
+      }
+    }
+    auto unpack = [&](int c, float* g, float* n) {  // g = dy w, n = h rstd
+      if (p.fmt == PKM_Q8_NONE)
+        h[c].unpack(n);
+      else
+        q8_decode(make_uint2(h[c].v[0].x, h[c].v[0].y), hs[c], p.fmt, n);
+      dy[c].unpack(g);
+      const int col = col0 + c * (WPR * 32 * kUnit);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n[e] *= rstd;
+      return col;
+    };
+    auto weigh = [&](int col, float* g) {
+      if (p.w && col < p.d) {
+        float w[8];
+        load8<DT>(static_cast<const E*>(p.w) + col, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] *= w[e];
+      }
+    };
     float dot = 0.f;
 #pragma unroll
     for (int c = 0; c < NU; ++c) {
-      const int col = col0 + c * (WPR * 32 * kUnit);
+      float g[8], n[8];
+      const int col = unpack(c, g, n);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[c][e] = n[c][e] = 0.f;
-      if (live && col < p.d) {
-        load8<DY>(static_cast<const Ey*>(p.dy) + base + col, g[c]);
-        if (p.fmt == PKM_Q8_NONE)
-          load8<DT>(static_cast<const E*>(p.h) + base + col, n[c]);
-        else
-          q8_decode(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.h) + base + col),
-                    p.scales[row * groups + col / kQ8Group], p.fmt, n[c]);
-      }
-    }
+      for (int e = 0; e < 8; ++e) dw[c][e] = fmaf(g[e], n[e], dw[c][e]);
+      weigh(col, g);
 #pragma unroll
-    for (int c = 0; c < NU; ++c) {
-      const int col = col0 + c * (WPR * 32 * kUnit);
-      float w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.f;
-      if (p.w && col < p.d) load8<DT>(static_cast<const E*>(p.w) + col, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        n[c][e] *= rstd;
-        dw[c][e] = fmaf(g[c][e], n[c][e], dw[c][e]);
-        g[c][e] *= w[e];
-        dot = fmaf(g[c][e], n[c][e], dot);
-      }
+      for (int e = 0; e < 8; ++e) dot = fmaf(g[e], n[e], dot);
     }
     const float mean = row_sum<WPR>(dot, red) / (float)p.d;
 #pragma unroll
     for (int c = 0; c < NU; ++c) {
-      const int col = col0 + c * (WPR * 32 * kUnit);
+      float g[8], n[8], o[8];
+      const int col = unpack(c, g, n);
       if (!(live && col < p.d)) continue;
-      float o[8];
+      weigh(col, g);
+      ds[c].unpack(o);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = 0.f;
-      if (p.dsum) load8<DT>(static_cast<const E*>(p.dsum) + base + col, o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] += rstd * (g[c][e] - n[c][e] * mean);
+      for (int e = 0; e < 8; ++e) o[e] += rstd * (g[e] - n[e] * mean);
       store8<DT>(static_cast<E*>(p.dx) + base + col, o);
     }
   }
@@ -247,25 +275,40 @@ constexpr int kBwdBlocks = 148 * 2;
 
 int rows_per_block(int wpr) { return wpr >= 8 ? 1 : 8 / wpr; }
 
-// Warps per row and units per lane: as few warps as hold the row with four
-// units a lane (no block barrier up to 1024 columns).
-template <typename F>
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// Units per lane and warps per row: as few warps as hold the row with UMAX
+// units a lane.  Four of bf16 (no block barrier up to 1024 columns), two of
+// fp32 (the same registers).
+template <int UMAX, typename F>
 cudaError_t norm_shape(int d, F&& f) {
-  if (d <= 256) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-  if (d <= 512) return f(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
-  if (d <= 1024) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
-  if (d <= 2048) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-  if (d <= 4096) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
-  if (d <= 8192) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
-  return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 16>{});
+  if (d <= 256) return f(Int<1>{}, Int<1>{});
+  if (d <= 512) return f(Int<2>{}, Int<1>{});
+  if constexpr (UMAX == 4) {
+    if (d <= 1024) return f(Int<4>{}, Int<1>{});
+    if (d <= 2048) return f(Int<4>{}, Int<2>{});
+    if (d <= 4096) return f(Int<4>{}, Int<4>{});
+    if (d <= 8192) return f(Int<4>{}, Int<8>{});
+    return f(Int<4>{}, Int<16>{});
+  } else {
+    if (d <= 1024) return f(Int<2>{}, Int<2>{});
+    if (d <= 2048) return f(Int<2>{}, Int<4>{});
+    if (d <= 4096) return f(Int<2>{}, Int<8>{});
+    if (d <= 8192) return f(Int<2>{}, Int<16>{});
+    return f(Int<2>{}, Int<32>{});
+  }
 }
 
-int bwd_blocks(int64_t T, int d) {
+// Blocks of the backward (each writes a partial weight gradient): two per SM
+// of 256 threads, at most one per group of rows.
+int bwd_blocks(int64_t T, int d, bool f32) {
   int rows = 1;
-  norm_shape(d, [&](auto, auto wpr) {
+  const auto f = [&](auto, auto wpr) {
     rows = rows_per_block(decltype(wpr)::value);
     return cudaSuccess;
-  });
+  };
+  f32 ? norm_shape<2>(d, f) : norm_shape<4>(d, f);
   const int64_t b = (T + rows - 1) / rows;
   return (int)(b < kBwdBlocks ? b : kBwdBlocks);
 }
@@ -275,7 +318,7 @@ bool need16(const void* p) { return p && al16(p); }
 
 template <pkm_dtype DT>
 cudaError_t fwd_launch(const NormFwd& p, cudaStream_t st) {
-  return norm_shape(p.d, [&](auto nu, auto wpr) {
+  return norm_shape<4>(p.d, [&](auto nu, auto wpr) {
     constexpr int NU = decltype(nu)::value, WPR = decltype(wpr)::value;
     const int rows = rows_per_block(WPR);
     norm_fwd_kernel<DT, NU, WPR>
@@ -287,8 +330,9 @@ cudaError_t fwd_launch(const NormFwd& p, cudaStream_t st) {
 
 template <pkm_dtype DT, pkm_dtype DY>
 cudaError_t bwd_launch(const NormBwd& p, float* dweight, cudaStream_t st) {
-  const int blocks = bwd_blocks(p.T, p.d);
-  const cudaError_t e = norm_shape(p.d, [&](auto nu, auto wpr) {
+  constexpr bool f32 = DT == PKM_F32 || DY == PKM_F32;
+  const int blocks = bwd_blocks(p.T, p.d, f32);
+  const cudaError_t e = norm_shape<f32 ? 2 : 4>(p.d, [&](auto nu, auto wpr) {
     constexpr int NU = decltype(nu)::value, WPR = decltype(wpr)::value;
     norm_bwd_kernel<DT, DY, NU, WPR><<<blocks, block_threads(WPR), 0, st>>>(p);
     note_launch();
@@ -318,7 +362,8 @@ pkm_status fwd_validate(const pkm_norm_args* a) {
 
 size_t bwd_bytes(const pkm_norm_bwd_args* a) {
   if (a->T <= 0 || a->d < 8 || a->d > kMaxD) return 0;
-  return (size_t)bwd_blocks(a->T, a->d) * (size_t)a->d * 4;
+  const bool f32 = a->dtype == PKM_F32 || a->dy_dtype == PKM_F32;
+  return (size_t)bwd_blocks(a->T, a->d, f32) * (size_t)a->d * 4;
 }
 
 pkm_status bwd_validate(const pkm_norm_bwd_args* a) {

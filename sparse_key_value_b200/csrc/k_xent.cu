@@ -43,12 +43,23 @@ struct XentStats {
   float2* part;  // [2 * tiles_n][T]: maximum (base 2) and sum
   float* picked;
 
-  __device__ __forceinline__ void tile(int, int64_t m, int n0, int half, int,
-                                       uint32_t tmem) const {
-    const bool live = m < T;
-    const int t = live ? target[m] : -1;
+  static constexpr int kStages = 6, kWarpBytes = 0;
+  struct State {
+    int target;
+  };
+  __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int,
+                                        int) const {
+    s.target = row0 + w.lane < T ? target[row0 + w.lane] : -1;
+  }
+  __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
+
+  __device__ __forceinline__ void tile(State& st, const EpiWarp& w, int, int64_t row0, int n0,
+                                       int, uint32_t tmem) const {
+    if (row0 >= T) return;  // the whole warp
+    const int64_t m = row0 + w.lane;
+    const int t = st.target;
     float mx = -INFINITY, sum = 0.f;
-    const int c0 = n0 + half * gp::kNh;
+    const int c0 = n0 + w.half * gp::kNh;
 #pragma unroll 1
     for (int g = 0; g < gp::kNh / 32; ++g) {
       const int col = c0 + g * 32;
@@ -79,36 +90,54 @@ struct XentStats {
           if (at == j) picked[m] = __uint_as_float(r[j]);
       }
     }
-    if (live) part[(int64_t)(c0 / gp::kNh) * T + m] = make_float2(mx, sum);
+    if (m < T) part[(int64_t)(c0 / gp::kNh) * T + m] = make_float2(mx, sum);
   }
 };
 
-// lse and loss from the partials: 32 rows per block, 16 strips of partials
-constexpr int kJoinStrips = 16;
+// lse and loss from the partials: 8 rows per block, 64 strips of partials (a
+// warp reads 8 rows of 4 strips), joined over the warp, then over the warps.
+constexpr int kJoinRows = 8, kJoinThreads = 512;
 
-__global__ void __launch_bounds__(32 * kJoinStrips) xent_join_kernel(
+struct MaxSum {
+  float mx, sum;
+  __device__ __forceinline__ void join(float qm, float qs) {
+    const float nm = fmaxf(mx, qm);
+    const float ref = nm == -INFINITY ? 0.f : nm;
+    sum = sum * ex2(mx - ref) + qs * ex2(qm - ref);
+    mx = nm;
+  }
+};
+
+__global__ void __launch_bounds__(kJoinThreads) xent_join_kernel(
     const float2* __restrict__ part, int slots, int64_t T, int V,
     const int32_t* __restrict__ target, int32_t ignore, const float* __restrict__ picked,
     float* __restrict__ loss, float* __restrict__ lse, int32_t* status) {
-  __shared__ float2 sm[kJoinStrips][32];
-  const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
-  const int64_t m = (int64_t)blockIdx.x * 32 + lane;
-  float mx = -INFINITY, sum = 0.f;
-  auto join = [&](float2 q) {
-    const float nm = fmaxf(mx, q.x);
-    const float ref = nm == -INFINITY ? 0.f : nm;
-    sum = sum * ex2(mx - ref) + q.y * ex2(q.x - ref);
-    mx = nm;
-  };
-  if (m < T) {
-#pragma unroll 4
-    for (int s = strip; s < slots; s += kJoinStrips) join(part[(int64_t)s * T + m]);
+  __shared__ float2 sm[kJoinThreads / 32][kJoinRows];
+  constexpr int kStrips = kJoinThreads / kJoinRows, kAtOnce = 4;
+  const int in = threadIdx.x % kJoinRows, strip = threadIdx.x / kJoinRows;
+  const int64_t m = (int64_t)blockIdx.x * kJoinRows + in;
+  MaxSum v{-INFINITY, 0.f};
+  for (int s0 = strip; s0 < slots && m < T; s0 += kAtOnce * kStrips) {
+    float2 q[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int s = s0 + u * kStrips;
+      q[u] = s < slots ? part[(int64_t)s * T + m] : make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) v.join(q[u].x, q[u].y);
   }
-  sm[strip][lane] = make_float2(mx, sum);
+#pragma unroll
+  for (int o = kJoinRows; o < 32; o <<= 1) {
+    const float qm = __shfl_xor_sync(0xffffffffu, v.mx, o);
+    const float qs = __shfl_xor_sync(0xffffffffu, v.sum, o);
+    v.join(qm, qs);
+  }
+  if ((threadIdx.x & 31) < kJoinRows) sm[threadIdx.x >> 5][in] = make_float2(v.mx, v.sum);
   __syncthreads();
-  if (strip != 0 || m >= T) return;
-  for (int s = 1; s < kJoinStrips; ++s) join(sm[s][lane]);
-  const float l = (mx + log2f(sum)) * kLn2;
+  if (threadIdx.x >= kJoinRows || m >= T) return;
+  for (int k = 1; k < kJoinThreads / 32; ++k) v.join(sm[k][in].x, sm[k][in].y);
+  const float l = (v.mx + log2f(v.sum)) * kLn2;
   lse[m] = l;
   const int32_t t = target[m];
   const bool counted = t != ignore && t >= 0 && t < V;
@@ -118,49 +147,64 @@ __global__ void __launch_bounds__(32 * kJoinStrips) xent_join_kernel(
 
 // d of one vocabulary piece, bf16
 struct XentDelta {
+  CUtensorMap out;  // [T][Vp]
   int64_t T;
-  int Vp, v0, V;  // piece columns, first column, vocabulary
+  int Vp, v0, V;    // piece columns, first column, vocabulary
   const int32_t* target;
   int32_t ignore;
   const float *lse, *dloss;
-  __nv_bfloat16* out;  // [T][ld]
-  int64_t ld;
 
-  __device__ __forceinline__ void tile(int, int64_t m, int n0, int half, int,
+  static constexpr int kStages = 6, kWarpBytes = 4096;
+  struct State {
+    int target;
+    float g, l2;
+    bool counted;
+  };
+  __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int,
+                                        int) const {
+    const int64_t m = row0 + w.lane;
+    s.target = m < T ? target[m] : ignore;
+    s.counted = s.target != ignore && s.target >= 0 && s.target < V;
+    s.g = s.counted ? dloss[m] : 0.f;
+    s.l2 = s.counted ? lse[m] * kLog2e : 0.f;
+  }
+  __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
+
+  __device__ __forceinline__ void tile(State& s, const EpiWarp& w, int, int64_t row0, int n0, int,
                                        uint32_t tmem) const {
-    const bool live = m < T;
-    const int t = live ? target[m] : ignore;
-    const bool counted = t != ignore && t >= 0 && t < V;
-    const float g = counted ? dloss[m] : 0.f;
-    const float l2 = counted ? lse[m] * kLog2e : 0.f;
-    const int c0 = n0 + half * gp::kNh;
+    if (row0 >= T) return;  // the whole warp
+    const int c0 = n0 + w.half * gp::kNh;
 #pragma unroll 1
-    for (int q = 0; q < gp::kNh / 32; ++q) {
-      const int col = c0 + q * 32;
+    for (int q = 0; q < gp::kNh; q += 32) {
+      const int col = c0 + q;
       if (col >= Vp) break;
       uint32_t r[32];
       __syncwarp();  // the load is warp-aligned
-      tmem_ld_32x32b_x32(tmem + q * 32, r);
+      tmem_ld_32x32b_x32(tmem + q, r);
       tmem_ld_wait();
-      if (!live) continue;
       float p[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) p[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -l2));
-      const uint32_t at = (uint32_t)t - (uint32_t)(v0 + col);
+      for (int j = 0; j < 32; ++j) p[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -s.l2));
+      const uint32_t at = (uint32_t)s.target - (uint32_t)(v0 + col);
       if (at < 32u) {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           if (at == j) p[j] -= 1.f;
       }
-      uint32_t w[16];
+      uint32_t o[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        w[j] = counted ? pack_bf16x2(p[2 * j] * g, p[2 * j + 1] * g) : 0u;
-      __nv_bfloat16* dst = out + m * ld + col;  // ld covers whole groups of 32 columns
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        reinterpret_cast<uint4*>(dst)[j] =
-            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        o[j] = s.counted ? pack_bf16x2(p[2 * j] * s.g, p[2 * j + 1] * s.g) : 0u;
+      const int h = (q >> 5) & 1;
+      if (h == 0) stage_free(w.lane);
+      stage_bf16(w.stage, w.lane, h, o);
+      if (h == 1 || col + 32 >= Vp) {
+        stage_ready();
+        if (w.lane == 0) {
+          tma_store_3d(&out, w.stage, col - 32 * h, (int)row0, 0);
+          bulk_commit();
+        }
+      }
     }
   }
 };
@@ -168,36 +212,16 @@ struct XentDelta {
 // Problem 0: dx partials, fp32 (overwritten or added to), one [T, d] slice per
 // z.  Problem 1: rows of dW.
 struct XentGrads {
-  int64_t T;
-  int Vp, d;
-  float* dx;
-  int add;
-  void* dW;  // at the piece's first row
-  int dw_bf16;
+  CUtensorMap map[2];
+  StoreOut out[2];
 
-  __device__ __forceinline__ void tile(int prob, int64_t m, int n0, int half, int z,
-                                       uint32_t tmem) const {
-    const int c0 = n0 + half * gp::kNh;
-    const bool live = m < (prob ? (int64_t)Vp : T);
-#pragma unroll 1
-    for (int q = 0; q < gp::kNh / 32; ++q) {
-      const int col = c0 + q * 32;
-      if (col >= d) break;
-      uint32_t r[32];
-      __syncwarp();  // the load is warp-aligned
-      tmem_ld_32x32b_x32(tmem + q * 32, r);
-      tmem_ld_wait();
-      if (!live) continue;
-      if (prob && dw_bf16) {
-        float f[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
-        store_cols_bf16(static_cast<__nv_bfloat16*>(dW) + m * d, col, d, f);
-      } else {
-        store_cols_f32((prob ? static_cast<float*>(dW) : dx + (int64_t)z * T * d) + m * d, col, d,
-                       r, !prob && add);
-      }
-    }
+  static constexpr int kStages = 6, kWarpBytes = 4096;
+  struct State {};
+  __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
+  __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
+  __device__ __forceinline__ void tile(State&, const EpiWarp& w, int prob, int64_t row0, int n0,
+                                       int z, uint32_t tmem) const {
+    store_tile(out[prob], &map[prob], w, row0, n0, z, tmem);
   }
 };
 
@@ -289,7 +313,7 @@ cudaError_t xent_forward(const pkm_xent_args* a, int32_t* status, cudaStream_t s
   const PairProbs<1> p{{pair_prob(a->T, a->V, a->d, false, false, 1, 8)}, 1, {}};
   const XentStats epi{a->T, a->V, a->targets, part, picked};
   PKM_TRY((launch_pair_gemm<1>(maps, p, epi, status, st)));
-  xent_join_kernel<<<(unsigned)((a->T + 31) / 32), 32 * kJoinStrips, 0, st>>>(
+  xent_join_kernel<<<(unsigned)((a->T + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, st>>>(
       part, fwd_slots(a->V), a->T, a->V, a->targets, a->ignore_index, picked, a->loss, a->lse,
       status);
   PKM_TRY(cudaGetLastError());
@@ -311,8 +335,8 @@ cudaError_t xent_backward(const pkm_xent_args* a, int32_t* status, cudaStream_t 
         !pair_map(&m1.b[0], Wp, Vp, a->d, a->d, false))
       return cudaErrorInvalidValue;
     const PairProbs<1> p{{pair_prob(a->T, Vp, a->d, false, false, 1, 8)}, 1, {}};
-    const XentDelta de{a->T,  Vp,    v0,    a->V, a->targets, a->ignore_index, a->lse, a->dloss,
-                       delta, L.ld};
+    XentDelta de{{}, a->T, Vp, v0, a->V, a->targets, a->ignore_index, a->lse, a->dloss};
+    if (!pair_out_map(&de.out, delta, Vp, a->T, 1, L.ld, PKM_BF16)) return cudaErrorInvalidValue;
     PKM_TRY((launch_pair_gemm<1>(m1, p, de, status, st)));
     PairMaps<2> m2;
     if (!pair_map(&m2.a[0], delta, a->T, Vp, L.ld, false) ||
@@ -323,8 +347,11 @@ cudaError_t xent_backward(const pkm_xent_args* a, int32_t* status, cudaStream_t 
     // a shorter last piece may fill fewer slices: the others keep their sums
     const PairProbs<2> q{{pair_prob(a->T, a->d, Vp, false, true, L.nz),
                           pair_prob(Vp, a->d, (int)a->T, true, true)}, 1, {}};
-    const XentGrads ge{a->T, Vp, a->d, dx, v0 > 0,
-                       static_cast<char*>(a->dW) + (size_t)v0 * a->d * (gb ? 2 : 4), gb};
+    XentGrads ge{{}, {{a->T, a->d, 0, v0 > 0}, {Vp, a->d, gb, 0}}};
+    if (!pair_out_map(&ge.map[0], dx, a->d, a->T, L.nz, a->d, PKM_F32) ||
+        !pair_out_map(&ge.map[1], static_cast<char*>(a->dW) + (size_t)v0 * a->d * (gb ? 2 : 4),
+                      a->d, Vp, 1, a->d, a->grad_dtype))
+      return cudaErrorInvalidValue;
     PKM_TRY((launch_pair_gemm<2>(m2, q, ge, status, st)));
   }
   if (direct) return cudaSuccess;

@@ -36,6 +36,25 @@ __device__ __forceinline__ void load8(const typename Elem<DT>::T* p, float* f) {
   }
 }
 
+// 8 consecutive elements as they are held: loads are issued for several
+// units before the first is unpacked, and wait in half the registers.
+template <pkm_dtype DT>
+struct Raw8 {
+  uint4 v[DT == PKM_F32 ? 2 : 1];
+  __device__ __forceinline__ void zero() {
+    v[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (DT == PKM_F32) v[1] = v[0];
+  }
+  __device__ __forceinline__ void load(const typename Elem<DT>::T* p) {
+    v[0] = *reinterpret_cast<const uint4*>(p);
+    if constexpr (DT == PKM_F32) v[1] = *reinterpret_cast<const uint4*>(p + 4);
+  }
+  __device__ __forceinline__ void unpack(float* f) const {
+    unpack16<DT>(v[0], f);
+    if constexpr (DT == PKM_F32) unpack16<DT>(v[1], f + 4);
+  }
+};
+
 // fp32 -> 8 consecutive elements (one rounding)
 template <pkm_dtype DT>
 __device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float* f) {

@@ -67,9 +67,11 @@ def test_forward_and_backward(T, V, d, kind, dtype):
 
 @pytest.mark.parametrize("T,V,kind", [(4095, 131072, "zipf"), (4096, 300, "zipf"),
                                       (4097, 65536, "uniform"), (20000, 131071, "zipf"),
-                                      (8300, 3, "uniform"), (5000, 70000, "same")])
+                                      (8300, 3, "uniform"), (5000, 70000, "same"),
+                                      (131072, 700, "zipf"), (140001, 200000, "zipf")])
 def test_backward_many_tokens(T, V, kind):
-    """Long lists: several sort blocks, ids over many chunks, up to 17 key bits."""
+    """Long lists: several sort blocks, ids over many chunks, up to 18 key bits, and
+    more tokens than one cluster sorts."""
     d = 64
     g = torch.Generator().manual_seed(T)
     ids, dout = _ids(g, T, V, kind), torch.randn(T, d, generator=g).to(BF)
