@@ -1,21 +1,28 @@
 // gemm_pair.cuh -- persistent bf16 GEMMs on pairs of SMs with an epilogue of
 // the caller's (loss statistics, softmax gradients, activation gradients).
 //
-//   acc[M, N] = A[M, K] B[N, K]^T, fp32 accumulation, 256 x 256 tiles per pair
+//   acc[M, N] = A[M, K] B[N, K]^T, fp32 accumulation, 256 x 512 tiles per pair
 //
 // through tcgen05.mma.cta_group::2: each CTA of a cluster of two loads its own
-// 128 rows of A and its own half of B (a ring of up to 6 stages of 32 KiB), one
-// instruction multiplies both, each CTA's epilogue reads its 128 rows from
-// TMEM while the next tile's products fill the other accumulator.  A or B may
-// be held K-major ([M][K]) or MN-major ([K][M]); one launch takes up to three
-// problems, so that the tiles of several products fill the GPU together.
+// 128 rows of A and its own half of B (a ring of stages of 48 KiB), one
+// instruction multiplies both CTAs' operands for 256 columns, two instructions
+// a step cover the tile.  Why 512 columns: the operand stream from L2 bounds a
+// pair of SMs.  256 columns need 64 bytes per SM and cycle at the full MMA
+// rate and reached 60-65 % of it (ncu: L2 slices at 35 %, DRAM idle); 512 need
+// 48.  The accumulators then fill TMEM (two buffers of 256 columns), so a
+// tile's products cannot start before the last tile's first buffer is read:
+// the products of the first buffer run ahead by up to a ring while the
+// epilogue reads the second.
+// A or B may be held K-major ([M][K]) or MN-major ([K][M]); one launch takes up
+// to three problems, so that the tiles of several products fill the GPU
+// together.
 //
 //   warp 0      TMA producer of this CTA's halves
 //   warp 1      TMEM; in the leader, the MMA issuer
 //   warps 2-9   epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 (rows) of
-//               column half (w - 2) / 4.  Two warps per lane quarter: with
-//               one, the exponentials of a 256-column tile outlast the
-//               products of a short K.
+//               column half (w - 2) / 4 of a buffer.  Two warps per lane
+//               quarter: with one, the exponentials outlast the products of a
+//               short K.
 // Spin-waits are bounded as in the library's other pipelined kernels: on a
 // timeout the status word is set, the roles stop issuing, the leader waits for
 // every copy it was told about and the pair meets before TMEM is freed.
@@ -28,9 +35,14 @@
 namespace pkm {
 
 namespace gp {
-constexpr int kM = 128, kN = 256, kNh = kN / 2, kKB = 64, kMaxStages = 6, kAcc = 2, kBox = 64;
+constexpr int kM = 128;             // rows per CTA (the pair covers 256)
+constexpr int kN = 256;             // columns of an instruction and a buffer
+constexpr int kNh = kN / 2;         // of them, loaded by each CTA
+constexpr int kBufs = 2;            // buffers: columns of a tile / kN
+constexpr int kTileN = kBufs * kN;
+constexpr int kKB = 64, kMaxStages = 4, kBox = 64;
 constexpr int kABytes = kM * kKB * 2, kBBytes = kNh * kKB * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kStageBytes = kABytes + kBufs * kBBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 // ring, staging of the epilogue warps, control words; the first kilobyte
@@ -88,8 +100,9 @@ __device__ __forceinline__ PairItem pair_item(const PairProbs<NP>& q, int pair, 
     const int j = iter - mine;
     if (pair >= r && j < s.extra)
       idx = j * (pairs - r) + pair - r;
-    else
-      idx = s.extra * (pairs - r) + (pair >= r ? j - s.extra : j) * pairs + pair;
+    else  // the remainder falls to the pairs from r on first
+      idx = s.extra * (pairs - r) + (pair >= r ? j - s.extra : j) * pairs +
+            (pair >= r ? pair - r : pair + pairs - r);
     if (idx >= s.n1) return PairItem{-1, 0};
     prob = q.first;
     end = NP;
@@ -115,14 +128,14 @@ __device__ __forceinline__ PairTile pair_tile(const PairProb& p, int idx) {
   const int in = rem - g * (p.group_m * p.tiles_n);
   const int gs = min(p.group_m, p.tiles_m - g * p.group_m);
   const int n = in / gs;
-  return PairTile{(int64_t)(g * p.group_m + in - n * gs) * (2 * gp::kM), n * gp::kN, z};
+  return PairTile{(int64_t)(g * p.group_m + in - n * gs) * (2 * gp::kM), n * gp::kTileN, z};
 }
 
 struct PairCtl {
   uint64_t full[gp::kMaxStages];   // leader: both CTAs' copies of a stage landed
   uint64_t empty[gp::kMaxStages];  // each CTA: the MMAs are done with a stage
-  uint64_t accf[gp::kAcc];         // each CTA: an accumulator is ready
-  uint64_t acce[gp::kAcc];         // leader: both epilogues drained an accumulator
+  uint64_t accf[gp::kBufs];        // each CTA: a buffer is ready
+  uint64_t acce[gp::kBufs];        // leader: both epilogues drained a buffer
   uint64_t epi[gp::kEpiWarps];     // an epilogue warp's own copies
   uint64_t drain;
   uint32_t tmem;
@@ -188,8 +201,45 @@ __device__ __forceinline__ void stage_ready() {
   __syncwarp();
 }
 
+// one look at a barrier's phase, without waiting
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// One lane of the (converged) warp.  The producer and the MMA issuer run their
+// loops as whole warps and only issue through this lane: their addresses and
+// descriptors are then warp-uniform values.  With the loops inside
+// `if (lane == 0)` the issuer spent 1.4 cycles for every cycle of the products
+// it issued (K = 4096: 66 % of the MMA rate).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// mbar_wait_or_abort by a whole warp, with one answer
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          int32_t* status) {
+  for (unsigned long long i = 0; i < kSpinLimit; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 255) == 255 && __any_sync(0xffffffffu, *abort != 0)) return false;
+  }
+  *abort = 1;
+  set_status(status, PKM_ERR_TIMEOUT);
+  return false;
+}
+
 struct EpiWarp {
-  int lane, half;         // half: columns 128 half .. + 127 of the tile
+  int lane, half;         // half: columns 128 half .. + 127 of a buffer
   unsigned char* stage;   // E::kWarpBytes of shared memory, 1024-byte aligned
   uint64_t* bar;          // a barrier of the warp's own, one arrival
   volatile int* abort;
@@ -199,10 +249,10 @@ struct EpiWarp {
 // E: a trivially copyable epilogue with
 //   kStages, kWarpBytes   ring stages; staging bytes per epilogue warp
 //   struct State          a warp's state over its tiles, zero-initialised
-//   begin(State&, w, prob, row0, n0, z)        before the accumulator is ready
+//   begin(State&, w, prob, row0, n0, z)        before the buffer is ready
 //   tile(State&, w, prob, row0, n0, z, tmem)   by a whole warp: rows row0 + lane,
 //       columns n0 + 128 half .. + 127 at TMEM address `tmem` (lane quarter
-//       and column included)
+//       and column included); n0 is the buffer's first column
 //   abandon(State&, w)    after an abort: lets copies in flight land
 // The accumulator itself -> the problem's output map: fp32 (stored or added
 // to; slice z is the map's third coordinate) or bf16.
@@ -272,7 +322,7 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
       mbar_init(&ctl->full[s], 1);   // the leader's producer registers both CTAs' bytes
       mbar_init(&ctl->empty[s], 1);  // the leader's commit
     }
-    for (int b = 0; b < kAcc; ++b) {
+    for (int b = 0; b < kBufs; ++b) {
       mbar_init(&ctl->accf[b], 1);
       mbar_init(&ctl->acce[b], 2 * kEpiWarps);
     }
@@ -288,7 +338,7 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
     }
   }
   if (warp == 1) {
-    tmem_alloc_pair(&ctl->tmem, kAcc * kN);
+    tmem_alloc_pair(&ctl->tmem, kTileN);
     tmem_relinquish_pair();
   }
   __syncwarp();  // the cluster barrier is warp-aligned: reconverge first
@@ -299,113 +349,164 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      uint32_t issued_mask = 0, issued_par = 0;
-      bool ok = true;
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int iter = 0; ok; ++iter) {
-        const PairItem it = pair_item(probs, pair, pairs, iter);
-        if (it.prob < 0) break;
-        const PairProb& p = probs.p[it.prob];
-        const CUtensorMap* ta = &maps.a[it.prob];
-        const CUtensorMap* tb = &maps.b[it.prob];
-        const PairTile tc = pair_tile(p, it.idx);
-        const int am = (int)(tc.m0 + (int64_t)rank * kM);  // this CTA's rows
-        const int bn = tc.n0 + (int)rank * kNh;            // this CTA's half of the columns
-        const int kb0 = tc.z * p.kb_per;
-        const int kb1 = min(kb0 + p.kb_per, (p.K + kKB - 1) / kKB);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_or_abort(&ctl->empty[stage], phase ^ 1, &ctl->abort, status)) {
-            ok = false;
-            break;
-          }
+    const bool issue = elect_one();
+    uint32_t issued_mask = 0, issued_par = 0;
+    bool ok = true;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int iter = 0; ok; ++iter) {
+      const PairItem it = pair_item(probs, pair, pairs, iter);
+      if (it.prob < 0) break;
+      const PairProb& p = probs.p[it.prob];
+      const CUtensorMap* ta = &maps.a[it.prob];
+      const CUtensorMap* tb = &maps.b[it.prob];
+      const PairTile tc = pair_tile(p, it.idx);
+      const int am = (int)(tc.m0 + (int64_t)rank * kM);  // this CTA's rows
+      const int bn = tc.n0 + (int)rank * kNh;  // this CTA's half of a buffer's columns
+      const int bufs = tc.n0 + kN < p.N ? 2 : 1;
+      const bool amn = p.amn, bmn = p.bmn;
+      const int kb0 = tc.z * p.kb_per;
+      const int kb1 = min(kb0 + p.kb_per, (p.K + kKB - 1) / kKB);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait(&ctl->empty[stage], phase ^ 1, &ctl->abort, status)) {
+          ok = false;
+          break;
+        }
+        if (issue) {
           unsigned char* sa = stages + stage * kStageBytes;
-          unsigned char* sb = sa + kABytes;
           const int kc = kb * kKB;
           const uint32_t bar = map_to(&ctl->full[stage], 0);
           // the leader registers the bytes of both CTAs' copies; a copy of
           // the partner's that lands first only takes the count below zero
-          if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * kStageBytes);
-          if (p.amn) {
+          if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * (kABytes + bufs * kBBytes));
+          if (amn) {
 #pragma unroll
             for (int j = 0; j < kM / kBox; ++j)
               tma_load_2d_pair(sa + j * kBox * 128, ta, bar, am + j * kBox, kc);
           } else {
             tma_load_2d_pair(sa, ta, bar, kc, am);
           }
-          if (p.bmn) {
+          for (int u = 0; u < bufs; ++u) {
+            unsigned char* sb = sa + kABytes + u * kBBytes;
+            const int n = bn + u * kN;
+            if (bmn) {
 #pragma unroll
-            for (int j = 0; j < kNh / kBox; ++j)
-              tma_load_2d_pair(sb + j * kBox * 128, tb, bar, bn + j * kBox, kc);
-          } else {
-            tma_load_2d_pair(sb, tb, bar, kc, bn);
-          }
-          issued_mask |= 1u << stage;
-          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
+              for (int j = 0; j < kNh / kBox; ++j)
+                tma_load_2d_pair(sb + j * kBox * 128, tb, bar, n + j * kBox, kc);
+            } else {
+              tma_load_2d_pair(sb, tb, bar, kc, n);
+            }
           }
         }
+        __syncwarp();
+        issued_mask |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
-      // on an abort the leader lets every copy it was told about land
-      if (!ok && leader) {
-        for (int s = 0; s < kStages; ++s)
-          if (issued_mask & (1u << s))
-            for (unsigned long long i = 0; i < kSpinLimit; ++i)
-              if (mbar_try_wait(&ctl->full[s], (issued_par >> s) & 1)) break;
-      }
+    }
+    // on an abort the leader lets every copy it was told about land
+    if (!ok && leader) {
+      for (int s = 0; s < kStages; ++s)
+        if (issued_mask & (1u << s))
+          for (unsigned long long i = 0; i < kSpinLimit; ++i)
+            if (mbar_try_wait(&ctl->full[s], (issued_par >> s) & 1)) break;
     }
   } else if (warp == 1) {
     // ----------------------------------------------- MMA issuer (leader)
-    if (lane == 0 && leader) {
+    if (leader) {
+      const bool issue = elect_one();
       bool ok = true;
       int stage = 0;
       uint32_t phase = 0;
+      uint32_t used0 = 0, used1 = 0;  // times each buffer was filled
       for (int iter = 0; ok; ++iter) {
         const PairItem it = pair_item(probs, pair, pairs, iter);
         if (it.prob < 0) break;
         const PairProb& p = probs.p[it.prob];
-        const uint32_t idesc = idesc_bf16_f32(2 * kM, kN) | (p.amn ? (1u << 15) : 0u) |
-                               (p.bmn ? (1u << 16) : 0u);
+        const bool amn = p.amn, bmn = p.bmn;
+        const uint32_t idesc = idesc_bf16_f32(2 * kM, kN) | (amn ? (1u << 15) : 0u) |
+                               (bmn ? (1u << 16) : 0u);
         // one 16-deep step inside a k-block: 32 bytes along a K-major row,
         // 16 lines of 128 bytes of an MN-major tile
-        const uint32_t astep = p.amn ? 2048 >> 4 : 32 >> 4, bstep = p.bmn ? 2048 >> 4 : 32 >> 4;
+        const uint32_t astep = amn ? 2048 >> 4 : 32 >> 4, bstep = bmn ? 2048 >> 4 : 32 >> 4;
         const PairTile tc = pair_tile(p, it.idx);
         const int kb0 = tc.z * p.kb_per;
         const int nkb = min(p.kb_per, (p.K + kKB - 1) / kKB - kb0);
-        const int buf = iter & 1;
-        // both epilogues have drained this accumulator's previous tile
-        if (!mbar_wait_or_abort(&ctl->acce[buf], ((iter >> 1) & 1) ^ 1, &ctl->abort, status)) {
+        const bool wide = tc.n0 + kN < p.N;
+        auto products = [&](int st, int u, bool first) {  // k-block in stage st, buffer u
+          const uint32_t sa = smem_u32(stages + st * kStageBytes);
+          const uint32_t sb = sa + kABytes + u * kBBytes;
+          const uint64_t ad = amn ? smem_desc_mn128(sa) : smem_desc_k128(sa);
+          const uint64_t bd = bmn ? smem_desc_mn128(sb) : smem_desc_k128(sb);
+#pragma unroll
+          for (int kk = 0; kk < kKB / 16; ++kk)
+            tc_mma_f16_pair(tmem + (uint32_t)(u * kN), ad + kk * astep, bd + kk * bstep, idesc,
+                            !(first && kk == 0));
+        };
+        // both epilogues have drained the first buffer's last tile
+        if (!warp_wait(&ctl->acce[0], (used0 & 1) ^ 1, &ctl->abort, status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t dt = tmem + (uint32_t)(buf * kN);
+        int back = 0, back_stage = stage;  // k-blocks the second buffer has had, its next stage
+        bool open = !wide;                 // the second buffer may be written
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait_or_abort(&ctl->full[stage], phase, &ctl->abort, status)) {
+          if (!warp_wait(&ctl->full[stage], phase, &ctl->abort, status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(stages + stage * kStageBytes);
-          const uint32_t sb = sa + kABytes;
-          const uint64_t ad = p.amn ? smem_desc_mn128(sa) : smem_desc_k128(sa);
-          const uint64_t bd = p.bmn ? smem_desc_mn128(sb) : smem_desc_k128(sb);
-#pragma unroll
-          for (int kk = 0; kk < kKB / 16; ++kk)
-            tc_mma_f16_pair(dt, ad + kk * astep, bd + kk * bstep, idesc, (kb | kk) != 0);
-          tc_commit_pair_both(&ctl->empty[stage]);  // both CTAs may refill the stage
+          if (issue) {
+            products(stage, 0, kb == 0);
+            if (kb == nkb - 1) tc_commit_pair_both(&ctl->accf[0]);
+            if (!wide) tc_commit_pair_both(&ctl->empty[stage]);  // both CTAs may refill the stage
+          }
+          __syncwarp();
+          if (wide) {
+            if (!open) {
+              // wait only when the ring is full or the tile's last k-block is in
+              const uint32_t par = (used1 & 1) ^ 1;
+              if (kb + 1 - back == kStages || kb == nkb - 1) {
+                if (!warp_wait(&ctl->acce[1], par, &ctl->abort, status)) {
+                  ok = false;
+                  break;
+                }
+                open = true;
+              } else {
+                open = __all_sync(0xffffffffu, mbar_test_wait(&ctl->acce[1], par));
+              }
+              if (open) tc_fence_after();
+            }
+            if (open)
+              for (; back <= kb; ++back) {
+                if (issue) {
+                  products(back_stage, 1, back == 0);
+                  tc_commit_pair_both(&ctl->empty[back_stage]);
+                }
+                __syncwarp();
+                if (++back_stage == kStages) back_stage = 0;
+              }
+          }
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (ok) tc_commit_pair_both(&ctl->accf[buf]);
+        if (!ok) break;
+        ++used0;
+        if (wide) {
+          if (issue) tc_commit_pair_both(&ctl->accf[1]);
+          __syncwarp();
+          ++used1;
+        }
       }
       // every MMA issued must complete before either CTA frees TMEM or exits
-      tc_commit_pair_local(&ctl->drain);
+      if (issue) tc_commit_pair_local(&ctl->drain);
+      __syncwarp();
       for (unsigned long long i = 0; i < kSpinLimit; ++i)
         if (mbar_try_wait(&ctl->drain, 0)) break;
     }
@@ -415,25 +516,33 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
     const EpiWarp w{lane, (warp - 2) >> 2, staging + (warp - 2) * E::kWarpBytes,
                     &ctl->epi[warp - 2], &ctl->abort, status};
     typename E::State state{};
-    for (int iter = 0;; ++iter) {
+    uint32_t used[kBufs] = {0, 0};
+    bool ok = true;
+    for (int iter = 0; ok; ++iter) {
       const PairItem it = pair_item(probs, pair, pairs, iter);
       if (it.prob < 0) break;
       const PairTile tc = pair_tile(probs.p[it.prob], it.idx);
       const int64_t row0 = tc.m0 + (int64_t)rank * kM + quarter * 32;
-      const int buf = iter & 1;
-      epi.begin(state, w, it.prob, row0, tc.n0, tc.z);
-      const bool got =
-          mbar_wait_or_abort(&ctl->accf[buf], (iter >> 1) & 1, &ctl->abort, status);
-      if (!__all_sync(0xffffffffu, got)) {
-        epi.abandon(state, w);
-        break;
+      const int bufs = tc.n0 + kN < probs.p[it.prob].N ? 2 : 1;
+#pragma unroll
+      for (int u = 0; u < kBufs; ++u) {
+        if (u >= bufs) break;
+        const int n0 = tc.n0 + u * kN;
+        epi.begin(state, w, it.prob, row0, n0, tc.z);
+        const bool got = mbar_wait_or_abort(&ctl->accf[u], used[u] & 1, &ctl->abort, status);
+        if (!__all_sync(0xffffffffu, got)) {
+          epi.abandon(state, w);
+          ok = false;
+          break;
+        }
+        ++used[u];
+        tc_fence_after();
+        epi.tile(state, w, it.prob, row0, n0, tc.z,
+                 tmem + ((uint32_t)(quarter * 32) << 16) + u * kN + w.half * kNh);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) remote_arrive(map_to(&ctl->acce[u], 0));
       }
-      tc_fence_after();
-      epi.tile(state, w, it.prob, row0, tc.n0, tc.z,
-               tmem + ((uint32_t)(quarter * 32) << 16) + buf * kN + w.half * kNh);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) remote_arrive(map_to(&ctl->acce[buf], 0));
     }
     if (E::kWarpBytes > 0) stage_free(lane);  // no store reads shared memory any more
   }
@@ -444,7 +553,7 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, kAcc * kN);
+  if (warp == 1) tmem_dealloc_pair(tmem, kTileN);
 }
 
 // out = the sum of nz slices of 8 n8 fp32 values, in slice order
@@ -523,7 +632,7 @@ inline PairProb pair_prob(int64_t M, int N, int K, bool amn, bool bmn, int nz = 
   p.N = N;
   p.K = K;
   p.tiles_m = (int)((M + 2 * gp::kM - 1) / (2 * gp::kM));
-  p.tiles_n = (N + gp::kN - 1) / gp::kN;
+  p.tiles_n = (N + gp::kTileN - 1) / gp::kTileN;
   p.kb_per = per;
   p.nz = (kb + per - 1) / per;
   p.amn = amn;
@@ -532,6 +641,29 @@ inline PairProb pair_prob(int64_t M, int N, int K, bool amn, bool bmn, int nz = 
   return p;
 }
 inline int64_t pair_items(const PairProb& p) { return (int64_t)p.tiles_m * p.tiles_n * p.nz; }
+
+// Pairs of SMs that the host's plans count on (148 SMs).
+constexpr int kPlanPairs = 74;
+
+// The longest pair's work, in k-blocks, when n0 items of len0 and n1 of len1
+// are dealt out as pair_item does; *extra receives the best evening-out.
+inline int64_t pair_span(int64_t n0, int64_t len0, int64_t n1, int64_t len1, int pairs,
+                         int* extra = nullptr) {
+  const int64_t r = n0 % pairs, lo = n0 / pairs;
+  int64_t best = -1;
+  for (int64_t x = 0; x <= (r && n1 ? len0 / len1 + 1 : 0); ++x) {
+    const int64_t early = x * (pairs - r) < n1 ? x * (pairs - r) : n1, rest = n1 - early;
+    const int64_t each = rest / pairs, more = rest % pairs;  // `more` pairs, from r on, take one more
+    const int64_t lo_span = lo * len0 + ((early + pairs - r - 1) / (pairs - r) + each + (more > 0)) * len1;
+    const int64_t hi_span = r ? (lo + 1) * len0 + (each + (more > pairs - r)) * len1 : 0;
+    const int64_t span = lo_span > hi_span ? lo_span : hi_span;
+    if (best < 0 || span < best) {
+      best = span;
+      if (extra) *extra = (int)x;
+    }
+  }
+  return best;
+}
 
 // Pairs that can be resident at once on the current device (0: none).  Cached
 // per kernel and device.
@@ -575,10 +707,8 @@ cudaError_t launch_pair_gemm(const PairMaps<NP>& maps, PairProbs<NP> probs, cons
   if (n0 + n1 >= (int64_t(1) << 30)) return cudaErrorInvalidValue;
   const int pairs = (int)(n0 + n1 < slots ? n0 + n1 : slots);
   probs.sched = PairSched{(int)n0, (int)n1, 0};
-  if (n1 > 0 && n0 % pairs) {
-    const int a = probs.p[0].kb_per, b = probs.p[probs.first].kb_per;
-    probs.sched.extra = (a + b / 2) / b;
-  }
+  if (n1 > 0)
+    pair_span(n0, probs.p[0].kb_per, n1, probs.p[probs.first].kb_per, pairs, &probs.sched.extra);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
   cfg.blockDim = dim3(gp::kThreads, 1, 1);

@@ -29,7 +29,7 @@ struct Memplus8Dz {
   CUtensorMap map;
   StoreOut out;
 
-  static constexpr int kStages = 6, kWarpBytes = 4096;
+  static constexpr int kStages = 4, kWarpBytes = 4096;
   struct State {};
   __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
@@ -52,7 +52,7 @@ struct Memplus8Gate {
   const uint8_t* y8;
   const float* y_scales;
 
-  static constexpr int kStages = 4, kWarpBytes = 4096 + 3 * 2048;  // 10 KiB
+  static constexpr int kStages = 3, kWarpBytes = 4096 + 3 * 2048;
   struct State {
     uint2 y[4];     // the lane's 32 bytes of the next columns
     float scale;
@@ -156,7 +156,7 @@ struct Memplus8Grads {
   CUtensorMap map[3];
   StoreOut out[3];
 
-  static constexpr int kStages = 6, kWarpBytes = 4096;
+  static constexpr int kStages = 4, kWarpBytes = 4096;
   struct State {};
   __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
@@ -174,18 +174,28 @@ struct Mp8Layout {
   int nz;
 };
 
-// Slices of the weight gradients: their tiles should give most pairs of SMs
-// one item that is not much longer than the pair's share of all products, and
-// a slice has at least 4 k-blocks.
+// Slices of the weight gradients (few tiles, a long contraction over the
+// tokens): the number whose longest pair of SMs has least to do, slices of at
+// least four k-blocks; a slice costs its sums' traffic (a k-block takes as
+// long as 4 MB of it).
 int weight_slices(int64_t T, int dm, int dv) {
   const int64_t kbT = (T + gp::kKB - 1) / gp::kKB;
-  const int64_t tw = (int64_t)((dm + 255) / 256) * ((dv + 255) / 256);
-  const int64_t share = (2 * tw * kbT + (T + 255) / 256 * ((dm + 255) / 256) *
-                                            ((dv + gp::kKB - 1) / gp::kKB)) / 74 + 1;
-  int64_t nz = (kbT + share - 1) / share;
-  if (nz > kbT / 4) nz = kbT / 4;
-  if (nz < 1) nz = 1;
-  return pair_prob(dm, dv, (int)T, true, true, (int)(nz > 64 ? 64 : nz)).nz;
+  const auto tiles = [](int64_t m, int64_t n) {
+    return (m + 255) / 256 * ((n + gp::kTileN - 1) / gp::kTileN);
+  };
+  const int64_t tw = tiles(dm, dv) + tiles(dv, dm);
+  int64_t best = -1, best_nz = 1;
+  for (int64_t nz = 1; nz <= 64 && (nz == 1 || nz * 4 <= kbT); ++nz) {
+    const int64_t per = (kbT + nz - 1) / nz, z = kbT > 0 ? (kbT + per - 1) / per : 1;
+    const int64_t cost = pair_span(tw * z, per > 0 ? per : 1, tiles(T, dm),
+                                   (dv + gp::kKB - 1) / gp::kKB, kPlanPairs) +
+                         z * 2 * dm * dv * 8 / (4 << 20);
+    if (best < 0 || cost < best) {
+      best = cost;
+      best_nz = z;
+    }
+  }
+  return (int)best_nz;
 }
 
 Mp8Layout mp8_layout(const pkm_memplus_bwd8_args* g) {

@@ -43,7 +43,7 @@ struct XentStats {
   float2* part;  // [2 * tiles_n][T]: maximum (base 2) and sum
   float* picked;
 
-  static constexpr int kStages = 6, kWarpBytes = 0;
+  static constexpr int kStages = 4, kWarpBytes = 0;
   struct State {
     int target;
   };
@@ -154,7 +154,7 @@ struct XentDelta {
   int32_t ignore;
   const float *lse, *dloss;
 
-  static constexpr int kStages = 6, kWarpBytes = 4096;
+  static constexpr int kStages = 4, kWarpBytes = 4096;
   struct State {
     int target;
     float g, l2;
@@ -215,7 +215,7 @@ struct XentGrads {
   CUtensorMap map[2];
   StoreOut out[2];
 
-  static constexpr int kStages = 6, kWarpBytes = 4096;
+  static constexpr int kStages = 4, kWarpBytes = 4096;
   struct State {};
   __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
@@ -230,8 +230,9 @@ struct XentGrads {
 bool need16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t rup(size_t x) { return (x + 255) / 256 * 256; }
 
-constexpr int64_t kPieceBytes = int64_t(256) << 20;  // most that a piece's d may take
+constexpr int64_t kPieceBytes = int64_t(512) << 20;  // most that a piece's d may take
 constexpr int kMinPiece = 1024;
+constexpr int kMaxSlices = 64;  // of dx
 
 struct XentLayout {
   size_t part, picked, fwd_total;  // forward
@@ -247,19 +248,36 @@ XentLayout xent_layout(const pkm_xent_args* a) {
   L.part = 0;
   L.picked = rup((size_t)fwd_slots(a->V) * T * sizeof(float2));
   L.fwd_total = L.picked + rup(T * 4);
-  // columns of a piece: as many as kPieceBytes holds, whole tiles
-  int64_t piece = kPieceBytes / 2 / (a->T > 0 ? a->T : 1) / gp::kN * gp::kN;
-  if (piece < kMinPiece) piece = kMinPiece;
-  if (piece > a->V) piece = a->V;
-  L.piece = (int)piece;
-  L.ld = (int)((piece + 63) / 64 * 64);
-  // few tiles of dx: slices of the piece, so that every pair of SMs has some
-  const int64_t tiles = (a->T + 255) / 256 * ((a->d + 255) / 256);
-  int64_t nz = 74 / (tiles > 0 ? tiles : 1);
-  const int64_t most = (piece + 511) / 512;
-  if (nz > most) nz = most;
-  if (nz > 16) nz = 16;
-  L.nz = pair_prob(a->T, a->d, L.piece, false, true, nz < 1 ? 1 : (int)nz).nz;
+  // Columns of a piece and slices of dx.  At least as many pieces as keep d
+  // within kPieceBytes; of the next few counts, and of slices of at least
+  // eight k-blocks, the plan whose longest pairs of SMs have least to do.  A
+  // slice costs its sums' traffic (a k-block of a 256 x 512 tile takes as long
+  // as 4 MB of memory traffic).
+  const int64_t V = a->V, Tt = a->T > 0 ? a->T : 1;
+  int64_t most = kPieceBytes / 2 / Tt / gp::kTileN * gp::kTileN;
+  if (most < kMinPiece) most = kMinPiece;
+  const int64_t fewest = (V + most - 1) / most;
+  const int64_t tm = (Tt + 255) / 256, td = (a->d + gp::kTileN - 1) / gp::kTileN;
+  const int64_t kbT = (Tt + 63) / 64, kbd = (a->d + 63) / 64;
+  int64_t best = -1;
+  for (int64_t n = fewest; n <= fewest + (V >= 8 * kMinPiece ? 3 : 0); ++n) {
+    int64_t piece = ((V + n - 1) / n + gp::kTileN - 1) / gp::kTileN * gp::kTileN;
+    if (piece > V) piece = V;
+    const int64_t pieces = (V + piece - 1) / piece, kbp = (piece + 63) / 64;
+    const int64_t delta = (tm * ((piece + gp::kTileN - 1) / gp::kTileN) + kPlanPairs - 1) /
+                          kPlanPairs * kbd;
+    for (int64_t nz = 1; nz <= kMaxSlices && (nz == 1 || nz * 8 <= kbp); ++nz) {
+      const int64_t per = (kbp + nz - 1) / nz, z = (kbp + per - 1) / per;
+      const int64_t grads = pair_span(tm * td * z, per, (piece + 255) / 256 * td, kbT, kPlanPairs);
+      const int64_t cost = pieces * (delta + grads) + pieces * z * Tt * a->d * 8 / (4 << 20);
+      if (best < 0 || cost < best) {
+        best = cost;
+        L.piece = (int)piece;
+        L.nz = (int)z;
+      }
+    }
+  }
+  L.ld = (L.piece + 63) / 64 * 64;
   L.delta = 0;
   L.dx = rup(T * (size_t)L.ld * 2);
   const bool direct = L.nz == 1 && a->grad_dtype == PKM_F32;

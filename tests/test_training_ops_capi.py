@@ -145,10 +145,10 @@ def test_xent_refuses_by_direction(lib):
         assert need > 0 and call(workspace_bytes=need - 1) == 6
         assert size(None) == 0 and size(ctypes.byref(_xent(d=60))) == 0
     assert fwd(T=0, x=None) == 0
-    # the piece of d stays within 256 MiB (or 1024 columns) however large the vocabulary
+    # the piece of d stays within 512 MiB (or 1024 columns) however large the vocabulary
     big = _xent(T=16384, V=262144, d=1024)
     need = lib.pkm_linear_xent_backward_workspace_size(ctypes.byref(big))
-    assert need <= (256 << 20) + 16384 * 1024 * 4 + 1024
+    assert need <= (512 << 20) + 4 * 16384 * 1024 * 4 + 1024
 
 
 def _mp8(**kw):
