@@ -6,23 +6,24 @@
 // through tcgen05.mma.cta_group::2: each CTA of a cluster of two loads its own
 // 128 rows of A and its own half of B (a ring of stages of 48 KiB), one
 // instruction multiplies both CTAs' operands for 256 columns, two instructions
-// a step cover the tile.  Why 512 columns: the operand stream from L2 bounds a
-// pair of SMs.  256 columns need 64 bytes per SM and cycle at the full MMA
-// rate and reached 60-65 % of it (ncu: L2 slices at 35 %, DRAM idle); 512 need
-// 48.  The accumulators then fill TMEM (two buffers of 256 columns), so a
-// tile's products cannot start before the last tile's first buffer is read:
-// the products of the first buffer run ahead by up to a ring while the
-// epilogue reads the second.
+// a step cover the tile.  Why 512 columns: 256 take 64 bytes of operands per SM
+// and cycle at the full MMA rate, about what L2 delivers; 512 take 48.  The
+// accumulators then fill TMEM (two buffers of 256 columns), so a tile's
+// products cannot start before the last tile's first buffer is read: the
+// products of the first buffer run ahead by up to a ring while the epilogue
+// reads the second.  Problems with few tiles take 256 columns a tile, to
+// spread over the SMs.
 // A or B may be held K-major ([M][K]) or MN-major ([K][M]); one launch takes up
 // to three problems, so that the tiles of several products fill the GPU
-// together.
+// together.  A dual epilogue takes two products over the same tile at once,
+// 256 columns of each, one per buffer.
 //
 //   warp 0      TMA producer of this CTA's halves
 //   warp 1      TMEM; in the leader, the MMA issuer
-//   warps 2-9   epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 (rows) of
-//               column half (w - 2) / 4 of a buffer.  Two warps per lane
-//               quarter: with one, the exponentials outlast the products of a
-//               short K.
+//   the others  E::kWarps epilogue warps: warp w reads TMEM lanes 32 (w % 4) ..
+//               + 31 (rows) of columns E::kCols ((w - 2) / 4) .. of a buffer.
+//               Eight or sixteen: an epilogue is a chain of latencies (TMEM,
+//               exponentials, staging) that only other warps cover.
 // Spin-waits are bounded as in the library's other pipelined kernels: on a
 // timeout the status word is set, the roles stop issuing, the leader waits for
 // every copy it was told about and the pair meets before TMEM is freed.
@@ -40,22 +41,29 @@ constexpr int kN = 256;             // columns of an instruction and a buffer
 constexpr int kNh = kN / 2;         // of them, loaded by each CTA
 constexpr int kBufs = 2;            // buffers: columns of a tile / kN
 constexpr int kTileN = kBufs * kN;
-constexpr int kKB = 64, kMaxStages = 4, kBox = 64;
+constexpr int kKB = 64, kMaxStages = 6, kMaxWarps = 16, kBox = 64;
 constexpr int kABytes = kM * kKB * 2, kBBytes = kNh * kKB * 2;
-constexpr int kStageBytes = kABytes + kBufs * kBBytes;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-// ring, staging of the epilogue warps, control words; the first kilobyte
-// aligns the ring (the swizzle goes by the address)
+template <class E>
+constexpr int stage_bytes() {
+  return kABytes + (E::kDual ? 1 : kBufs) * kBBytes;
+}
+template <class E>
+constexpr int threads() {
+  return 64 + 32 * E::kWarps;
+}
+// ring, staging of the epilogue warps, what they share, control words; the
+// first kilobyte aligns the ring (the swizzle goes by the address)
 template <class E>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)E::kStages * kStageBytes + (size_t)kEpiWarps * E::kWarpBytes + 256;
+  return 1024 + (size_t)E::kStages * stage_bytes<E>() + (size_t)E::kWarps * E::kWarpBytes +
+         E::kSharedBytes + 512;
 }
 }  // namespace gp
 
 struct PairProb {
   int64_t M;
   int N, K;
+  int tile_n;                        // columns of a tile: 512, or 256
   int tiles_m, tiles_n, nz, kb_per;  // nz slices of kb_per k-blocks
   int amn, bmn;                      // operand held MN-major
   int group_m;                       // tile rows walked together (operand reuse in L2)
@@ -128,7 +136,23 @@ __device__ __forceinline__ PairTile pair_tile(const PairProb& p, int idx) {
   const int in = rem - g * (p.group_m * p.tiles_n);
   const int gs = min(p.group_m, p.tiles_m - g * p.group_m);
   const int n = in / gs;
-  return PairTile{(int64_t)(g * p.group_m + in - n * gs) * (2 * gp::kM), n * gp::kTileN, z};
+  return PairTile{(int64_t)(g * p.group_m + in - n * gs) * (2 * gp::kM), n * p.tile_n, z};
+}
+
+// Buffers that a tile's products fill at a time.
+template <class E>
+__device__ __forceinline__ int pair_bufs(const PairProb& p, const PairTile& t) {
+  return !E::kDual && p.tile_n > gp::kN && t.n0 + gp::kN < p.N ? 2 : 1;
+}
+
+// The product that the producer and the MMA issuer work on in a turn: an item,
+// or with a dual epilogue each item of problem 0 and the same one of problem 1.
+template <class E, int NP>
+__device__ __forceinline__ PairItem pair_turn(const PairProbs<NP>& q, int pair, int pairs,
+                                              int iter) {
+  PairItem it = pair_item(q, pair, pairs, E::kDual ? iter >> 1 : iter);
+  if (E::kDual && it.prob >= 0) it.prob = iter & 1;
+  return it;
 }
 
 struct PairCtl {
@@ -136,7 +160,7 @@ struct PairCtl {
   uint64_t empty[gp::kMaxStages];  // each CTA: the MMAs are done with a stage
   uint64_t accf[gp::kBufs];        // each CTA: a buffer is ready
   uint64_t acce[gp::kBufs];        // leader: both epilogues drained a buffer
-  uint64_t epi[gp::kEpiWarps];     // an epilogue warp's own copies
+  uint64_t epi[4];                 // the epilogue warps' own, one per row quarter
   uint64_t drain;
   uint32_t tmem;
   volatile int abort;
@@ -239,20 +263,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 struct EpiWarp {
-  int lane, half;         // half: columns 128 half .. + 127 of a buffer
-  unsigned char* stage;   // E::kWarpBytes of shared memory, 1024-byte aligned
-  uint64_t* bar;          // a barrier of the warp's own, one arrival
+  int lane, quarter, part;  // rows 32 quarter .. + 31, columns kCols part .. of a buffer
+  unsigned char* stage;     // E::kWarpBytes of shared memory, 1024-byte aligned
+  unsigned char* shared;    // E::kSharedBytes for all epilogue warps
+  uint64_t* bars;           // one barrier per row quarter
   volatile int* abort;
   int32_t* status;
 };
 
 // E: a trivially copyable epilogue with
-//   kStages, kWarpBytes   ring stages; staging bytes per epilogue warp
+//   kWarps, kCols         8 warps of 128 columns, or 16 of 64
+//   kStages, kWarpBytes, kSharedBytes   ring stages; shared memory per warp, for all
+//   kBarArrivals          arrivals of the epilogue warps' own barriers (EpiWarp::bars)
+//   kDual                 two products over the same tile (see above)
 //   struct State          a warp's state over its tiles, zero-initialised
 //   begin(State&, w, prob, row0, n0, z)        before the buffer is ready
 //   tile(State&, w, prob, row0, n0, z, tmem)   by a whole warp: rows row0 + lane,
-//       columns n0 + 128 half .. + 127 at TMEM address `tmem` (lane quarter
-//       and column included); n0 is the buffer's first column
+//       columns n0 + kCols part .. at TMEM address `tmem` (lane quarter and
+//       column included; a dual epilogue finds the second product 256 columns
+//       further); n0 is the buffer's first column
 //   abandon(State&, w)    after an abort: lets copies in flight land
 // The accumulator itself -> the problem's output map: fp32 (stored or added
 // to; slice z is the map's third coordinate) or bf16.
@@ -262,56 +291,64 @@ struct StoreOut {
   int bf16, add;
 };
 
+template <int COLS>
 __device__ __forceinline__ void store_tile(const StoreOut& o, const CUtensorMap* map,
                                            const EpiWarp& w, int64_t row0, int n0, int z,
                                            uint32_t tmem) {
-  if (row0 >= o.rows) return;  // the whole warp
-  const int c0 = n0 + w.half * gp::kNh;
-  const int step = o.bf16 ? 64 : 32;
-  for (int q = 0; q < gp::kNh; q += step) {
-    if (c0 + q >= o.cols) break;
-    stage_free(w.lane);
-#pragma unroll 1
-    for (int h = 0; h < step / 32; ++h) {
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(tmem + q + 32 * h, r);
-      tmem_ld_wait();
-      if (o.bf16) {
-        uint32_t p[16];
+  const int c0 = n0 + w.part * COLS;
+  if (row0 >= o.rows || c0 >= o.cols) return;  // the whole warp
+  uint32_t r[2][32];
+  tmem_ld_32x32b_x32(tmem, r[0]);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          p[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-        stage_bf16(w.stage, w.lane, h, p);
-      } else {
-        stage_f32(w.stage, w.lane, r);
-      }
+  for (int q = 0; q < COLS / 32; ++q) {
+    if (c0 + 32 * q >= o.cols) break;
+    tmem_ld_wait();
+    // the next columns are on their way while these are staged
+    if (q + 1 < COLS / 32) tmem_ld_32x32b_x32(tmem + 32 * (q + 1), r[(q + 1) & 1]);
+    const uint32_t* v = r[q & 1];
+    if (o.bf16) {
+      if ((q & 1) == 0) stage_free(w.lane);
+      uint32_t p[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        p[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+      stage_bf16(w.stage, w.lane, q & 1, p);
+      if ((q & 1) == 0 && c0 + 32 * (q + 1) < o.cols) continue;
+    } else {
+      stage_free(w.lane);
+      stage_f32(w.stage, w.lane, v);
     }
     stage_ready();
     if (w.lane == 0) {
+      const int col = c0 + 32 * (o.bf16 ? q & ~1 : q);
       if (o.add)
-        tma_add_3d(map, w.stage, c0 + q, (int)row0, z);
+        tma_add_3d(map, w.stage, col, (int)row0, z);
       else
-        tma_store_3d(map, w.stage, c0 + q, (int)row0, z);
+        tma_store_3d(map, w.stage, col, (int)row0, z);
       bulk_commit();
     }
     __syncwarp();
   }
+  tmem_ld_wait();
 }
 
 template <int NP, class E>
-__global__ void __launch_bounds__(gp::kThreads, 1)
+__global__ void __launch_bounds__(gp::threads<E>(), 1)
     pair_gemm_kernel(const __grid_constant__ PairMaps<NP> maps,
                      const __grid_constant__ PairProbs<NP> probs, const __grid_constant__ E epi,
                      int32_t* status) {
   using namespace gp;
-  constexpr int kStages = E::kStages;
-  static_assert(kStages <= kMaxStages && E::kWarpBytes % 1024 == 0, "shared memory layout");
-  static_assert(sizeof(PairCtl) <= 256 && smem_bytes<E>() <= 227 * 1024, "shared memory size");
+  constexpr int kStages = E::kStages, kStageBytes = stage_bytes<E>(), kEpiWarps = E::kWarps;
+  static_assert(kStages <= kMaxStages && E::kWarpBytes % 1024 == 0 && E::kSharedBytes % 16 == 0,
+                "shared memory layout");
+  static_assert(sizeof(PairCtl) <= 512 && smem_bytes<E>() <= 227 * 1024, "shared memory size");
+  static_assert(kEpiWarps * E::kCols == 4 * kN && kEpiWarps <= kMaxWarps, "columns per warp");
   extern __shared__ unsigned char smem_raw[];
   unsigned char* stages = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* staging = stages + kStages * kStageBytes;
-  PairCtl* ctl = reinterpret_cast<PairCtl*>(staging + kEpiWarps * E::kWarpBytes);
+  unsigned char* shared = staging + kEpiWarps * E::kWarpBytes;
+  PairCtl* ctl = reinterpret_cast<PairCtl*>(shared + E::kSharedBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
@@ -326,7 +363,7 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
       mbar_init(&ctl->accf[b], 1);
       mbar_init(&ctl->acce[b], 2 * kEpiWarps);
     }
-    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&ctl->epi[w], 1);
+    for (int q = 0; q < 4; ++q) mbar_init(&ctl->epi[q], E::kBarArrivals);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     fence_barrier_init();
@@ -355,7 +392,7 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     for (int iter = 0; ok; ++iter) {
-      const PairItem it = pair_item(probs, pair, pairs, iter);
+      const PairItem it = pair_turn<E>(probs, pair, pairs, iter);
       if (it.prob < 0) break;
       const PairProb& p = probs.p[it.prob];
       const CUtensorMap* ta = &maps.a[it.prob];
@@ -363,7 +400,7 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
       const PairTile tc = pair_tile(p, it.idx);
       const int am = (int)(tc.m0 + (int64_t)rank * kM);  // this CTA's rows
       const int bn = tc.n0 + (int)rank * kNh;  // this CTA's half of a buffer's columns
-      const int bufs = tc.n0 + kN < p.N ? 2 : 1;
+      const int bufs = pair_bufs<E>(p, tc);
       const bool amn = p.amn, bmn = p.bmn;
       const int kb0 = tc.z * p.kb_per;
       const int kb1 = min(kb0 + p.kb_per, (p.K + kKB - 1) / kKB);
@@ -423,7 +460,7 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
       uint32_t phase = 0;
       uint32_t used0 = 0, used1 = 0;  // times each buffer was filled
       for (int iter = 0; ok; ++iter) {
-        const PairItem it = pair_item(probs, pair, pairs, iter);
+        const PairItem it = pair_turn<E>(probs, pair, pairs, iter);
         if (it.prob < 0) break;
         const PairProb& p = probs.p[it.prob];
         const bool amn = p.amn, bmn = p.bmn;
@@ -435,10 +472,11 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
         const PairTile tc = pair_tile(p, it.idx);
         const int kb0 = tc.z * p.kb_per;
         const int nkb = min(p.kb_per, (p.K + kKB - 1) / kKB - kb0);
-        const bool wide = tc.n0 + kN < p.N;
+        const bool wide = pair_bufs<E>(p, tc) > 1;
+        const int b0 = E::kDual ? it.prob : 0;  // the (first) buffer
         auto products = [&](int st, int u, bool first) {  // k-block in stage st, buffer u
           const uint32_t sa = smem_u32(stages + st * kStageBytes);
-          const uint32_t sb = sa + kABytes + u * kBBytes;
+          const uint32_t sb = sa + kABytes + (E::kDual ? 0 : u) * kBBytes;
           const uint64_t ad = amn ? smem_desc_mn128(sa) : smem_desc_k128(sa);
           const uint64_t bd = bmn ? smem_desc_mn128(sb) : smem_desc_k128(sb);
 #pragma unroll
@@ -446,8 +484,9 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
             tc_mma_f16_pair(tmem + (uint32_t)(u * kN), ad + kk * astep, bd + kk * bstep, idesc,
                             !(first && kk == 0));
         };
-        // both epilogues have drained the first buffer's last tile
-        if (!warp_wait(&ctl->acce[0], (used0 & 1) ^ 1, &ctl->abort, status)) {
+        // both epilogues have drained the buffer's last tile
+        const uint32_t n_used = E::kDual && b0 ? used1 : used0;
+        if (!warp_wait(&ctl->acce[b0], (n_used & 1) ^ 1, &ctl->abort, status)) {
           ok = false;
           break;
         }
@@ -461,8 +500,8 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
           }
           tc_fence_after();
           if (issue) {
-            products(stage, 0, kb == 0);
-            if (kb == nkb - 1) tc_commit_pair_both(&ctl->accf[0]);
+            products(stage, b0, kb == 0);
+            if (kb == nkb - 1) tc_commit_pair_both(&ctl->accf[b0]);
             if (!wide) tc_commit_pair_both(&ctl->empty[stage]);  // both CTAs may refill the stage
           }
           __syncwarp();
@@ -497,7 +536,10 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
           }
         }
         if (!ok) break;
-        ++used0;
+        if (b0)
+          ++used1;
+        else
+          ++used0;
         if (wide) {
           if (issue) tc_commit_pair_both(&ctl->accf[1]);
           __syncwarp();
@@ -512,24 +554,28 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
     }
   } else {
     // ----------------------------------------------------------- epilogue
-    const int quarter = warp & 3;
-    const EpiWarp w{lane, (warp - 2) >> 2, staging + (warp - 2) * E::kWarpBytes,
-                    &ctl->epi[warp - 2], &ctl->abort, status};
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
+    const EpiWarp w{lane, quarter, part, staging + (warp - 2) * E::kWarpBytes, shared,
+                    ctl->epi, &ctl->abort, status};
+    const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + part * E::kCols;
     typename E::State state{};
     uint32_t used[kBufs] = {0, 0};
     bool ok = true;
     for (int iter = 0; ok; ++iter) {
       const PairItem it = pair_item(probs, pair, pairs, iter);
       if (it.prob < 0) break;
-      const PairTile tc = pair_tile(probs.p[it.prob], it.idx);
+      const PairProb& p = probs.p[it.prob];
+      const PairTile tc = pair_tile(p, it.idx);
       const int64_t row0 = tc.m0 + (int64_t)rank * kM + quarter * 32;
-      const int bufs = tc.n0 + kN < probs.p[it.prob].N ? 2 : 1;
+      const int bufs = pair_bufs<E>(p, tc);
 #pragma unroll
       for (int u = 0; u < kBufs; ++u) {
         if (u >= bufs) break;
         const int n0 = tc.n0 + u * kN;
         epi.begin(state, w, it.prob, row0, n0, tc.z);
-        const bool got = mbar_wait_or_abort(&ctl->accf[u], used[u] & 1, &ctl->abort, status);
+        bool got = mbar_wait_or_abort(&ctl->accf[u], used[u] & 1, &ctl->abort, status);
+        if (E::kDual && got)
+          got = mbar_wait_or_abort(&ctl->accf[1], used[u] & 1, &ctl->abort, status);
         if (!__all_sync(0xffffffffu, got)) {
           epi.abandon(state, w);
           ok = false;
@@ -537,11 +583,13 @@ __global__ void __launch_bounds__(gp::kThreads, 1)
         }
         ++used[u];
         tc_fence_after();
-        epi.tile(state, w, it.prob, row0, n0, tc.z,
-                 tmem + ((uint32_t)(quarter * 32) << 16) + u * kN + w.half * kNh);
+        epi.tile(state, w, it.prob, row0, n0, tc.z, mine + u * kN);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) remote_arrive(map_to(&ctl->acce[u], 0));
+        if (lane == 0) {
+          remote_arrive(map_to(&ctl->acce[u], 0));
+          if (E::kDual) remote_arrive(map_to(&ctl->acce[1], 0));
+        }
       }
     }
     if (E::kWarpBytes > 0) stage_free(lane);  // no store reads shared memory any more
@@ -623,8 +671,15 @@ inline bool pair_out_map(CUtensorMap* m, const void* base, int64_t cols, int64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Columns of a tile: 512, or 256 where those still leave no pair of SMs more
+// than one item (twice the SMs at work on a short batch).
+inline int pair_tile_n(int64_t M, int N, int64_t nz) {
+  const int64_t items = (M + 2 * gp::kM - 1) / (2 * gp::kM) * ((N + gp::kN - 1) / gp::kN) * nz;
+  return items <= 74 ? gp::kN : gp::kTileN;
+}
+
 inline PairProb pair_prob(int64_t M, int N, int K, bool amn, bool bmn, int nz = 1,
-                          int group_m = 1) {
+                          int group_m = 1, int tile_n = 0) {
   const int kb = (K + gp::kKB - 1) / gp::kKB;
   const int per = kb > nz ? (kb + nz - 1) / nz : 1;  // every slice gets at least one k-block
   PairProb p{};
@@ -632,7 +687,8 @@ inline PairProb pair_prob(int64_t M, int N, int K, bool amn, bool bmn, int nz = 
   p.N = N;
   p.K = K;
   p.tiles_m = (int)((M + 2 * gp::kM - 1) / (2 * gp::kM));
-  p.tiles_n = (N + gp::kTileN - 1) / gp::kTileN;
+  p.tile_n = tile_n ? tile_n : pair_tile_n(M, N, nz);
+  p.tiles_n = (N + p.tile_n - 1) / p.tile_n;
   p.kb_per = per;
   p.nz = (kb + per - 1) / per;
   p.amn = amn;
@@ -645,21 +701,53 @@ inline int64_t pair_items(const PairProb& p) { return (int64_t)p.tiles_m * p.til
 // Pairs of SMs that the host's plans count on (148 SMs).
 constexpr int kPlanPairs = 74;
 
-// The longest pair's work, in k-blocks, when n0 items of len0 and n1 of len1
-// are dealt out as pair_item does; *extra receives the best evening-out.
+// A problem's item in units of one 256-column k-block: its products, and about
+// six such steps of the epilogue that nothing covers.
+inline int64_t pair_len(int64_t kb, int tile_n) { return kb * (tile_n / gp::kN) + 6; }
+
+// The longest pair's work when n0 items of len0 and n1 of len1 are dealt out
+// as pair_item does; *extra receives the best evening-out.
 inline int64_t pair_span(int64_t n0, int64_t len0, int64_t n1, int64_t len1, int pairs,
                          int* extra = nullptr) {
   const int64_t r = n0 % pairs, lo = n0 / pairs;
   int64_t best = -1;
-  for (int64_t x = 0; x <= (r && n1 ? len0 / len1 + 1 : 0); ++x) {
+  const int64_t near = r && n1 ? len0 / len1 : 0;  // about what evens a long item out
+  for (int64_t x = near > 1 ? near - 1 : 0; x <= near + (r && n1); ++x) {
     const int64_t early = x * (pairs - r) < n1 ? x * (pairs - r) : n1, rest = n1 - early;
     const int64_t each = rest / pairs, more = rest % pairs;  // `more` pairs, from r on, take one more
-    const int64_t lo_span = lo * len0 + ((early + pairs - r - 1) / (pairs - r) + each + (more > 0)) * len1;
+    const int64_t lo_span =
+        lo * len0 + ((early + pairs - r - 1) / (pairs - r) + each + (more > 0)) * len1;
     const int64_t hi_span = r ? (lo + 1) * len0 + (each + (more > pairs - r)) * len1 : 0;
     const int64_t span = lo_span > hi_span ? lo_span : hi_span;
     if (best < 0 || span < best) {
       best = span;
       if (extra) *extra = (int)x;
+    }
+  }
+  return best;
+}
+
+// How a launch of two lists is cut: the first list's `kb0` k-blocks into nz
+// slices (at most max_nz, of at least min_kb), tiles of 256 or 512 columns.
+// items0/1(tile_n): tiles of a list; slice_cost: what a slice adds, in units.
+struct PairPlan {
+  int nz = 1, tile0 = gp::kTileN, tile1 = gp::kTileN;
+  int64_t cost = -1;
+};
+template <class F0, class F1>
+inline PairPlan pair_plan(F0 items0, int64_t kb0, int max_nz, int min_kb, double slice_cost,
+                          F1 items1, int64_t kb1) {
+  PairPlan best;
+  for (int64_t nz = 1; nz <= max_nz && (nz == 1 || nz * min_kb <= kb0);
+       nz += nz < 8 ? 1 : nz < 16 ? 2 : 8) {
+    const int64_t per = kb0 > nz ? (kb0 + nz - 1) / nz : 1, z = kb0 > 0 ? (kb0 + per - 1) / per : 1;
+    if (z != nz) continue;  // the same cut as a smaller number
+    for (int t = 0; t < 4; ++t) {
+      const int t0 = t & 1 ? gp::kN : gp::kTileN, t1 = t & 2 ? gp::kN : gp::kTileN;
+      const int64_t cost =
+          pair_span(items0(t0) * z, pair_len(per, t0), items1(t1), pair_len(kb1, t1), kPlanPairs) +
+          (int64_t)(slice_cost * z);
+      if (best.cost < 0 || cost < best.cost) best = PairPlan{(int)z, t0, t1, cost};
     }
   }
   return best;
@@ -679,7 +767,7 @@ int pair_slots() {
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
-  cfg.blockDim = dim3(gp::kThreads, 1, 1);
+  cfg.blockDim = dim3(gp::threads<E>(), 1, 1);
   cfg.dynamicSmemBytes = gp::smem_bytes<E>();
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -703,15 +791,20 @@ cudaError_t launch_pair_gemm(const PairMaps<NP>& maps, PairProbs<NP> probs, cons
   const int slots = pair_slots<NP, E>();
   if (slots < 1) return cudaErrorNotSupported;
   int64_t n0 = 0, n1 = 0;
-  for (int i = 0; i < NP; ++i) (i < probs.first ? n0 : n1) += pair_items(probs.p[i]);
+  if (E::kDual)
+    n0 = pair_items(probs.p[0]);
+  else
+    for (int i = 0; i < NP; ++i) (i < probs.first ? n0 : n1) += pair_items(probs.p[i]);
   if (n0 + n1 >= (int64_t(1) << 30)) return cudaErrorInvalidValue;
   const int pairs = (int)(n0 + n1 < slots ? n0 + n1 : slots);
   probs.sched = PairSched{(int)n0, (int)n1, 0};
   if (n1 > 0)
-    pair_span(n0, probs.p[0].kb_per, n1, probs.p[probs.first].kb_per, pairs, &probs.sched.extra);
+    pair_span(n0, pair_len(probs.p[0].kb_per, probs.p[0].tile_n), n1,
+              pair_len(probs.p[probs.first].kb_per, probs.p[probs.first].tile_n), pairs,
+              &probs.sched.extra);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
-  cfg.blockDim = dim3(gp::kThreads, 1, 1);
+  cfg.blockDim = dim3(gp::threads<E>(), 1, 1);
   cfg.dynamicSmemBytes = gp::smem_bytes<E>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -6,12 +6,12 @@
 //   dW2 = z^T dout
 //
 // x is read back to bf16 (exact: 8 significant bits) for the tensor cores; y
-// is decoded where it is used.  dz is kept in fp32; the epilogue of a's
-// product reads it and writes dy, da and z, so neither a nor an elementwise
-// pass touches HBM.  da and z are rounded to bf16 once, the operand type of
-// the three products that follow; those run in one launch, the weight
-// gradients (few tiles, a long contraction over the tokens) cut into slices
-// that are summed in order.
+// is decoded where it is used.  One launch computes a and dz of the same tile,
+// each in its own accumulator, and its epilogue writes dy, da and z: neither a
+// nor dz nor an elementwise pass touches HBM.  da and z are rounded to bf16
+// once, the operand type of the three products that follow; those run in one
+// launch, the weight gradients (few tiles, a long contraction over the tokens)
+// cut into slices that are summed in order.
 // Bound by the tensor cores for long batches (10 T d_model d_v operations),
 // by launches for short ones.
 #include <math.h>
@@ -24,50 +24,27 @@ namespace pkm {
 
 namespace {
 
-// dz, fp32
-struct Memplus8Dz {
-  CUtensorMap map;
-  StoreOut out;
-
-  static constexpr int kStages = 4, kWarpBytes = 4096;
-  struct State {};
-  __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
-  __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
-  __device__ __forceinline__ void tile(State&, const EpiWarp& w, int, int64_t row0, int n0, int z,
-                                       uint32_t tmem) const {
-    store_tile(out, &map, w, row0, n0, z, tmem);
-  }
-};
-
-// a in TMEM, dz and y from memory -> dy, da, z.  A warp takes 32 columns at a
-// time: dz comes by tensor copies and the lane's bytes of y by loads, the next
-// 32 columns' as soon as these are in registers, the tile's first before its
-// products are done; the three results go out by tensor copies.  A half of
-// the tile is one quantisation group, so a lane has one scale.
+// a and dz in TMEM, y from memory -> dy, da, z, 32 columns at a time through
+// the warp's staging rows.  The lane's bytes of y for the next columns are
+// loaded while these are worked on, the tile's first before its products are
+// done; a warp's columns lie in one quantisation group, so a lane has one scale.
 struct Memplus8Gate {
-  CUtensorMap dz_map, dy_map, da_map, z_map;
+  CUtensorMap dy_map, da_map, z_map;
   int64_t T;
   int dv;
   pkm_q8 fmt;
   const uint8_t* y8;
   const float* y_scales;
 
-  static constexpr int kStages = 3, kWarpBytes = 4096 + 3 * 2048;
+  static constexpr int kWarps = 8, kCols = 128, kStages = 5, kWarpBytes = 3 * 2048;
+  static constexpr int kSharedBytes = 0, kBarArrivals = 1;
+  static constexpr bool kDual = true;
   struct State {
-    uint2 y[4];     // the lane's 32 bytes of the next columns
+    uint2 y[4];
     float scale;
-    uint32_t phase;
-    bool waiting;   // a copy of dz is in flight
-    bool dead;      // a wait ran out: no more copies
   };
 
-  __device__ __forceinline__ void fetch(State& s, const EpiWarp& w, int64_t row0, int col) const {
-    if (w.lane == 0) {
-      mbar_arrive_expect_tx(w.bar, 4096);
-      tma_load_3d(w.stage, &dz_map, w.bar, col, (int)row0, 0);
-    }
-    s.waiting = true;
-    const int64_t m = row0 + w.lane;
+  __device__ __forceinline__ void fetch(State& s, int64_t m, int col) const {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (m < T && col + 8 * u < dv)
@@ -75,48 +52,31 @@ struct Memplus8Gate {
   }
   __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int n0,
                                         int) const {
-    const int c0 = n0 + w.half * gp::kNh;
-    if (row0 >= T || c0 >= dv || s.dead) return;
-    fetch(s, w, row0, c0);
+    const int c0 = n0 + w.part * kCols;
     const int64_t m = row0 + w.lane;
-    if (m < T) s.scale = y_scales[m * q8_groups(dv) + c0 / kQ8Group];
+    if (m >= T || c0 >= dv) return;
+    s.scale = y_scales[m * q8_groups(dv) + c0 / kQ8Group];
+    fetch(s, m, c0);
   }
-  __device__ __forceinline__ void abandon(State& s, const EpiWarp& w) const {
-    if (s.waiting)
-      for (unsigned long long i = 0; i < kSpinLimit; ++i)
-        if (mbar_try_wait(w.bar, s.phase)) break;
-    s.waiting = false;
-    s.dead = true;
-  }
+  __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
 
   __device__ __forceinline__ void tile(State& s, const EpiWarp& w, int, int64_t row0, int n0, int,
                                        uint32_t tmem) const {
-    const int c0 = n0 + w.half * gp::kNh;
-    if (row0 >= T || c0 >= dv || s.dead) return;  // the whole warp
-    unsigned char* const outs = w.stage + 4096;
+    const int c0 = n0 + w.part * kCols;
+    if (row0 >= T || c0 >= dv) return;  // the whole warp
 #pragma unroll 1
-    for (int q = 0; q < gp::kNh / 32; ++q) {
+    for (int q = 0; q < kCols / 32; ++q) {
       const int col = c0 + q * 32;
       if (col >= dv) break;
-      const bool got = mbar_wait_or_abort(w.bar, s.phase, w.abort, w.status);  // dz
-      if (!__all_sync(0xffffffffu, got)) {
-        abandon(s, w);
-        return;
-      }
-      s.phase ^= 1;
-      s.waiting = false;
+      uint32_t a[32], d[32];
+      tmem_ld_32x32b_x32(tmem + q * 32, a);
+      tmem_ld_32x32b_x32(tmem + gp::kN + q * 32, d);
       uint2 yq[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) yq[u] = s.y[u];
-      uint4 d[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        d[j] = *reinterpret_cast<const uint4*>(w.stage + w.lane * 128 + ((j ^ (w.lane & 7)) << 4));
-      uint32_t r[32];
-      tmem_ld_32x32b_x32(tmem + q * 32, r);
+      if (q + 1 < kCols / 32) fetch(s, row0 + w.lane, col + 32);
+      __syncwarp();  // the wait is warp-aligned
       tmem_ld_wait();
-      __syncwarp();  // every lane has its dz: the buffer may be filled again
-      if (q + 1 < gp::kNh / 32 && col + 32 < dv) fetch(s, w, row0, col + 32);
       stage_free(w.lane);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -124,26 +84,23 @@ struct Memplus8Gate {
         q8_decode(yq[u], s.scale, fmt, y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const uint4& dq = d[2 * u + (e >> 2)];
-          const float dzv = __uint_as_float((e & 3) == 0 ? dq.x : (e & 3) == 1 ? dq.y
-                                                                : (e & 3) == 2 ? dq.z : dq.w);
-          const float a = __uint_as_float(r[8 * u + e]);
-          const float sg = __fdividef(1.0f, 1.0f + __expf(-a));
-          const float g = a * sg;
-          o[0][e] = dzv * g;
-          o[1][e] = dzv * y[e] * fmaf(g, 1.0f - sg, sg);
+          const float av = __uint_as_float(a[8 * u + e]), dz = __uint_as_float(d[8 * u + e]);
+          const float sg = __fdividef(1.0f, 1.0f + __expf(-av));
+          const float g = av * sg;
+          o[0][e] = dz * g;
+          o[1][e] = dz * y[e] * fmaf(g, 1.0f - sg, sg);
           o[2][e] = y[e] * g;
         }
 #pragma unroll
         for (int k = 0; k < 3; ++k)
-          *reinterpret_cast<uint4*>(stage64_at(outs + k * 2048, w.lane, u)) =
+          *reinterpret_cast<uint4*>(stage64_at(w.stage + k * 2048, w.lane, u)) =
               pack16<PKM_BF16>(o[k]);
       }
       stage_ready();
       if (w.lane == 0) {
-        tma_store_3d(&dy_map, outs, col, (int)row0, 0);
-        tma_store_3d(&da_map, outs + 2048, col, (int)row0, 0);
-        tma_store_3d(&z_map, outs + 4096, col, (int)row0, 0);
+        tma_store_3d(&dy_map, w.stage, col, (int)row0, 0);
+        tma_store_3d(&da_map, w.stage + 2048, col, (int)row0, 0);
+        tma_store_3d(&z_map, w.stage + 4096, col, (int)row0, 0);
         bulk_commit();
       }
       __syncwarp();
@@ -156,13 +113,15 @@ struct Memplus8Grads {
   CUtensorMap map[3];
   StoreOut out[3];
 
-  static constexpr int kStages = 4, kWarpBytes = 4096;
+  static constexpr int kWarps = 8, kCols = 128, kStages = 4, kWarpBytes = 4096, kSharedBytes = 0;
+  static constexpr int kBarArrivals = 1;
+  static constexpr bool kDual = false;
   struct State {};
   __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
   __device__ __forceinline__ void tile(State&, const EpiWarp& w, int prob, int64_t row0, int n0,
                                        int z, uint32_t tmem) const {
-    store_tile(out[prob], &map[prob], w, row0, n0, z, tmem);
+    store_tile<kCols>(out[prob], &map[prob], w, row0, n0, z, tmem);
   }
 };
 
@@ -170,32 +129,19 @@ bool need16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) 
 size_t rup(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Mp8Layout {
-  size_t xb, dz, da, z, w1, w2, total;
+  size_t xb, da, z, w1, w2, total;
   int nz;
+  PairPlan plan;
 };
 
-// Slices of the weight gradients (few tiles, a long contraction over the
-// tokens): the number whose longest pair of SMs has least to do, slices of at
-// least four k-blocks; a slice costs its sums' traffic (a k-block takes as
-// long as 4 MB of it).
-int weight_slices(int64_t T, int dm, int dv) {
-  const int64_t kbT = (T + gp::kKB - 1) / gp::kKB;
-  const auto tiles = [](int64_t m, int64_t n) {
-    return (m + 255) / 256 * ((n + gp::kTileN - 1) / gp::kTileN);
-  };
-  const int64_t tw = tiles(dm, dv) + tiles(dv, dm);
-  int64_t best = -1, best_nz = 1;
-  for (int64_t nz = 1; nz <= 64 && (nz == 1 || nz * 4 <= kbT); ++nz) {
-    const int64_t per = (kbT + nz - 1) / nz, z = kbT > 0 ? (kbT + per - 1) / per : 1;
-    const int64_t cost = pair_span(tw * z, per > 0 ? per : 1, tiles(T, dm),
-                                   (dv + gp::kKB - 1) / gp::kKB, kPlanPairs) +
-                         z * 2 * dm * dv * 8 / (4 << 20);
-    if (best < 0 || cost < best) {
-      best = cost;
-      best_nz = z;
-    }
-  }
-  return (int)best_nz;
+// The weight gradients have few tiles and a long contraction over the tokens:
+// cut into slices of at least four k-blocks (a unit of the plan takes as long
+// as 2 MB of the slices' traffic).
+PairPlan grads_plan(int64_t T, int dm, int dv) {
+  const auto tiles = [](int64_t m, int64_t n, int tn) { return (m + 255) / 256 * ((n + tn - 1) / tn); };
+  return pair_plan([&](int tn) { return tiles(dm, dv, tn) + tiles(dv, dm, tn); },
+                   (T + gp::kKB - 1) / gp::kKB, 64, 4, 2.0 * dm * dv * 8 / (2 << 20),
+                   [&](int tn) { return tiles(T, dm, tn); }, (dv + gp::kKB - 1) / gp::kKB);
 }
 
 Mp8Layout mp8_layout(const pkm_memplus_bwd8_args* g) {
@@ -207,9 +153,9 @@ Mp8Layout mp8_layout(const pkm_memplus_bwd8_args* g) {
     off += rup(b);
     return o;
   };
-  L.nz = weight_slices(g->T, g->d_model, g->d_v);
+  L.plan = grads_plan(g->T, g->d_model, g->d_v);
+  L.nz = L.plan.nz;
   L.xb = take(T * dm * 2);
-  L.dz = take(T * dv * 4);
   L.da = take(T * dv * 2);
   L.z = take(T * dv * 2);
   const bool direct = L.nz == 1 && g->grad_dtype == PKM_F32;
@@ -231,7 +177,7 @@ pkm_status mp8_sizes(const pkm_memplus_bwd8_args* g) {
   return PKM_OK;
 }
 
-pkm_status mp8_validate(const pkm_memplus_bwd8_args* g) {
+pkm_status mp8_validate(const pkm_memplus_bwd8_args* g, Mp8Layout* L) {
   const pkm_status s = mp8_sizes(g);
   if (s != PKM_OK) return s;
   if (!need16(g->dW1) || !need16(g->dW2)) return PKM_ERR_INVALID_ARG;
@@ -239,7 +185,8 @@ pkm_status mp8_validate(const pkm_memplus_bwd8_args* g) {
   const void* need[] = {g->x8, g->x_scales, g->W1, g->W2, g->y8, g->y_scales, g->dout, g->dy, g->dx};
   for (const void* p : need)
     if (!need16(p)) return PKM_ERR_INVALID_ARG;
-  if (!need16(g->workspace) || g->workspace_bytes < mp8_layout(g).total)
+  *L = mp8_layout(g);
+  if (!need16(g->workspace) || g->workspace_bytes < L->total)
     return PKM_ERR_WORKSPACE;
   return PKM_OK;
 }
@@ -251,40 +198,30 @@ pkm_status mp8_validate(const pkm_memplus_bwd8_args* g) {
     note_launch();                    \
   } while (0)
 
-cudaError_t memplus8_backward(const pkm_memplus_bwd8_args* g, int32_t* status, cudaStream_t st) {
-  const Mp8Layout L = mp8_layout(g);
+cudaError_t memplus8_backward(const pkm_memplus_bwd8_args* g, const Mp8Layout& L, int32_t* status,
+                              cudaStream_t st) {
   char* ws = static_cast<char*>(g->workspace);
   const int64_t T = g->T;
   const int dm = g->d_model, dv = g->d_v;
   auto* xb = reinterpret_cast<__nv_bfloat16*>(ws + L.xb);
-  auto* dz = reinterpret_cast<float*>(ws + L.dz);
   auto* da = reinterpret_cast<__nv_bfloat16*>(ws + L.da);
   auto* z = reinterpret_cast<__nv_bfloat16*>(ws + L.z);
   cudaError_t e = launch_act8_load(g->x8, g->x_scales, T, dm, g->fmt, xb, PKM_BF16, st);
   if (e != cudaSuccess) return e;
-  {  // dz = dout W2^T
-    PairMaps<1> m;
-    if (!pair_map(&m.a[0], g->dout, T, dm, dm, false) ||
-        !pair_map(&m.b[0], g->W2, dv, dm, dm, false))
+  {  // a = x W1 and dz = dout W2^T, and everything elementwise
+    PairMaps<2> m;
+    if (!pair_map(&m.a[0], xb, T, dm, dm, false) || !pair_map(&m.b[0], g->W1, dv, dm, dv, true) ||
+        !pair_map(&m.a[1], g->dout, T, dm, dm, false) ||
+        !pair_map(&m.b[1], g->W2, dv, dm, dm, false))
       return cudaErrorInvalidValue;
-    const PairProbs<1> p{{pair_prob(T, dv, dm, false, false)}, 1, {}};
-    Memplus8Dz epi{{}, {T, dv, 0, 0}};
-    if (!pair_out_map(&epi.map, dz, dv, T, 1, dv, PKM_F32)) return cudaErrorInvalidValue;
-    PKM_TRY((launch_pair_gemm<1>(m, p, epi, status, st)));
-  }
-  {  // a = x W1 and everything elementwise
-    PairMaps<1> m;
-    if (!pair_map(&m.a[0], xb, T, dm, dm, false) || !pair_map(&m.b[0], g->W1, dv, dm, dv, true))
-      return cudaErrorInvalidValue;
-    const PairProbs<1> p{{pair_prob(T, dv, dm, false, true)}, 1, {}};
-    Memplus8Gate epi{{}, {}, {}, {}, T, dv, g->fmt, static_cast<const uint8_t*>(g->y8),
-                     g->y_scales};
-    if (!pair_out_map(&epi.dz_map, dz, dv, T, 1, dv, PKM_F32) ||
-        !pair_out_map(&epi.dy_map, g->dy, dv, T, 1, dv, PKM_BF16, true) ||
+    const PairProbs<2> p{{pair_prob(T, dv, dm, false, true, 1, 1, gp::kN),
+                          pair_prob(T, dv, dm, false, false, 1, 1, gp::kN)}, 2, {}};
+    Memplus8Gate epi{{}, {}, {}, T, dv, g->fmt, static_cast<const uint8_t*>(g->y8), g->y_scales};
+    if (!pair_out_map(&epi.dy_map, g->dy, dv, T, 1, dv, PKM_BF16, true) ||
         !pair_out_map(&epi.da_map, da, dv, T, 1, dv, PKM_BF16, true) ||
         !pair_out_map(&epi.z_map, z, dv, T, 1, dv, PKM_BF16, true))
       return cudaErrorInvalidValue;
-    PKM_TRY((launch_pair_gemm<1>(m, p, epi, status, st)));
+    PKM_TRY((launch_pair_gemm<2>(m, p, epi, status, st)));
   }
   const bool gb = g->grad_dtype == PKM_BF16;
   const bool direct = L.nz == 1 && !gb;
@@ -297,9 +234,9 @@ cudaError_t memplus8_backward(const pkm_memplus_bwd8_args* g, int32_t* status, c
         !pair_map(&m.b[1], g->dout, dm, (int)T, dm, true) ||
         !pair_map(&m.a[2], da, T, dv, dv, false) || !pair_map(&m.b[2], g->W1, dm, dv, dv, false))
       return cudaErrorInvalidValue;
-    const PairProbs<3> p{{pair_prob(dm, dv, (int)T, true, true, L.nz),
-                          pair_prob(dv, dm, (int)T, true, true, L.nz),
-                          pair_prob(T, dm, dv, false, false)}, 2, {}};
+    const PairProbs<3> p{{pair_prob(dm, dv, (int)T, true, true, L.nz, 1, L.plan.tile0),
+                          pair_prob(dv, dm, (int)T, true, true, L.nz, 1, L.plan.tile0),
+                          pair_prob(T, dm, dv, false, false, 1, 1, L.plan.tile1)}, 2, {}};
     Memplus8Grads epi{{}, {{dm, dv, 0, 0}, {dv, dm, 0, 0}, {T, dm, gb, 0}}};
     if (!pair_out_map(&epi.map[0], w1, dv, dm, L.nz, dv, PKM_F32) ||
         !pair_out_map(&epi.map[1], w2, dm, dv, L.nz, dm, PKM_F32) ||
@@ -326,7 +263,8 @@ PKM_API size_t pkm_memplus_backward_act8_workspace_size(const pkm_memplus_bwd8_a
 
 PKM_API pkm_status pkm_memplus_backward_act8(const pkm_memplus_bwd8_args* g,
                                              pkm_stream_t stream) {
-  const pkm_status s = mp8_validate(g);
+  Mp8Layout L{};
+  const pkm_status s = mp8_validate(g, &L);
   if (s != PKM_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (g->T == 0) {
@@ -338,7 +276,7 @@ PKM_API pkm_status pkm_memplus_backward_act8(const pkm_memplus_bwd8_args* g,
   }
   int32_t* status = status_ptr();
   if (!status) return PKM_ERR_CUDA;
-  return memplus8_backward(g, status, st) == cudaSuccess ? PKM_OK : PKM_ERR_CUDA;
+  return memplus8_backward(g, L, status, st) == cudaSuccess ? PKM_OK : PKM_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -6,9 +6,9 @@
 //   d[t, v] = (exp(logit[t, v] - lse[t]) - [v = target[t]]) dloss[t]
 //   dx = d W,  dW = d^T x
 //
-// Forward: the logits live in TMEM only.  Each 256 x 256 tile's epilogue
-// reduces its columns to a running maximum and sum per row (two column halves
-// of 128), a small kernel joins the partials.  Base 2 throughout: with
+// Forward: the logits live in TMEM only.  Each tile's epilogue
+// reduces its columns to a running maximum and sum per row, a small kernel
+// joins the tiles' partials.  Base 2 throughout: with
 // s = logit log2(e), a term is 2^(s - max) -- one multiply-add and one ex2 --
 // and the rounding of log2(e) scales every term alike (1.3e-8 of the logit).
 // Backward: d for a piece of the vocabulary (recomputed logits, rounded to
@@ -34,79 +34,108 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Row maximum and sum of a tile's column half -> part[slot][row], and the
-// target's logit.
+struct MaxSum {  // of terms 2^s: the maximum and the sum of 2^(s - maximum)
+  float mx, sum;
+  __device__ __forceinline__ void join(float qm, float qs) {
+    const float nm = fmaxf(mx, qm);
+    const float ref = nm == -INFINITY ? 0.f : nm;  // all -inf so far: every term is 0
+    sum = sum * ex2(mx - ref) + qs * ex2(qm - ref);
+    mx = nm;
+  }
+};
+
+// Row maximum and sum of a tile -> part[tile column][row], and the target's
+// logit.  A lane carries its row over the tile's two buffers; the four warps of
+// a row quarter join theirs through shared memory.
 struct XentStats {
   int64_t T;
-  int V;
+  int V, tile_n;
   const int32_t* target;
-  float2* part;  // [2 * tiles_n][T]: maximum (base 2) and sum
+  float2* part;  // [tiles_n][T]
   float* picked;
 
-  static constexpr int kStages = 4, kWarpBytes = 0;
+  static constexpr int kWarps = 16, kCols = 64, kStages = 4, kWarpBytes = 0;
+  static constexpr int kSharedBytes = 2 * 4 * 128 * sizeof(float2), kBarArrivals = 4;
+  static constexpr bool kDual = false;
   struct State {
     int target;
+    MaxSum v;
+    int turn;
   };
-  __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int,
+  __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int n0,
                                         int) const {
+    if (n0 % tile_n) return;  // the tile's second buffer
     s.target = row0 + w.lane < T ? target[row0 + w.lane] : -1;
+    s.v = MaxSum{-INFINITY, 0.f};
   }
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
 
+  __device__ __forceinline__ void columns(State& st, int64_t m, int col, uint32_t* r) const {
+    if (col + 32 > V) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col + j >= V) r[j] = 0xff800000u;  // -inf: no such column
+    }
+    float top[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top[j] = __uint_as_float(r[j]);
+#pragma unroll
+    for (int j = 4; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(r[j]));
+    const float all = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    const float nm = fmaxf(st.v.mx, all * kLog2e);
+    const float ref = nm == -INFINITY ? 0.f : nm;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
+    st.v.sum = fmaf(st.v.sum, ex2(st.v.mx - ref), (s[0] + s[1]) + (s[2] + s[3]));
+    st.v.mx = nm;
+    const uint32_t at = (uint32_t)st.target - (uint32_t)col;
+    if (at < 32u) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (at == j) picked[m] = __uint_as_float(r[j]);
+    }
+  }
+
   __device__ __forceinline__ void tile(State& st, const EpiWarp& w, int, int64_t row0, int n0,
                                        int, uint32_t tmem) const {
-    if (row0 >= T) return;  // the whole warp
     const int64_t m = row0 + w.lane;
-    const int t = st.target;
-    float mx = -INFINITY, sum = 0.f;
-    const int c0 = n0 + w.half * gp::kNh;
-#pragma unroll 1
-    for (int g = 0; g < gp::kNh / 32; ++g) {
-      const int col = c0 + g * 32;
-      if (col >= V) break;
-      uint32_t r[32];
-      __syncwarp();  // the load is warp-aligned
-      tmem_ld_32x32b_x32(tmem + g * 32, r);
+    const int c0 = n0 + w.part * kCols;
+    if (row0 < T && c0 < V) {
+      uint32_t a[32], b[32];
+      tmem_ld_32x32b_x32(tmem, a);
       tmem_ld_wait();
-      if (col + 32 > V) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (col + j >= V) r[j] = 0xff800000u;  // -inf: no such column
-      }
-      float top = __uint_as_float(r[0]);
-#pragma unroll
-      for (int j = 1; j < 32; ++j) top = fmaxf(top, __uint_as_float(r[j]));
-      const float nm = fmaxf(mx, top * kLog2e);
-      const float ref = nm == -INFINITY ? 0.f : nm;  // all -inf so far: every term is 0
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
-      sum = fmaf(sum, ex2(mx - ref), (s[0] + s[1]) + (s[2] + s[3]));
-      mx = nm;
-      const uint32_t at = (uint32_t)t - (uint32_t)col;
-      if (at < 32u) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (at == j) picked[m] = __uint_as_float(r[j]);
-      }
+      tmem_ld_32x32b_x32(tmem + 32, b);  // on its way while the first columns are summed
+      columns(st, m, c0, a);
+      __syncwarp();  // the wait is warp-aligned
+      tmem_ld_wait();
+      if (c0 + 32 < V) columns(st, m, c0 + 32, b);
     }
-    if (m < T) part[(int64_t)(c0 / gp::kNh) * T + m] = make_float2(mx, sum);
+    if (n0 % tile_n + gp::kN < tile_n && n0 + gp::kN < V) return;  // the second buffer follows
+    __syncwarp();
+    // two sets of slots in turn: a set is written again only after the tile in
+    // between, whose buffers the joining warp has handed back after its reads
+    float2* slot = reinterpret_cast<float2*>(w.shared) + (st.turn & 1) * 4 * 128;
+    slot[w.part * 128 + w.quarter * 32 + w.lane] = make_float2(st.v.mx, st.v.sum);
+    __syncwarp();
+    if (w.lane == 0) mbar_arrive(&w.bars[w.quarter]);
+    const uint32_t parity = st.turn & 1;
+    st.turn ^= 1;
+    if (w.part != 0) return;
+    if (mbar_wait_or_abort(&w.bars[w.quarter], parity, w.abort, w.status) && m < T) {
+      for (int k = 1; k < 4; ++k) {
+        const float2 q = slot[k * 128 + w.quarter * 32 + w.lane];
+        st.v.join(q.x, q.y);
+      }
+      part[(int64_t)(n0 / tile_n) * T + m] = make_float2(st.v.mx, st.v.sum);
+    }
+    __syncwarp();
   }
 };
 
 // lse and loss from the partials: 8 rows per block, 64 strips of partials (a
 // warp reads 8 rows of 4 strips), joined over the warp, then over the warps.
 constexpr int kJoinRows = 8, kJoinThreads = 512;
-
-struct MaxSum {
-  float mx, sum;
-  __device__ __forceinline__ void join(float qm, float qs) {
-    const float nm = fmaxf(mx, qm);
-    const float ref = nm == -INFINITY ? 0.f : nm;
-    sum = sum * ex2(mx - ref) + qs * ex2(qm - ref);
-    mx = nm;
-  }
-};
 
 __global__ void __launch_bounds__(kJoinThreads) xent_join_kernel(
     const float2* __restrict__ part, int slots, int64_t T, int V,
@@ -154,13 +183,15 @@ struct XentDelta {
   int32_t ignore;
   const float *lse, *dloss;
 
-  static constexpr int kStages = 4, kWarpBytes = 4096;
+  static constexpr int kWarps = 16, kCols = 64, kStages = 4, kWarpBytes = 2048, kSharedBytes = 0;
+  static constexpr int kBarArrivals = 1;
+  static constexpr bool kDual = false;
   struct State {
     int target;
     float g, l2;
     bool counted;
   };
-  __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int,
+  __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int n0,
                                         int) const {
     const int64_t m = row0 + w.lane;
     s.target = m < T ? target[m] : ignore;
@@ -170,42 +201,45 @@ struct XentDelta {
   }
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
 
+  __device__ __forceinline__ void columns(const State& s, const EpiWarp& w, int64_t row0, int col,
+                                          const uint32_t* r) const {
+    float p[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) p[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -s.l2));
+    const uint32_t at = (uint32_t)s.target - (uint32_t)(v0 + col);
+    if (at < 32u) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (at == j) p[j] -= 1.f;
+    }
+    uint32_t o[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      o[j] = s.counted ? pack_bf16x2(p[2 * j] * s.g, p[2 * j + 1] * s.g) : 0u;
+    stage_free(w.lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(stage64_at(w.stage, w.lane, j)) =
+          make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    stage_ready();
+    if (w.lane == 0) {
+      tma_store_3d(&out, w.stage, col, (int)row0, 0);
+      bulk_commit();
+    }
+    __syncwarp();
+  }
+
   __device__ __forceinline__ void tile(State& s, const EpiWarp& w, int, int64_t row0, int n0, int,
                                        uint32_t tmem) const {
-    if (row0 >= T) return;  // the whole warp
-    const int c0 = n0 + w.half * gp::kNh;
-#pragma unroll 1
-    for (int q = 0; q < gp::kNh; q += 32) {
-      const int col = c0 + q;
-      if (col >= Vp) break;
-      uint32_t r[32];
-      __syncwarp();  // the load is warp-aligned
-      tmem_ld_32x32b_x32(tmem + q, r);
-      tmem_ld_wait();
-      float p[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) p[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -s.l2));
-      const uint32_t at = (uint32_t)s.target - (uint32_t)(v0 + col);
-      if (at < 32u) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (at == j) p[j] -= 1.f;
-      }
-      uint32_t o[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        o[j] = s.counted ? pack_bf16x2(p[2 * j] * s.g, p[2 * j + 1] * s.g) : 0u;
-      const int h = (q >> 5) & 1;
-      if (h == 0) stage_free(w.lane);
-      stage_bf16(w.stage, w.lane, h, o);
-      if (h == 1 || col + 32 >= Vp) {
-        stage_ready();
-        if (w.lane == 0) {
-          tma_store_3d(&out, w.stage, col - 32 * h, (int)row0, 0);
-          bulk_commit();
-        }
-      }
-    }
+    const int c0 = n0 + w.part * kCols;
+    if (row0 >= T || c0 >= Vp) return;  // the whole warp
+    uint32_t a[32], b[32];
+    tmem_ld_32x32b_x32(tmem, a);
+    tmem_ld_wait();
+    tmem_ld_32x32b_x32(tmem + 32, b);  // on its way while the first columns are worked on
+    columns(s, w, row0, c0, a);
+    tmem_ld_wait();
+    if (c0 + 32 < Vp) columns(s, w, row0, c0 + 32, b);
   }
 };
 
@@ -215,13 +249,15 @@ struct XentGrads {
   CUtensorMap map[2];
   StoreOut out[2];
 
-  static constexpr int kStages = 4, kWarpBytes = 4096;
+  static constexpr int kWarps = 8, kCols = 128, kStages = 4, kWarpBytes = 4096, kSharedBytes = 0;
+  static constexpr int kBarArrivals = 1;
+  static constexpr bool kDual = false;
   struct State {};
   __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
   __device__ __forceinline__ void tile(State&, const EpiWarp& w, int prob, int64_t row0, int n0,
                                        int z, uint32_t tmem) const {
-    store_tile(out[prob], &map[prob], w, row0, n0, z, tmem);
+    store_tile<kCols>(out[prob], &map[prob], w, row0, n0, z, tmem);
   }
 };
 
@@ -234,54 +270,53 @@ constexpr int64_t kPieceBytes = int64_t(512) << 20;  // most that a piece's d ma
 constexpr int kMinPiece = 1024;
 constexpr int kMaxSlices = 64;  // of dx
 
-struct XentLayout {
-  size_t part, picked, fwd_total;  // forward
-  int piece, ld, nz;
-  size_t delta, dx, bwd_total;     // backward
+struct XentLayout {  // of the backward
+  int piece, ld, nz, tile_dx, tile_dw;
+  size_t delta, dx, total;
 };
 
-int fwd_slots(int V) { return 2 * ((V + gp::kN - 1) / gp::kN); }
+PairProb fwd_prob(const pkm_xent_args* a) {
+  return pair_prob(a->T, a->V, a->d, false, false, 1, 8);
+}
 
 XentLayout xent_layout(const pkm_xent_args* a) {
   XentLayout L{};
   const size_t T = (size_t)a->T;
-  L.part = 0;
-  L.picked = rup((size_t)fwd_slots(a->V) * T * sizeof(float2));
-  L.fwd_total = L.picked + rup(T * 4);
-  // Columns of a piece and slices of dx.  At least as many pieces as keep d
-  // within kPieceBytes; of the next few counts, and of slices of at least
-  // eight k-blocks, the plan whose longest pairs of SMs have least to do.  A
-  // slice costs its sums' traffic (a k-block of a 256 x 512 tile takes as long
-  // as 4 MB of memory traffic).
+  // Columns of a piece and slices of dx: at least as many pieces as keep d
+  // within kPieceBytes, of the next few counts the plan whose longest pairs of
+  // SMs have least to do.  A slice costs its sums' traffic (a unit of the
+  // plans takes as long as 2 MB of it).
   const int64_t V = a->V, Tt = a->T > 0 ? a->T : 1;
   int64_t most = kPieceBytes / 2 / Tt / gp::kTileN * gp::kTileN;
   if (most < kMinPiece) most = kMinPiece;
   const int64_t fewest = (V + most - 1) / most;
-  const int64_t tm = (Tt + 255) / 256, td = (a->d + gp::kTileN - 1) / gp::kTileN;
-  const int64_t kbT = (Tt + 63) / 64, kbd = (a->d + 63) / 64;
-  int64_t best = -1;
-  for (int64_t n = fewest; n <= fewest + (V >= 8 * kMinPiece ? 3 : 0); ++n) {
+  const auto tiles = [](int64_t m, int64_t n, int tn) { return (m + 255) / 256 * ((n + tn - 1) / tn); };
+  double best = -1;
+  // (a short batch's products take less time than weighing more plans)
+  for (int64_t n = fewest; n <= fewest + (Tt >= 1024 && V >= 8 * kMinPiece ? 3 : 0); ++n) {
     int64_t piece = ((V + n - 1) / n + gp::kTileN - 1) / gp::kTileN * gp::kTileN;
     if (piece > V) piece = V;
-    const int64_t pieces = (V + piece - 1) / piece, kbp = (piece + 63) / 64;
-    const int64_t delta = (tm * ((piece + gp::kTileN - 1) / gp::kTileN) + kPlanPairs - 1) /
-                          kPlanPairs * kbd;
-    for (int64_t nz = 1; nz <= kMaxSlices && (nz == 1 || nz * 8 <= kbp); ++nz) {
-      const int64_t per = (kbp + nz - 1) / nz, z = (kbp + per - 1) / per;
-      const int64_t grads = pair_span(tm * td * z, per, (piece + 255) / 256 * td, kbT, kPlanPairs);
-      const int64_t cost = pieces * (delta + grads) + pieces * z * Tt * a->d * 8 / (4 << 20);
-      if (best < 0 || cost < best) {
-        best = cost;
-        L.piece = (int)piece;
-        L.nz = (int)z;
-      }
+    const int64_t pieces = (V + piece - 1) / piece;
+    const int64_t delta = (tiles(Tt, piece, gp::kTileN) + kPlanPairs - 1) / kPlanPairs *
+                          pair_len((a->d + 63) / 64, gp::kTileN);
+    const PairPlan plan = pair_plan(
+        [&](int tn) { return tiles(Tt, a->d, tn); }, (piece + 63) / 64, kMaxSlices, 8,
+        (double)Tt * a->d * 8 / (2 << 20), [&](int tn) { return tiles(piece, a->d, tn); },
+        (Tt + 63) / 64);
+    const double cost = (double)pieces * (delta + plan.cost + 8);  // two launches a piece
+    if (best < 0 || cost < best) {
+      best = cost;
+      L.piece = (int)piece;
+      L.nz = plan.nz;
+      L.tile_dx = plan.tile0;
+      L.tile_dw = plan.tile1;
     }
   }
   L.ld = (L.piece + 63) / 64 * 64;
   L.delta = 0;
   L.dx = rup(T * (size_t)L.ld * 2);
   const bool direct = L.nz == 1 && a->grad_dtype == PKM_F32;
-  L.bwd_total = L.dx + (direct ? 0 : rup((size_t)L.nz * T * (size_t)a->d * 4));
+  L.total = L.dx + (direct ? 0 : rup((size_t)L.nz * T * (size_t)a->d * 4));
   return L;
 }
 
@@ -297,7 +332,14 @@ pkm_status xent_sizes(const pkm_xent_args* a) {
   return PKM_OK;
 }
 
-pkm_status xent_validate(const pkm_xent_args* a, bool backward) {
+size_t fwd_bytes(const pkm_xent_args* a, size_t* picked) {
+  const size_t at = rup((size_t)fwd_prob(a).tiles_n * (size_t)a->T * sizeof(float2));
+  if (picked) *picked = at;
+  return at + rup((size_t)a->T * 4);
+}
+
+pkm_status xent_validate(const pkm_xent_args* a, XentLayout* L) {  // L: of the backward
+  const bool backward = L != nullptr;
   const pkm_status s = xent_sizes(a);
   if (s != PKM_OK) return s;
   if (backward && !need16(a->dW)) return PKM_ERR_INVALID_ARG;
@@ -306,8 +348,9 @@ pkm_status xent_validate(const pkm_xent_args* a, bool backward) {
     return PKM_ERR_INVALID_ARG;
   if (!backward && !need16(a->loss)) return PKM_ERR_INVALID_ARG;
   if (backward && (!need16(a->dloss) || !need16(a->dx))) return PKM_ERR_INVALID_ARG;
-  const XentLayout L = xent_layout(a);
-  if (!need16(a->workspace) || a->workspace_bytes < (backward ? L.bwd_total : L.fwd_total))
+  if (backward) *L = xent_layout(a);
+  if (!need16(a->workspace) ||
+      a->workspace_bytes < (backward ? L->total : fwd_bytes(a, nullptr)))
     return PKM_ERR_WORKSPACE;
   return PKM_OK;
 }
@@ -320,26 +363,27 @@ pkm_status xent_validate(const pkm_xent_args* a, bool backward) {
   } while (0)
 
 cudaError_t xent_forward(const pkm_xent_args* a, int32_t* status, cudaStream_t st) {
-  const XentLayout L = xent_layout(a);
   char* ws = static_cast<char*>(a->workspace);
-  auto* part = reinterpret_cast<float2*>(ws + L.part);
-  auto* picked = reinterpret_cast<float*>(ws + L.picked);
+  size_t picked_at = 0;
+  fwd_bytes(a, &picked_at);
+  auto* part = reinterpret_cast<float2*>(ws);
+  auto* picked = reinterpret_cast<float*>(ws + picked_at);
   PairMaps<1> maps;
   if (!pair_map(&maps.a[0], a->x, a->T, a->d, a->d, false) ||
       !pair_map(&maps.b[0], a->W, a->V, a->d, a->d, false))
     return cudaErrorInvalidValue;
-  const PairProbs<1> p{{pair_prob(a->T, a->V, a->d, false, false, 1, 8)}, 1, {}};
-  const XentStats epi{a->T, a->V, a->targets, part, picked};
+  const PairProbs<1> p{{fwd_prob(a)}, 1, {}};
+  const XentStats epi{a->T, a->V, p.p[0].tile_n, a->targets, part, picked};
   PKM_TRY((launch_pair_gemm<1>(maps, p, epi, status, st)));
   xent_join_kernel<<<(unsigned)((a->T + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, st>>>(
-      part, fwd_slots(a->V), a->T, a->V, a->targets, a->ignore_index, picked, a->loss, a->lse,
+      part, p.p[0].tiles_n, a->T, a->V, a->targets, a->ignore_index, picked, a->loss, a->lse,
       status);
   PKM_TRY(cudaGetLastError());
   return cudaSuccess;
 }
 
-cudaError_t xent_backward(const pkm_xent_args* a, int32_t* status, cudaStream_t st) {
-  const XentLayout L = xent_layout(a);
+cudaError_t xent_backward(const pkm_xent_args* a, const XentLayout& L, int32_t* status,
+                          cudaStream_t st) {
   char* ws = static_cast<char*>(a->workspace);
   auto* delta = reinterpret_cast<__nv_bfloat16*>(ws + L.delta);
   const bool direct = L.nz == 1 && a->grad_dtype == PKM_F32;
@@ -354,7 +398,7 @@ cudaError_t xent_backward(const pkm_xent_args* a, int32_t* status, cudaStream_t 
       return cudaErrorInvalidValue;
     const PairProbs<1> p{{pair_prob(a->T, Vp, a->d, false, false, 1, 8)}, 1, {}};
     XentDelta de{{}, a->T, Vp, v0, a->V, a->targets, a->ignore_index, a->lse, a->dloss};
-    if (!pair_out_map(&de.out, delta, Vp, a->T, 1, L.ld, PKM_BF16)) return cudaErrorInvalidValue;
+    if (!pair_out_map(&de.out, delta, Vp, a->T, 1, L.ld, PKM_BF16, true)) return cudaErrorInvalidValue;
     PKM_TRY((launch_pair_gemm<1>(m1, p, de, status, st)));
     PairMaps<2> m2;
     if (!pair_map(&m2.a[0], delta, a->T, Vp, L.ld, false) ||
@@ -363,8 +407,8 @@ cudaError_t xent_backward(const pkm_xent_args* a, int32_t* status, cudaStream_t 
         !pair_map(&m2.b[1], a->x, a->d, (int)a->T, a->d, true))
       return cudaErrorInvalidValue;
     // a shorter last piece may fill fewer slices: the others keep their sums
-    const PairProbs<2> q{{pair_prob(a->T, a->d, Vp, false, true, L.nz),
-                          pair_prob(Vp, a->d, (int)a->T, true, true)}, 1, {}};
+    const PairProbs<2> q{{pair_prob(a->T, a->d, Vp, false, true, L.nz, 1, L.tile_dx),
+                          pair_prob(Vp, a->d, (int)a->T, true, true, 1, 1, L.tile_dw)}, 1, {}};
     XentGrads ge{{}, {{a->T, a->d, 0, v0 > 0}, {Vp, a->d, gb, 0}}};
     if (!pair_out_map(&ge.map[0], dx, a->d, a->T, L.nz, a->d, PKM_F32) ||
         !pair_out_map(&ge.map[1], static_cast<char*>(a->dW) + (size_t)v0 * a->d * (gb ? 2 : 4),
@@ -385,15 +429,15 @@ using namespace pkm;
 extern "C" {
 
 PKM_API size_t pkm_linear_xent_forward_workspace_size(const pkm_xent_args* a) {
-  return xent_sizes(a) == PKM_OK ? xent_layout(a).fwd_total : 0;
+  return xent_sizes(a) == PKM_OK ? fwd_bytes(a, nullptr) : 0;
 }
 
 PKM_API size_t pkm_linear_xent_backward_workspace_size(const pkm_xent_args* a) {
-  return xent_sizes(a) == PKM_OK ? xent_layout(a).bwd_total : 0;
+  return xent_sizes(a) == PKM_OK ? xent_layout(a).total : 0;
 }
 
 PKM_API pkm_status pkm_linear_xent_forward(const pkm_xent_args* a, pkm_stream_t stream) {
-  const pkm_status s = xent_validate(a, false);
+  const pkm_status s = xent_validate(a, nullptr);
   if (s != PKM_OK || a->T == 0) return s;
   int32_t* status = status_ptr();
   if (!status) return PKM_ERR_CUDA;
@@ -403,7 +447,8 @@ PKM_API pkm_status pkm_linear_xent_forward(const pkm_xent_args* a, pkm_stream_t 
 }
 
 PKM_API pkm_status pkm_linear_xent_backward(const pkm_xent_args* a, pkm_stream_t stream) {
-  const pkm_status s = xent_validate(a, true);
+  XentLayout L{};
+  const pkm_status s = xent_validate(a, &L);
   if (s != PKM_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (a->T == 0)
@@ -413,7 +458,7 @@ PKM_API pkm_status pkm_linear_xent_backward(const pkm_xent_args* a, pkm_stream_t
                : PKM_ERR_CUDA;
   int32_t* status = status_ptr();
   if (!status) return PKM_ERR_CUDA;
-  return xent_backward(a, status, st) == cudaSuccess ? PKM_OK : PKM_ERR_CUDA;
+  return xent_backward(a, L, status, st) == cudaSuccess ? PKM_OK : PKM_ERR_CUDA;
 }
 
 }  // extern "C"
