@@ -172,22 +172,22 @@ struct PairCtl {
 // stores to global memory touch 32 lines an instruction: for a 128 x 256 fp32
 // tile that alone took as long as the products of K = 1024.)
 
-// 32 fp32 columns, rows of 128 bytes
-__device__ __forceinline__ void stage_f32(unsigned char* buf, int lane, const uint32_t* r) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-        make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+// 2^x and 1 / x, as the hardware approximates them (2^-22 and 2^-23 relative;
+// subnormals flushed)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-// columns 32 h .. + 31 of 64 bf16 columns, rows of 128 bytes
-__device__ __forceinline__ void stage_bf16(unsigned char* buf, int lane, int h,
-                                           const uint32_t* w) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4)) =
-        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-// piece j (of 4) of 32 bf16 columns, rows of 64 bytes
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Piece j (of four, 16 bytes) of the lane's row: 32 bf16 or 16 fp32 columns,
+// rows of 64 bytes, 2 KiB a warp
 __device__ __forceinline__ unsigned char* stage64_at(unsigned char* buf, int lane, int j) {
   return buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
 }
@@ -238,6 +238,15 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Arrive on a barrier of either CTA without a cluster-scope release: nothing but
+// "TMEM has been read" is passed on, which tcgen05.wait::ld and the fence
+// before it have settled.  (With the cluster-scope release the epilogue waited
+// about 2000 cycles for its earlier global writes at every buffer.)
+__device__ __forceinline__ void remote_arrive_local_scope(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 // One lane of the (converged) warp.  The producer and the MMA issuer run their
 // loops as whole warps and only issue through this lane: their addresses and
 // descriptors are then warp-uniform values.  With the loops inside
@@ -278,10 +287,13 @@ struct EpiWarp {
 //   kDual                 two products over the same tile (see above)
 //   struct State          a warp's state over its tiles, zero-initialised
 //   begin(State&, w, prob, row0, n0, z)        before the buffer is ready
-//   tile(State&, w, prob, row0, n0, z, tmem)   by a whole warp: rows row0 + lane,
-//       columns n0 + kCols part .. at TMEM address `tmem` (lane quarter and
-//       column included; a dual epilogue finds the second product 256 columns
-//       further); n0 is the buffer's first column
+//   tile(State&, w, prob, row0, n0, z, tmem, release)   by a whole warp: rows
+//       row0 + lane, columns n0 + kCols part .. at TMEM address `tmem` (lane
+//       quarter and column included; a dual epilogue finds the second product
+//       256 columns further); n0 is the buffer's first column.  It calls
+//       release() once, as soon as it has read TMEM: sixteen warps hold a
+//       buffer in registers, and the next products start then and not after
+//       the epilogue.
 //   abandon(State&, w)    after an abort: lets copies in flight land
 // The accumulator itself -> the problem's output map: fp32 (stored or added
 // to; slice z is the map's third coordinate) or bf16.
@@ -291,45 +303,68 @@ struct StoreOut {
   int bf16, add;
 };
 
-template <int COLS>
+constexpr int kStageRowBytes = 64, kStageBytesPerWarp = 32 * kStageRowBytes;
+
+// Four 16-byte pieces of the lane's row -> columns `col` .. of the map's rows
+// row0 .. + 31 of slice z.
+__device__ __forceinline__ void stage_out(const CUtensorMap* map, const EpiWarp& w, int col,
+                                          int64_t row0, int z, const uint4* v, bool add) {
+  stage_free(w.lane);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(stage64_at(w.stage, w.lane, j)) = v[j];
+  stage_ready();
+  if (w.lane == 0) {
+    if (add)
+      tma_add_3d(map, w.stage, col, (int)row0, z);
+    else
+      tma_store_3d(map, w.stage, col, (int)row0, z);
+    bulk_commit();
+  }
+  __syncwarp();
+}
+
+template <class Release>
 __device__ __forceinline__ void store_tile(const StoreOut& o, const CUtensorMap* map,
                                            const EpiWarp& w, int64_t row0, int n0, int z,
-                                           uint32_t tmem) {
-  const int c0 = n0 + w.part * COLS;
-  if (row0 >= o.rows || c0 >= o.cols) return;  // the whole warp
-  uint32_t r[2][32];
-  tmem_ld_32x32b_x32(tmem, r[0]);
-#pragma unroll
-  for (int q = 0; q < COLS / 32; ++q) {
-    if (c0 + 32 * q >= o.cols) break;
-    tmem_ld_wait();
-    // the next columns are on their way while these are staged
-    if (q + 1 < COLS / 32) tmem_ld_32x32b_x32(tmem + 32 * (q + 1), r[(q + 1) & 1]);
-    const uint32_t* v = r[q & 1];
-    if (o.bf16) {
-      if ((q & 1) == 0) stage_free(w.lane);
-      uint32_t p[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        p[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-      stage_bf16(w.stage, w.lane, q & 1, p);
-      if ((q & 1) == 0 && c0 + 32 * (q + 1) < o.cols) continue;
-    } else {
-      stage_free(w.lane);
-      stage_f32(w.stage, w.lane, v);
-    }
-    stage_ready();
-    if (w.lane == 0) {
-      const int col = c0 + 32 * (o.bf16 ? q & ~1 : q);
-      if (o.add)
-        tma_add_3d(map, w.stage, col, (int)row0, z);
-      else
-        tma_store_3d(map, w.stage, col, (int)row0, z);
-      bulk_commit();
-    }
-    __syncwarp();
+                                           uint32_t tmem, Release release) {
+  const int c0 = n0 + w.part * 64;
+  if (row0 >= o.rows || c0 >= o.cols) {  // the whole warp
+    release();
+    return;
   }
+  uint32_t r[64];
+  tmem_ld_32x32b_x32(tmem, r);
+  tmem_ld_32x32b_x32(tmem + 32, r + 32);
   tmem_ld_wait();
+  release();
+  if (o.bf16) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (c0 + 32 * h >= o.cols) break;
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t* q = r + 32 * h + 8 * j;
+        v[j] = make_uint4(pack_bf16x2(__uint_as_float(q[0]), __uint_as_float(q[1])),
+                          pack_bf16x2(__uint_as_float(q[2]), __uint_as_float(q[3])),
+                          pack_bf16x2(__uint_as_float(q[4]), __uint_as_float(q[5])),
+                          pack_bf16x2(__uint_as_float(q[6]), __uint_as_float(q[7])));
+      }
+      stage_out(map, w, c0 + 32 * h, row0, z, v, o.add);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      if (c0 + 16 * h >= o.cols) break;
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t* q = r + 16 * h + 4 * j;
+        v[j] = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+      stage_out(map, w, c0 + 16 * h, row0, z, v, o.add);
+    }
+  }
 }
 
 template <int NP, class E>
@@ -583,13 +618,15 @@ __global__ void __launch_bounds__(gp::threads<E>(), 1)
         }
         ++used[u];
         tc_fence_after();
-        epi.tile(state, w, it.prob, row0, n0, tc.z, mine + u * kN);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          remote_arrive(map_to(&ctl->acce[u], 0));
-          if (E::kDual) remote_arrive(map_to(&ctl->acce[1], 0));
-        }
+        epi.tile(state, w, it.prob, row0, n0, tc.z, mine + u * kN, [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            remote_arrive_local_scope(map_to(&ctl->acce[u], 0));
+            if (E::kDual) remote_arrive_local_scope(map_to(&ctl->acce[1], 0));
+          }
+          __syncwarp();
+        });
       }
     }
     if (E::kWarpBytes > 0) stage_free(lane);  // no store reads shared memory any more
@@ -604,16 +641,24 @@ __global__ void __launch_bounds__(gp::threads<E>(), 1)
   if (warp == 1) tmem_dealloc_pair(tmem, kTileN);
 }
 
-// out = the sum of nz slices of 8 n8 fp32 values, in slice order
+// out = the sum of nz slices of 8 n8 fp32 values, in slice order; the second
+// half of the grid (y = 1) does the same for part2 and out2.
 template <pkm_dtype GT>
 __global__ void __launch_bounds__(256) slice_sum_kernel(const float* __restrict__ part, int nz,
                                                         int64_t n8,
-                                                        typename Elem<GT>::T* __restrict__ out) {
+                                                        typename Elem<GT>::T* __restrict__ out,
+                                                        const float* __restrict__ part2,
+                                                        typename Elem<GT>::T* __restrict__ out2) {
+  if (blockIdx.y) {
+    part = part2;
+    out = out2;
+  }
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8;
        i += (int64_t)gridDim.x * 256) {
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll 4
     for (int z = 0; z < nz; ++z)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -633,14 +678,17 @@ __global__ void __launch_bounds__(256) slice_sum_kernel(const float* __restrict_
 // -------------------------------------------------------------- host side
 
 inline cudaError_t launch_slice_sum(const float* part, int nz, int64_t n, void* out, pkm_dtype dt,
-                                    cudaStream_t st) {
+                                    cudaStream_t st, const float* part2 = nullptr,
+                                    void* out2 = nullptr) {
   const int64_t n8 = n / 8, blocks = (n8 + 255) / 256;
-  const unsigned grid = (unsigned)(blocks < 148 * 8 ? blocks : 148 * 8);
+  const dim3 grid((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8), part2 ? 2 : 1);
   if (dt == PKM_BF16)
-    slice_sum_kernel<PKM_BF16>
-        <<<grid, 256, 0, st>>>(part, nz, n8, static_cast<__nv_bfloat16*>(out));
+    slice_sum_kernel<PKM_BF16><<<grid, 256, 0, st>>>(part, nz, n8,
+                                                     static_cast<__nv_bfloat16*>(out), part2,
+                                                     static_cast<__nv_bfloat16*>(out2));
   else
-    slice_sum_kernel<PKM_F32><<<grid, 256, 0, st>>>(part, nz, n8, static_cast<float*>(out));
+    slice_sum_kernel<PKM_F32><<<grid, 256, 0, st>>>(part, nz, n8, static_cast<float*>(out), part2,
+                                                    static_cast<float*>(out2));
   return cudaGetLastError();
 }
 
@@ -653,21 +701,19 @@ inline bool pair_map(CUtensorMap* m, const void* base, int64_t rows, int K, int6
   return make_tmap_bf16(m, base, 2, dims, strides, box);
 }
 
-// Tensor map of an output (or fp32 input) of an epilogue: [slices][rows][cols]
-// with `ld` elements from row to row; boxes of 32 rows and 128 bytes (64 with
-// half) of columns.
+// Tensor map of an epilogue's output: [slices][rows][cols] with `ld` elements
+// from row to row; boxes of 32 rows and 64 bytes of columns.
 inline bool pair_out_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows,
-                         int64_t slices, int64_t ld, pkm_dtype dt, bool half = false) {
+                         int64_t slices, int64_t ld, pkm_dtype dt) {
   auto enc = tmap_encoder();
   if (!enc) return false;
   const int b = dt == PKM_F32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)slices};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * b, (cuuint64_t)(ld * rows) * b};
-  const cuuint32_t box[3] = {(cuuint32_t)((half ? 64 : 128) / b), 32, 1}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)(kStageRowBytes / b), 32, 1}, one[3] = {1, 1, 1};
   return enc(m, dt == PKM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
              3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

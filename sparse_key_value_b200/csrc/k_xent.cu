@@ -25,14 +25,7 @@ namespace pkm {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 struct MaxSum {  // of terms 2^s: the maximum and the sum of 2^(s - maximum)
   float mx, sum;
@@ -84,10 +77,16 @@ struct XentStats {
     const float all = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     const float nm = fmaxf(st.v.mx, all * kLog2e);
     const float ref = nm == -INFINITY ? 0.f : nm;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    // two columns an instruction where it is not the exponential
+    const float2 l2 = make_float2(kLog2e, kLog2e), minus = make_float2(-ref, -ref);
+    float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) s[j & 3] += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
-    st.v.sum = fmaf(st.v.sum, ex2(st.v.mx - ref), (s[0] + s[1]) + (s[2] + s[3]));
+    for (int j = 0; j < 32; j += 2) {
+      const float2 x = __ffma2_rn(
+          make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), l2, minus);
+      s[(j >> 1) & 1] = __fadd2_rn(s[(j >> 1) & 1], make_float2(ex2(x.x), ex2(x.y)));
+    }
+    st.v.sum = fmaf(st.v.sum, ex2(st.v.mx - ref), (s[0].x + s[0].y) + (s[1].x + s[1].y));
     st.v.mx = nm;
     const uint32_t at = (uint32_t)st.target - (uint32_t)col;
     if (at < 32u) {
@@ -97,19 +96,21 @@ struct XentStats {
     }
   }
 
+  template <class Release>
   __device__ __forceinline__ void tile(State& st, const EpiWarp& w, int, int64_t row0, int n0,
-                                       int, uint32_t tmem) const {
+                                       int, uint32_t tmem, Release release) const {
     const int64_t m = row0 + w.lane;
     const int c0 = n0 + w.part * kCols;
     if (row0 < T && c0 < V) {
-      uint32_t a[32], b[32];
-      tmem_ld_32x32b_x32(tmem, a);
+      uint32_t r[64];
+      tmem_ld_32x32b_x32(tmem, r);
+      tmem_ld_32x32b_x32(tmem + 32, r + 32);
       tmem_ld_wait();
-      tmem_ld_32x32b_x32(tmem + 32, b);  // on its way while the first columns are summed
-      columns(st, m, c0, a);
-      __syncwarp();  // the wait is warp-aligned
-      tmem_ld_wait();
-      if (c0 + 32 < V) columns(st, m, c0 + 32, b);
+      release();
+      columns(st, m, c0, r);
+      if (c0 + 32 < V) columns(st, m, c0 + 32, r + 32);
+    } else {
+      release();
     }
     if (n0 % tile_n + gp::kN < tile_n && n0 + gp::kN < V) return;  // the second buffer follows
     __syncwarp();
@@ -183,7 +184,8 @@ struct XentDelta {
   int32_t ignore;
   const float *lse, *dloss;
 
-  static constexpr int kWarps = 16, kCols = 64, kStages = 4, kWarpBytes = 2048, kSharedBytes = 0;
+  static constexpr int kWarps = 16, kCols = 64, kStages = 4, kSharedBytes = 0;
+  static constexpr int kWarpBytes = kStageBytesPerWarp;
   static constexpr int kBarArrivals = 1;
   static constexpr bool kDual = false;
   struct State {
@@ -204,8 +206,14 @@ struct XentDelta {
   __device__ __forceinline__ void columns(const State& s, const EpiWarp& w, int64_t row0, int col,
                                           const uint32_t* r) const {
     float p[32];
+    const float2 l2 = make_float2(kLog2e, kLog2e), minus = make_float2(-s.l2, -s.l2);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) p[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -s.l2));
+    for (int j = 0; j < 32; j += 2) {
+      const float2 x = __ffma2_rn(
+          make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), l2, minus);
+      p[j] = ex2(x.x);
+      p[j + 1] = ex2(x.y);
+    }
     const uint32_t at = (uint32_t)s.target - (uint32_t)(v0 + col);
     if (at < 32u) {
 #pragma unroll
@@ -213,33 +221,34 @@ struct XentDelta {
         if (at == j) p[j] -= 1.f;
     }
     uint32_t o[16];
+    const float2 g = make_float2(s.g, s.g);
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      o[j] = s.counted ? pack_bf16x2(p[2 * j] * s.g, p[2 * j + 1] * s.g) : 0u;
-    stage_free(w.lane);
+    for (int j = 0; j < 16; ++j) {
+      const float2 v = __fmul2_rn(make_float2(p[2 * j], p[2 * j + 1]), g);
+      o[j] = s.counted ? pack_bf16x2(v.x, v.y) : 0u;
+    }
+    uint4 v4[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint4*>(stage64_at(w.stage, w.lane, j)) =
-          make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-    stage_ready();
-    if (w.lane == 0) {
-      tma_store_3d(&out, w.stage, col, (int)row0, 0);
-      bulk_commit();
-    }
-    __syncwarp();
+      v4[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    stage_out(&out, w, col, row0, 0, v4, false);
   }
 
+  template <class Release>
   __device__ __forceinline__ void tile(State& s, const EpiWarp& w, int, int64_t row0, int n0, int,
-                                       uint32_t tmem) const {
+                                       uint32_t tmem, Release release) const {
     const int c0 = n0 + w.part * kCols;
-    if (row0 >= T || c0 >= Vp) return;  // the whole warp
-    uint32_t a[32], b[32];
-    tmem_ld_32x32b_x32(tmem, a);
+    if (row0 >= T || c0 >= Vp) {  // the whole warp
+      release();
+      return;
+    }
+    uint32_t r[64];
+    tmem_ld_32x32b_x32(tmem, r);
+    tmem_ld_32x32b_x32(tmem + 32, r + 32);
     tmem_ld_wait();
-    tmem_ld_32x32b_x32(tmem + 32, b);  // on its way while the first columns are worked on
-    columns(s, w, row0, c0, a);
-    tmem_ld_wait();
-    if (c0 + 32 < Vp) columns(s, w, row0, c0 + 32, b);
+    release();
+    columns(s, w, row0, c0, r);
+    if (c0 + 32 < Vp) columns(s, w, row0, c0 + 32, r + 32);
   }
 };
 
@@ -249,15 +258,17 @@ struct XentGrads {
   CUtensorMap map[2];
   StoreOut out[2];
 
-  static constexpr int kWarps = 8, kCols = 128, kStages = 4, kWarpBytes = 4096, kSharedBytes = 0;
+  static constexpr int kWarps = 16, kCols = 64, kStages = 4, kSharedBytes = 0;
+  static constexpr int kWarpBytes = kStageBytesPerWarp;
   static constexpr int kBarArrivals = 1;
   static constexpr bool kDual = false;
   struct State {};
   __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
+  template <class Release>
   __device__ __forceinline__ void tile(State&, const EpiWarp& w, int prob, int64_t row0, int n0,
-                                       int z, uint32_t tmem) const {
-    store_tile<kCols>(out[prob], &map[prob], w, row0, n0, z, tmem);
+                                       int z, uint32_t tmem, Release release) const {
+    store_tile(out[prob], &map[prob], w, row0, n0, z, tmem, release);
   }
 };
 
@@ -398,7 +409,7 @@ cudaError_t xent_backward(const pkm_xent_args* a, const XentLayout& L, int32_t* 
       return cudaErrorInvalidValue;
     const PairProbs<1> p{{pair_prob(a->T, Vp, a->d, false, false, 1, 8)}, 1, {}};
     XentDelta de{{}, a->T, Vp, v0, a->V, a->targets, a->ignore_index, a->lse, a->dloss};
-    if (!pair_out_map(&de.out, delta, Vp, a->T, 1, L.ld, PKM_BF16, true)) return cudaErrorInvalidValue;
+    if (!pair_out_map(&de.out, delta, Vp, a->T, 1, L.ld, PKM_BF16)) return cudaErrorInvalidValue;
     PKM_TRY((launch_pair_gemm<1>(m1, p, de, status, st)));
     PairMaps<2> m2;
     if (!pair_map(&m2.a[0], delta, a->T, Vp, L.ld, false) ||

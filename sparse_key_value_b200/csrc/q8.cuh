@@ -135,9 +135,19 @@ __device__ __forceinline__ void q8_decode(const uint2& q, float scale, pkm_q8 fm
       v[2 * h + 1] = f.y * scale;
     }
   } else {
+    // a byte u = q + 128 put under the exponent of 2^23 is the fp32 number
+    // 2^23 + u, from which 2^23 + 128 goes off exactly
+    const float2 off = make_float2(-8388736.0f, -8388736.0f), s2 = make_float2(scale, scale);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = (float)((int32_t)(w[e >> 2] << (24 - 8 * (e & 3))) >> 24) * scale;
+    for (int e = 0; e < 8; e += 2) {
+      const uint32_t u = w[e >> 2] ^ 0x80808080u;
+      const float2 f = make_float2(
+          __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440u | (e & 3))),
+          __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440u | ((e + 1) & 3))));
+      const float2 r = __fmul2_rn(__fadd2_rn(f, off), s2);
+      v[e] = r.x;
+      v[e + 1] = r.y;
+    }
   }
 }
 
