@@ -396,20 +396,35 @@ def _same_device(dev: torch.device, *ts):
 def _shape(name: str, t: Optional[torch.Tensor], shape, dtype=None):
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:  # shape: a tuple (torch.Size is one)
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
 
 
+# The current stream of a device as a plain handle: building a torch Stream
+# object for it takes longer than the rest of a call's checks together.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _enqueue(fn: str, args, dev: torch.device, stream):
     """Call the entry point with ``args`` on the tensors' device and stream."""
     f = getattr(load(), fn)
+    if stream is not None:
+        s = stream.cuda_stream
+    elif _raw_stream is not None:
+        s = _raw_stream(dev.index)
+    else:
+        s = torch.cuda.current_stream(dev).cuda_stream
     if torch.cuda.current_device() == dev.index:
-        check(f(*args, _stream(dev, stream)), fn)
+        check(f(*args, s), fn)
     else:
         with torch.cuda.device(dev):
-            check(f(*args, _stream(dev, stream)), fn)
+            check(f(*args, s), fn)
 
 
 def _workspace(workspace, need: int, dev: torch.device):
@@ -430,7 +445,7 @@ def _embed_args(ids, n_rows, d, dtype, scale, pad_id) -> "_lib.EmbedArgs":
         if not -2 ** 31 <= pad_id < 2 ** 31:  # ctypes would cut it silently
             raise ValueError(f"pad_id {pad_id} is not an int32")
         a.has_pad, a.pad_id = 1, pad_id
-    a.ids = _p(ids)
+    a.ids = _ptr(ids)
     return a
 
 
@@ -448,7 +463,7 @@ def embedding_forward(table, ids, scale: float = 1.0, pad_id: Optional[int] = No
         out = torch.empty(*ids.shape, d, dtype=table.dtype, device=dev)
     _shape("out", out, (*ids.shape, d), table.dtype)
     _same_device(dev, ids, out)
-    a.table, a.out = _p(table), _p(out)
+    a.table, a.out = _ptr(table), _ptr(out)
     _enqueue("pkm_embed_forward", (ctypes.byref(a),), dev, stream)
     return out
 
@@ -475,7 +490,7 @@ def embedding_backward(dout, ids, n_rows: int, scale: float = 1.0, pad_id: Optio
     need = int(load().pkm_embed_workspace_size(ctypes.byref(a)))
     workspace = _workspace(workspace, need, dev)
     _same_device(dev, ids, grad)
-    a.dout, a.grad, a.workspace, a.workspace_bytes = _p(dout), _p(grad), _p(workspace), \
+    a.dout, a.grad, a.workspace, a.workspace_bytes = _ptr(dout), _ptr(grad), _ptr(workspace), \
         workspace.numel() * workspace.element_size()
     _enqueue("pkm_embed_backward", (ctypes.byref(a),), dev, stream)
     return grad
@@ -519,7 +534,7 @@ def act8_store(x, fmt: str = "int8", stream=None):
     code, dtype = _q8_name(fmt)
     T, d = x.shape
     q, scales = _q8_empty(T, d, dtype, x.device)
-    _enqueue("pkm_act8_store", (_p(x), T, d, _dt(x), code, _p(q), _p(scales)), x.device, stream)
+    _enqueue("pkm_act8_store", (_ptr(x), T, d, _dt(x), code, _ptr(q), _ptr(scales)), x.device, stream)
     return q, scales
 
 
@@ -532,7 +547,7 @@ def act8_load(q, scales, dtype=torch.bfloat16, out=None, stream=None):
         out = torch.empty(T, d, dtype=dtype, device=q.device)
     _shape("out", out, (T, d))
     _same_device(q.device, out)
-    _enqueue("pkm_act8_load", (_p(q), _p(scales), T, d, fmt, _p(out), _dt(out)), q.device, stream)
+    _enqueue("pkm_act8_load", (_ptr(q), _ptr(scales), T, d, fmt, _ptr(out), _dt(out)), q.device, stream)
     return out
 
 
@@ -563,8 +578,8 @@ def add_rmsnorm_forward(x, weight=None, residual=None, eps: float = 1e-6,
     if fmt is not None:
         code, qdt = _q8_name(fmt)
         q, scales = _q8_empty(T, d, qdt, dev)
-    a = _lib.NormArgs(T, d, _dt(x), eps, code, _p(x), _p(residual), _p(weight), _p(h), _p(y),
-                      _p(q), _p(scales), _p(rstd))
+    a = _lib.NormArgs(T, d, _dt(x), eps, code, _ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y),
+                      _ptr(q), _ptr(scales), _ptr(rstd))
     _enqueue("pkm_add_rmsnorm_forward", (ctypes.byref(a),), dev, stream)
     return dict(sum=x if h is None else h, y=y, rstd=rstd, q8=q, scales=scales)
 
@@ -595,12 +610,12 @@ def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, scales=None, want_dwe
     _same_device(dev, sum, scales, weight, rstd, dsum)
     dx = torch.empty(T, d, dtype=dt, device=dev)
     dweight = torch.empty(d, dtype=torch.float32, device=dev) if want_dweight else None
-    a = _lib.NormBwdArgs(T, d, _dt(dx), _dt(dy), fmt, _p(dy), _p(sum), _p(scales), _p(weight),
-                         _p(rstd), _p(dsum), _p(dx), _p(dweight), None, 0)
+    a = _lib.NormBwdArgs(T, d, _dt(dx), _dt(dy), fmt, _ptr(dy), _ptr(sum), _ptr(scales), _ptr(weight),
+                         _ptr(rstd), _ptr(dsum), _ptr(dx), _ptr(dweight), None, 0)
     if want_dweight:
         need = int(load().pkm_add_rmsnorm_backward_workspace_size(ctypes.byref(a)))
         workspace = _workspace(workspace, need, dev)
-        a.workspace, a.workspace_bytes = _p(workspace), \
+        a.workspace, a.workspace_bytes = _ptr(workspace), \
             workspace.numel() * workspace.element_size()
     _enqueue("pkm_add_rmsnorm_backward", (ctypes.byref(a),), dev, stream)
     return dict(dx=dx, dweight=dweight)
@@ -616,7 +631,7 @@ def _xent_args(x, W, targets, ignore_index: int) -> "_lib.XentArgs":
         raise ValueError(f"ignore_index {ignore_index} is not an int32")
     a = _lib.XentArgs()
     a.T, a.V, a.d, a.dtype, a.ignore_index = T, W.shape[0], d, _dt(x), ignore_index
-    a.x, a.W, a.targets = _p(x), _p(W), _p(targets)
+    a.x, a.W, a.targets = _ptr(x), _ptr(W), _ptr(targets)
     return a
 
 
@@ -630,10 +645,10 @@ def linear_xent_forward(x, W, targets, ignore_index: int = -100, workspace=None,
     dev = x.device
     loss = torch.empty(a.T, dtype=torch.float32, device=dev)
     lse = torch.empty(a.T, dtype=torch.float32, device=dev)
-    a.loss, a.lse = _p(loss), _p(lse)
+    a.loss, a.lse = _ptr(loss), _ptr(lse)
     need = int(load().pkm_linear_xent_forward_workspace_size(ctypes.byref(a)))
     workspace = _workspace(workspace, need, dev)
-    a.workspace, a.workspace_bytes = _p(workspace), workspace.numel() * workspace.element_size()
+    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     _enqueue("pkm_linear_xent_forward", (ctypes.byref(a),), dev, stream)
     return loss, lse
 
@@ -657,10 +672,10 @@ def linear_xent_backward(x, W, targets, lse, dloss, ignore_index: int = -100,
     _shape("dW", dW, W.shape, dx.dtype)
     _same_device(dev, lse, dloss, dx, dW)
     a.grad_dtype = _dt(dx)
-    a.lse, a.dloss, a.dx, a.dW = _p(lse), _p(dloss), _p(dx), _p(dW)
+    a.lse, a.dloss, a.dx, a.dW = _ptr(lse), _ptr(dloss), _ptr(dx), _ptr(dW)
     need = int(load().pkm_linear_xent_backward_workspace_size(ctypes.byref(a)))
     workspace = _workspace(workspace, need, dev)
-    a.workspace, a.workspace_bytes = _p(workspace), workspace.numel() * workspace.element_size()
+    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     _enqueue("pkm_linear_xent_backward", (ctypes.byref(a),), dev, stream)
     return dx, dW
 
@@ -689,11 +704,11 @@ def memplus_backward_act8(x8, x_scales, W1, W2, y8, y_scales, dout, grad_dtype=t
     dx = torch.empty(T, dm, dtype=grad_dtype, device=dev)
     dW1 = torch.empty(dm, dv, dtype=grad_dtype, device=dev)
     dW2 = torch.empty(dv, dm, dtype=grad_dtype, device=dev)
-    a = _lib.MemplusBwd8Args(T, dm, dv, fmt, _dt(dx), _p(x8), _p(x_scales), _p(W1), _p(W2),
-                             _p(y8), _p(y_scales), _p(dout), _p(dy), _p(dx), _p(dW1), _p(dW2),
+    a = _lib.MemplusBwd8Args(T, dm, dv, fmt, _dt(dx), _ptr(x8), _ptr(x_scales), _ptr(W1), _ptr(W2),
+                             _ptr(y8), _ptr(y_scales), _ptr(dout), _ptr(dy), _ptr(dx), _ptr(dW1), _ptr(dW2),
                              None, 0)
     need = int(load().pkm_memplus_backward_act8_workspace_size(ctypes.byref(a)))
     workspace = _workspace(workspace, need, dev)
-    a.workspace, a.workspace_bytes = _p(workspace), workspace.numel() * workspace.element_size()
+    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     _enqueue("pkm_memplus_backward_act8", (ctypes.byref(a),), dev, stream)
     return dict(dy=dy, dx=dx, dW1=dW1, dW2=dW2)

@@ -7,14 +7,14 @@
 // Backward: grad[r] = scale * sum of dout[t] over the tokens t with ids[t] = r,
 // every row of the table's gradient written.  Three launches:
 //   1. embed_sort_kernel: one cluster sorts the tokens by id (stable radix
-//      sort, histograms exchanged through distributed shared memory) and marks
-//      the rows that occur in a bitmap, while the other clusters already zero
-//      the first rows of the gradient.
+//      sort, counts and tokens exchanged through distributed shared memory) and
+//      marks the rows that occur in a bitmap, while the other clusters already
+//      zero the first rows of the gradient.
 //   2. embed_sum_kernel: the sorted list is cut into chunks of kChunk entries,
 //      one block sums a chunk's parts in order; the blocks after those zero the
 //      rows that no token reads, so each row is written once.
-//   3. embed_join_kernel: the parts of an id that crosses chunks, joined in
-//      chunk order.
+//   3. embed_join_kernel: the parts of an id that covers three chunks or more,
+//      joined in chunk order.
 // No atomics on values: the same bits every run, and a frequent id spreads
 // over many blocks.  Bound by the gradient's write (n_rows * d), then by the
 // launches' latency.  Lists of more than kSortMost tokens go through the
@@ -90,7 +90,9 @@ __device__ __forceinline__ uint32_t embed_key(int32_t id, int64_t n_rows, int ha
 
 __global__ void embed_keys_kernel(const int32_t* __restrict__ ids, int64_t T, int64_t n_rows,
                                   int has_pad, int32_t pad, uint32_t* __restrict__ keys,
-                                  uint32_t* __restrict__ pos, int32_t* status) {
+                                  uint32_t* __restrict__ pos, uint32_t* n_cross,
+                                  int32_t* status) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *n_cross = 0;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < T;
        i += (int64_t)gridDim.x * blockDim.x) {
     keys[i] = embed_key(ids[i], n_rows, has_pad, pad, status);
@@ -118,40 +120,181 @@ struct EmbedSort {
   uint32_t *key[2], *pos[2];  // [0] receives the sorted list
   uint32_t* bitmap;           // rows that occur, or null
   int64_t words;
+  uint32_t* n_cross;          // ids that cross chunks, counted by the sums; zeroed here
   uint4* fill;                // zeroed by the clusters after the first, or null
   int64_t fill_units;
 };
 
-// Dynamic shared memory: per-warp digit counts, then the CTA's digit totals,
-// then each token's rank within its warp and digit.
-size_t sort_smem(int digit, int rounds) {
-  return ((size_t)32 << digit) * 2 + ((size_t)4 << digit) + (size_t)rounds * kSortThreads * 2;
+// Dynamic shared memory: the tokens passed on (short lists) or each token's
+// rank (long ones), the warps' digit counts, the CTA's digit totals.
+size_t sort_smem(int digit, int rounds, bool shared_list) {
+  return ((size_t)32 << digit) * 2 + ((size_t)4 << digit) +
+         (size_t)rounds * kSortThreads * (shared_list ? 8 : 2);
 }
 
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+// One digit's counts and places, shared by the two sorts below: `cnt` holds the
+// warps' digit counts, `total` the CTA's.  Afterwards cnt[w][d] is the number
+// of this CTA's tokens with digit d in the warps before w and total[d] the
+// first place of the CTA's tokens with digit d.  Three CTA barriers' worth of
+// work, two of them over the cluster.
+__device__ __forceinline__ void sort_places(uint16_t* cnt, uint32_t* total, uint32_t* scan, int bins,
+                                            uint32_t ncta, uint32_t rank) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __syncthreads();
+  if (tid < bins) {
+    uint32_t c[32];
+#pragma unroll
+    for (int w = 0; w < 32; ++w) c[w] = cnt[w * bins + tid];
+    uint32_t run = 0;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) {
+      cnt[w * bins + tid] = (uint16_t)run;
+      run += c[w];
+    }
+    total[tid] = run;
+  }
+  __syncwarp();
+  cluster_sync_all();
+  // the smaller digits of every CTA, then the same digit of the CTAs before this one
+  uint32_t before = 0, all = 0;
+  if (tid < bins) {
+#pragma unroll
+    for (uint32_t c = 0; c < kSortCluster; ++c) {
+      const uint32_t t = c < ncta ? ld_cluster(map_to(&total[tid], c)) : 0u;
+      before += c < rank ? t : 0u;
+      all += t;
+    }
+  }
+  uint32_t incl = all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncwarp();
+  cluster_sync_all();  // every CTA has read the totals; `scan` is written
+  if (tid < bins) {
+    uint32_t base = incl - all + before;
+    for (int w = 0; w < warp; ++w) base += scan[w];
+    total[tid] = base;
+  }
+  __syncthreads();
+}
+
+// The rank of the lane's digit among the warp's earlier tokens with it.
+__device__ __forceinline__ uint32_t digit_rank(uint16_t* mine, uint32_t d, bool valid,
+                                               uint32_t none) {
+  const uint32_t lt = (1u << (threadIdx.x & 31)) - 1u;
+  const uint32_t peers = __match_any_sync(0xffffffffu, valid ? d : none);
+  const uint32_t before = valid ? mine[d] : 0u;
+  __syncwarp();
+  if (valid && (peers & lt) == 0) mine[d] = (uint16_t)(before + __popc(peers));
+  __syncwarp();
+  return before + __popc(peers & lt);
+}
+
+// Zeroes the fill region (clusters after the first).
+__device__ __forceinline__ bool sort_fills(const EmbedSort& p, uint32_t ncta) {
+  if (blockIdx.x < ncta) return false;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int64_t i = (int64_t)(blockIdx.x - ncta) * kSortThreads + threadIdx.x; i < p.fill_units;
+       i += (int64_t)(gridDim.x - ncta) * kSortThreads)
+    __stcs(p.fill + i, zero);
+  return true;
+}
+
+__device__ __forceinline__ void sort_clear(uint16_t* cnt, int bins) {
+  uint4* c = reinterpret_cast<uint4*>(cnt);
+  for (int b = threadIdx.x; b < 4 * bins; b += kSortThreads) c[b] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+}
+
+// Lists of at most R * kSortThreads tokens per CTA: tokens stay in registers
+// within a pass and pass to their next CTA through distributed shared memory,
+// so global memory (busy with the fill) is met only at both ends.
+template <int R>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedSort p,
                                                                   int32_t* status) {
   const uint32_t ncta = cluster_size(), rank = cluster_rank();
-  const int tid = threadIdx.x;
-  if (blockIdx.x >= ncta) {  // a filling cluster
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int64_t i = (int64_t)(blockIdx.x - ncta) * kSortThreads + tid; i < p.fill_units;
-         i += (int64_t)(gridDim.x - ncta) * kSortThreads)
-      p.fill[i] = zero;
-    return;
-  }
+  if (sort_fills(p, ncta)) return;
+  if (rank == 0 && threadIdx.x == 0) *p.n_cross = 0;
   extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int kOwn = R * kSortThreads;  // tokens of a CTA
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bins = 1 << p.digit;
-  uint16_t* cnt = reinterpret_cast<uint16_t*>(smem);                       // [32][bins]
-  uint32_t* total = reinterpret_cast<uint32_t*>(smem + (size_t)64 * bins);  // [bins]
-  uint16_t* ranks = reinterpret_cast<uint16_t*>(smem + (size_t)68 * bins);
+  uint2* list = reinterpret_cast<uint2*>(smem);  // [kOwn] key, position
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(smem + (size_t)kOwn * 8);  // [32][bins]
+  uint32_t* total = reinterpret_cast<uint32_t*>(cnt + 32 * bins);         // [bins]
   __shared__ uint32_t scan[32];
-  const int warp = tid >> 5, lane = tid & 31;
-  const uint32_t lt = (1u << lane) - 1u;
-  uint16_t* mine = cnt + (size_t)warp * bins;
-  // a warp owns rounds * 32 consecutive tokens, so (CTA, warp, round, lane)
-  // is the list's order
-  const int64_t i0 = (int64_t)rank * p.rounds * kSortThreads + (int64_t)warp * p.rounds * 32 + lane;
+  // a warp owns R * 32 consecutive tokens, so (CTA, warp, round, lane) is the
+  // list's order
+  const int l0 = warp * R * 32 + lane;
+  const int64_t i0 = (int64_t)rank * kOwn + l0;
+  uint32_t key[R], pos[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = i0 + r * 32;
+    pos[r] = (uint32_t)i;
+    key[r] = i < p.T ? embed_key(p.ids[i], p.n_rows, p.has_pad, p.pad, status) : 0u;
+  }
+  if (p.bitmap)
+    for (int64_t w = (int64_t)rank * kSortThreads + tid; w < p.words;
+         w += (int64_t)ncta * kSortThreads)
+      p.bitmap[w] = 0;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.digit;
+    sort_clear(cnt, bins);
+    uint32_t rk[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      rk[r] = digit_rank(cnt + warp * bins, (key[r] >> shift) & (bins - 1), i0 + r * 32 < p.T, bins);
+    sort_places(cnt, total, scan, bins, ncta, rank);
+    const bool last = pass == p.passes - 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (i0 + r * 32 >= p.T) continue;
+      const uint32_t d = (key[r] >> shift) & (bins - 1);
+      const uint32_t dst = total[d] + cnt[warp * bins + d] + rk[r];
+      if (last) {
+        p.key[0][dst] = key[r];
+        p.pos[0][dst] = pos[r];
+        if (p.bitmap && key[r] < p.n_rows) atomicOr(p.bitmap + (key[r] >> 5), 1u << (key[r] & 31));
+      } else {
+        st_cluster(map_to(&list[dst % kOwn], dst / kOwn), key[r], pos[r]);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // the pass's list is complete; `total` may be rewritten
+    if (!last) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint2 v = list[l0 + r * 32];
+        key[r] = v.x;
+        pos[r] = v.y;
+      }
+    }
+  }
+}
 
+// Longer lists, up to kSortMost tokens: the passes' lists in global memory.
+__global__ void __launch_bounds__(kSortThreads) embed_sort_long_kernel(const EmbedSort p,
+                                                                       int32_t* status) {
+  const uint32_t ncta = cluster_size(), rank = cluster_rank();
+  if (sort_fills(p, ncta)) return;
+  if (rank == 0 && threadIdx.x == 0) *p.n_cross = 0;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bins = 1 << p.digit;
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(smem);               // [32][bins]
+  uint32_t* total = reinterpret_cast<uint32_t*>(cnt + 32 * bins);  // [bins]
+  uint16_t* ranks = reinterpret_cast<uint16_t*>(total + bins);
+  __shared__ uint32_t scan[32];
+  const int64_t i0 = (int64_t)rank * p.rounds * kSortThreads + (int64_t)warp * p.rounds * 32 + lane;
   if (p.bitmap)
     for (int64_t w = (int64_t)rank * kSortThreads + tid; w < p.words;
          w += (int64_t)ncta * kSortThreads)
@@ -161,69 +304,24 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedSor
     const int out = (p.passes - 1 - pass) & 1;
     const uint32_t* skey = p.key[out ^ 1];
     const uint32_t* spos = p.pos[out ^ 1];
-    for (int b = tid; b < 16 * bins; b += kSortThreads)
-      reinterpret_cast<uint32_t*>(cnt)[b] = 0;
-    __syncthreads();
+    sort_clear(cnt, bins);
     for (int r = 0; r < p.rounds; ++r) {
       const int64_t i = i0 + r * 32;
-      uint32_t d = bins;  // lanes past the end form their own group
-      if (i < p.T) {
-        const uint32_t k = pass == 0
-                               ? embed_key(p.ids[i], p.n_rows, p.has_pad, p.pad, status)
-                               : __ldcg(skey + i);
-        d = (k >> shift) & (bins - 1);
-      }
-      const uint32_t peers = __match_any_sync(0xffffffffu, d);
-      const uint32_t before = i < p.T ? mine[d] : 0u;
-      __syncwarp();
-      if (i < p.T && (peers & lt) == 0) mine[d] = (uint16_t)(before + __popc(peers));
-      __syncwarp();
-      ranks[r * kSortThreads + tid] = (uint16_t)(before + __popc(peers & lt));
+      uint32_t k = 0;
+      if (i < p.T)
+        k = pass == 0 ? embed_key(p.ids[i], p.n_rows, p.has_pad, p.pad, status)
+                      : __ldcg(skey + i);
+      ranks[r * kSortThreads + tid] = (uint16_t)digit_rank(
+          cnt + warp * bins, (k >> shift) & (bins - 1), i < p.T, bins);
     }
-    __syncthreads();
-    if (tid < bins) {  // counts -> prefixes over the warps; the CTA's totals
-      uint32_t run = 0;
-#pragma unroll 8
-      for (int w = 0; w < 32; ++w) {
-        const uint32_t c = cnt[(size_t)w * bins + tid];
-        cnt[(size_t)w * bins + tid] = (uint16_t)run;
-        run += c;
-      }
-      total[tid] = run;
-    }
-    __syncwarp();
-    cluster_sync_all();
-    // first place of this CTA's tokens with digit `tid`: the smaller digits
-    // of every CTA, then the same digit of the CTAs before this one
-    uint32_t before = 0, all = 0;
-    if (tid < bins)
-      for (uint32_t c = 0; c < ncta; ++c) {
-        const uint32_t t = ld_cluster(map_to(&total[tid], c));
-        before += c < rank ? t : 0u;
-        all += t;
-      }
-    uint32_t incl = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncwarp();
-    cluster_sync_all();  // every CTA has read the totals; `scan` is written
-    if (tid < bins) {
-      uint32_t base = incl - all + before;
-      for (int w = 0; w < warp; ++w) base += scan[w];
-      total[tid] = base;
-    }
-    __syncthreads();
+    sort_places(cnt, total, scan, bins, ncta, rank);
     for (int r = 0; r < p.rounds; ++r) {
       const int64_t i = i0 + r * 32;
       if (i >= p.T) break;
       const uint32_t k = pass == 0 ? embed_key(p.ids[i], p.n_rows, p.has_pad, p.pad, nullptr)
                                    : __ldcg(skey + i);
       const uint32_t d = (k >> shift) & (bins - 1);
-      const uint32_t dst = total[d] + mine[d] + ranks[r * kSortThreads + tid];
+      const uint32_t dst = total[d] + cnt[warp * bins + d] + ranks[r * kSortThreads + tid];
       p.key[out][dst] = k;
       p.pos[out][dst] = pass == 0 ? (uint32_t)i : __ldcg(spos + i);
       if (pass == 0 && p.bitmap && k < p.n_rows) atomicOr(p.bitmap + (k >> 5), 1u << (k & 31));
@@ -272,42 +370,61 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
     const uint32_t* __restrict__ skey, const uint32_t* __restrict__ spos, int64_t T,
     uint32_t mark, const typename Elem<DT>::T* __restrict__ dout, int d, float scale, int add,
     typename Elem<GT>::T* __restrict__ grad, float* __restrict__ first,
-    float* __restrict__ last, int slices, int64_t n_sum, const EmbedFill fill) {
+    float* __restrict__ last, int slices, int64_t n_sum, uint32_t* __restrict__ n_cross,
+    uint32_t* __restrict__ cross, const EmbedFill fill) {
   if ((int64_t)blockIdx.x >= n_sum) {
     fill_rows<GT>(fill, blockIdx.x - n_sum, d, grad);
     return;
   }
-  __shared__ uint32_t keys[kChunk + 2];  // [0]: the key before the chunk, [len + 1]: after it
-  __shared__ uint32_t rows[kChunk];
+  // this chunk's keys and the next one's: [0] is the key before the chunk
+  __shared__ uint32_t keys[2 * kChunk + 2];
+  __shared__ uint32_t rows[2 * kChunk];
   const int64_t c = blockIdx.x / slices, i0 = c * kChunk;
   const int len = (int)min((int64_t)kChunk, T - i0);
-  for (int j = threadIdx.x; j < len + 2; j += blockDim.x) {
+  for (int j = threadIdx.x; j < 2 * kChunk + 2; j += blockDim.x) {
     const int64_t i = i0 + j - 1;
-    keys[j] = i >= 0 && i < T ? skey[i] : mark;
-    if (j >= 1 && j <= len) rows[j - 1] = spos[i];
+    const bool in = i >= 0 && i < T;
+    keys[j] = in ? skey[i] : mark;
+    if (in && j >= 1 && j <= 2 * kChunk) rows[j - 1] = spos[i];
   }
+  // the key before the last chunk (mark sorts last, so it is no earlier key)
+  const uint32_t before = i0 > kChunk ? skey[i0 - kChunk - 1] : mark;
   __syncthreads();
+  // An id over two chunks is summed whole by the chunk it begins in; one over
+  // three or more goes in parts, `first` and `last`, to the join.
+  int e0 = 0, e1 = len;
+  bool starts = keys[0] != keys[1] || keys[1] == mark;
+  if (!starts && before != keys[1] && keys[len + 1] != keys[1]) {
+    while (e0 < len && keys[e0 + 1] == keys[0]) ++e0;
+    starts = true;
+  }
+  const uint32_t tail = keys[len];
+  const bool goes_over = len == kChunk && tail != mark && keys[len + 1] == tail &&
+                         !(keys[0] == tail && keys[1] == tail);
+  if (goes_over && keys[2 * kChunk + 1] != tail)
+    while (e1 < 2 * kChunk && keys[e1 + 1] == tail) ++e1;
+  if (goes_over && e1 == len && threadIdx.x == 0 && blockIdx.x % slices == 0)
+    cross[atomicAdd(n_cross, 1u)] = (uint32_t)c;  // entries stand for themselves: any order
   const int col = ((int)(blockIdx.x % slices) * kSumUnits + threadIdx.x) * kUnit;
   if (col >= d) return;
   float acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  bool starts = keys[1] == mark || keys[0] != keys[1];  // the current part begins its id
-  for (int j0 = 0; j0 < len && keys[j0 + 1] != mark; j0 += kAhead) {
+  for (int j0 = e0; j0 < e1 && keys[j0 + 1] != mark; j0 += kAhead) {
     float f[kAhead][8];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (j0 + u < len && keys[j0 + u + 1] != mark)
+      if (j0 + u < e1 && keys[j0 + u + 1] != mark)
         load8<DT>(dout + (int64_t)rows[j0 + u] * d + col, f[u]);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int j = j0 + u;
-      if (j >= len || keys[j + 1] == mark) break;
+      if (j >= e1 || keys[j + 1] == mark) break;
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += f[u][e];
       const uint32_t key = keys[j + 1];
       const bool goes_on = keys[j + 2] == key;
-      if (goes_on && j + 1 < len) continue;
+      if (goes_on && j + 1 < e1) continue;
       if (!starts)
         store8<PKM_F32>(first + c * d + col, acc);
       else if (goes_on)
@@ -321,45 +438,75 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
   }
 }
 
-// The id that begins in chunk c and goes on: its parts in chunk order.
+// An id that begins in chunk c and goes on past the next: its parts in chunk
+// order, cut into a run of chunks per warp (a frequent id has many), the runs
+// joined in order.  The blocks share the sums' list of such ids.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinBlocks = 148;
+
 template <pkm_dtype GT>
-__global__ void __launch_bounds__(32) embed_join_kernel(
-    const uint32_t* __restrict__ skey, int64_t T, uint32_t mark, int d, float scale, int add,
-    typename Elem<GT>::T* __restrict__ grad, const float* __restrict__ first,
-    const float* __restrict__ last) {
-  const int64_t c = blockIdx.x, end = (c + 1) * kChunk;
-  if (end >= T) return;
-  const uint32_t key = skey[end - 1];
-  if (key == mark || skey[end] != key) return;
-  if (c > 0 && skey[c * kChunk - 1] == key) return;  // begins in an earlier chunk
+__device__ __forceinline__ void join_one(int64_t c, const uint32_t* skey, int64_t T, int d,
+                                         float scale, int add, typename Elem<GT>::T* grad,
+                                         const float* first, const float* last,
+                                         float (*part)[32 * kUnit]) {
+  const uint32_t key = skey[(c + 1) * kChunk];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // chunks c + 1 .. stop - 1 hold the rest: 32 chunks looked at at a time
   const int64_t chunks = (T + kChunk - 1) / kChunk;
   int64_t stop = c + 1;
   for (;; stop += 32) {
-    const int64_t q = stop + threadIdx.x;  // chunk q begins with the id
+    const int64_t q = stop + lane;  // chunk q begins with the id
     const uint32_t m = __ballot_sync(0xffffffffu, q < chunks && skey[q * kChunk] == key);
     if (m != 0xffffffffu) {
       stop += __ffs(~m) - 1;
       break;
     }
   }
-  const int col = (blockIdx.y * 32 + threadIdx.x) * kUnit;
-  if (col >= d) return;
+  const int64_t run = (stop - c - 1 + kJoinWarps - 1) / kJoinWarps;
+  const int64_t q1 = c + 1 + warp * run, q2 = min(stop, q1 + run);
+  const int col = (blockIdx.y * 32 + lane) * kUnit;
   float acc[8];
-  load8<PKM_F32>(last + c * d + col, acc);
-  for (int64_t q0 = c + 1; q0 < stop; q0 += 4) {
-    float f[4][8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (q0 + u < stop) load8<PKM_F32>(first + (q0 + u) * d + col, f[u]);
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  if (col < d) {
+    if (warp == 0) load8<PKM_F32>(last + c * d + col, acc);
+    for (int64_t q0 = q1; q0 < q2; q0 += 4) {
+      float f[4][8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (q0 + u < stop) {
+      for (int u = 0; u < 4; ++u)
+        if (q0 + u < q2) load8<PKM_F32>(first + (q0 + u) * d + col, f[u]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += f[u][e];
-      }
+      for (int u = 0; u < 4; ++u)
+        if (q0 + u < q2) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] += f[u][e];
+        }
+    }
   }
+#pragma unroll
+  for (int e = 0; e < 8; e += 4)
+    *reinterpret_cast<float4*>(&part[warp][lane * kUnit + e]) =
+        make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+  __syncthreads();
+  if (warp != 0 || col >= d) return;
+  for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += part[w][lane * kUnit + e];
   write_grad<GT>(grad + (int64_t)key * d + col, acc, scale, add);
+}
+
+template <pkm_dtype GT>
+__global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(
+    const uint32_t* __restrict__ skey, int64_t T, int d, float scale, int add,
+    typename Elem<GT>::T* __restrict__ grad, const float* __restrict__ first,
+    const float* __restrict__ last, const uint32_t* __restrict__ n_cross,
+    const uint32_t* __restrict__ cross) {
+  __shared__ float part[kJoinWarps][32 * kUnit];
+  const uint32_t n = *n_cross;
+  for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
+    join_one<GT>(cross[i], skey, T, d, scale, add, grad, first, last, part);
+    __syncthreads();  // `part` may be written again
+  }
 }
 
 int key_bits(int64_t n_rows) {  // bits that hold the keys 0 .. n_rows
@@ -372,7 +519,7 @@ size_t rup(size_t x) { return (x + 255) / 256 * 256; }
 bool need16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct EmbedLayout {
-  size_t keys, pos, skey, spos, radix, bitmap, first, last, total;
+  size_t keys, pos, skey, spos, radix, bitmap, cross, first, last, total;
   bool cluster;  // the list fits the one-cluster sort
 };
 
@@ -393,6 +540,7 @@ EmbedLayout embed_layout(const pkm_embed_args* a) {
   L.spos = take(T * 4);
   L.radix = L.cluster ? 0 : take(radix_sort_workspace(a->T));
   L.bitmap = L.cluster && !a->accumulate ? take((size_t)(a->n_rows + 31) / 32 * 4) : 0;
+  L.cross = take((chunks + 1) * 4);  // count, then chunks
   L.first = take(chunks * d * 4);
   L.last = take(chunks * d * 4);
   L.total = off;
@@ -418,7 +566,7 @@ pkm_status embed_validate(const pkm_embed_args* a, bool backward) {
 
 // Rows that the sort's launch zeroes beside the sort: about as many bytes as
 // the memory takes in the sort's time.
-constexpr int64_t kFillBeside = int64_t(32) << 20;
+constexpr int64_t kFillBeside = int64_t(64) << 20;
 
 template <pkm_dtype DT, pkm_dtype GT>
 cudaError_t embed_sums(const pkm_embed_args* a, const EmbedLayout& L, char* ws,
@@ -434,14 +582,17 @@ cudaError_t embed_sums(const pkm_embed_args* a, const EmbedLayout& L, char* ws,
   const int64_t n_sum = chunks * slices;
   const int64_t n_fill = fill.bitmap ? (fill.n_rows - fill.first + 31) / 32 : 0;
   if (n_sum + n_fill > 0x7fffffff) return cudaErrorInvalidValue;
+  uint32_t* cross = reinterpret_cast<uint32_t*>(ws + L.cross);
   embed_sum_kernel<DT, GT><<<(unsigned)(n_sum + n_fill), kSumUnits, 0, st>>>(
       skey, spos, a->T, (uint32_t)a->n_rows, static_cast<const typename Elem<DT>::T*>(a->dout),
-      a->d, a->scale, a->accumulate, grad, first, last, slices, n_sum, fill);
+      a->d, a->scale, a->accumulate, grad, first, last, slices, n_sum, cross,
+      cross + 1, fill);
   note_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || chunks < 2) return e;
-  embed_join_kernel<GT><<<dim3((unsigned)(chunks - 1), (units + 31) / 32), 32, 0, st>>>(
-      skey, a->T, (uint32_t)a->n_rows, a->d, a->scale, a->accumulate, grad, first, last);
+  const unsigned blocks = (unsigned)(chunks - 1 < kJoinBlocks ? chunks - 1 : kJoinBlocks);
+  embed_join_kernel<GT><<<dim3(blocks, (units + 31) / 32), 32 * kJoinWarps, 0, st>>>(
+      skey, a->T, a->d, a->scale, a->accumulate, grad, first, last, cross, cross + 1);
   note_launch();
   return cudaGetLastError();
 }
@@ -465,6 +616,7 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
   p.pos[0] = reinterpret_cast<uint32_t*>(ws + L.spos);
   p.key[1] = reinterpret_cast<uint32_t*>(ws + L.keys);
   p.pos[1] = reinterpret_cast<uint32_t*>(ws + L.pos);
+  p.n_cross = reinterpret_cast<uint32_t*>(ws + L.cross);
   int clusters = 1;
   if (!a->accumulate) {
     p.bitmap = reinterpret_cast<uint32_t*>(ws + L.bitmap);
@@ -479,10 +631,18 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
     const int64_t want = (blocks + ncta - 1) / ncta, most = 136 / ncta;
     clusters += (int)(want < most ? want : most);
   }
-  const size_t smem = sort_smem(p.digit, p.rounds);
-  cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sort_smem(kMaxDigit, kSortRounds));
+  // rounds of the short sort: a power of two, the tokens of a CTA
+  int short_rounds = 1;
+  while (short_rounds < p.rounds) short_rounds *= 2;
+  auto kern = short_rounds == 1   ? embed_sort_kernel<1>
+              : short_rounds == 2 ? embed_sort_kernel<2>
+              : short_rounds == 4 ? embed_sort_kernel<4>
+                                  : embed_sort_long_kernel;
+  const bool is_short = short_rounds <= 4;
+  const size_t smem = sort_smem(p.digit, is_short ? short_rounds : p.rounds, is_short);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sort_smem(kMaxDigit, is_short ? 4 : kSortRounds,
+                                                      is_short));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * ncta), 1, 1);
@@ -496,7 +656,7 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, p, status);
+  e = cudaLaunchKernelEx(&cfg, kern, p, status);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -515,7 +675,8 @@ cudaError_t embed_backward(const pkm_embed_args* a, int32_t* status, cudaStream_
     uint32_t* pos = reinterpret_cast<uint32_t*>(ws + L.pos);
     const int64_t blocks = (a->T + 255) / 256;
     embed_keys_kernel<<<(unsigned)(blocks < 1184 ? blocks : 1184), 256, 0, st>>>(
-        a->ids, a->T, a->n_rows, a->has_pad, a->pad_id, keys, pos, status);
+        a->ids, a->T, a->n_rows, a->has_pad, a->pad_id, keys, pos,
+        reinterpret_cast<uint32_t*>(ws + L.cross), status);
     note_launch();
     e = launch_radix_sort(keys, pos, a->T, key_bits(a->n_rows),
                           reinterpret_cast<uint32_t*>(ws + L.skey),
