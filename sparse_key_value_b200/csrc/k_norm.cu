@@ -26,19 +26,20 @@ constexpr int kNormThreads = 256;
 
 constexpr int block_threads(int wpr) { return wpr * 32 > kNormThreads ? wpr * 32 : kNormThreads; }
 
-// Sum over the row's WPR warps (the warps of a row are consecutive); every
-// thread of the block calls it.  Fixed order: the same bits every run.
+// Sum over the row's WPR warps (consecutive ones, a named barrier of their
+// own; `red` [2][warps], used in turn: the barrier of the next sum follows
+// every read of this one).  Fixed order: the same bits every run.
 template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
+__device__ __forceinline__ float row_sum(float v, float* red, int turn) {
   v = warp_sum(v);
   if constexpr (WPR > 1) {
     const int warp = threadIdx.x >> 5;
-    __syncthreads();  // the previous use of `red` has been read
-    if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
+    float* r = red + (turn & 1) * (block_threads(WPR) / 32);
+    if ((threadIdx.x & 31) == 0) r[warp] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WPR), "n"(32 * WPR) : "memory");
     v = 0.f;
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) v += red[warp / WPR * WPR + w];
+    for (int w = 0; w < WPR; ++w) v += r[warp / WPR * WPR + w];
   }
   return v;
 }
@@ -57,7 +58,7 @@ struct NormFwd {
 template <pkm_dtype DT, int NU, int WPR>
 __global__ void __launch_bounds__(block_threads(WPR)) norm_fwd_kernel(const NormFwd p) {
   using E = typename Elem<DT>::T;
-  __shared__ float red[block_threads(WPR) / 32];
+  __shared__ float red[2 * block_threads(WPR) / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kRows = block_threads(WPR) / 32 / WPR;
   const int64_t row = (int64_t)blockIdx.x * kRows + warp / WPR;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(block_threads(WPR)) norm_fwd_kernel(const Norm
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(h[c][e], h[c][e], ss);
   }
-  ss = row_sum<WPR>(ss, red);
+  ss = row_sum<WPR>(ss, red, 0);
   const float rstd = 1.0f / sqrtf(ss / (float)p.d + p.eps);
   if (live && p.rstd && col0 == 0) p.rstd[row] = rstd;
   const int groups = q8_groups(p.d);
@@ -135,21 +136,26 @@ struct NormBwd {
   float* part;  // [blocks, d] weight-gradient partials, or null
 };
 
+// Blocks of the backward per SM.
+constexpr int bwd_per_sm(int wpr) { return block_threads(wpr) <= 256 ? 3 : 1; }
+
 // DY: type of dy; DT: type of h (when not 8-bit), weight, dsum and dx.  A
-// row's dy, h and dsum wait packed in registers, all loaded up front: two
-// blocks per SM then keep about 90 KB of loads in flight.
+// row's dy, h and dsum wait packed in registers, all loaded up front: the
+// blocks of an SM then keep about 75 KB of loads in flight.
 template <pkm_dtype DT, pkm_dtype DY, int NU, int WPR>
-__global__ void __launch_bounds__(block_threads(WPR), WPR <= 16 ? 512 / block_threads(WPR) : 1)
+__global__ void __launch_bounds__(block_threads(WPR), bwd_per_sm(WPR))
     norm_bwd_kernel(const NormBwd p) {
   using E = typename Elem<DT>::T;
   using Ey = typename Elem<DY>::T;
   constexpr int kWarps = block_threads(WPR) / 32;
   constexpr int kTeams = kWarps / WPR;  // rows in flight per block
-  __shared__ float red[kWarps];
+  __shared__ float red[2 * kWarps];
+  int turn = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = warp / WPR;
   const int col0 = ((warp % WPR) * 32 + lane) * kUnit;
   const int groups = q8_groups(p.d);
+  pdl_launch_dependents();  // the partials' sum waits for this kernel's end
   float dw[NU][8];
 #pragma unroll
   for (int c = 0; c < NU; ++c)
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(block_threads(WPR), WPR <= 16 ? 512 / block_th
 #pragma unroll
       for (int e = 0; e < 8; ++e) dot = fmaf(g[e], n[e], dot);
     }
-    const float mean = row_sum<WPR>(dot, red) / (float)p.d;
+    const float mean = row_sum<WPR>(dot, red, turn++) / (float)p.d;
 #pragma unroll
     for (int c = 0; c < NU; ++c) {
       float g[8], n[8], o[8];
@@ -253,25 +259,30 @@ __global__ void __launch_bounds__(block_threads(WPR), WPR <= 16 ? 512 / block_th
   }
 }
 
-// dweight[c] = sum over blocks of part[block][c]: 32 columns per block, 8
-// row strides, joined in order
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int blocks,
-                                                      int d, float* __restrict__ dw) {
-  __shared__ float s[8][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+// dweight[c] = sum over blocks of part[block][c]: 32 columns per block, 16
+// row strides of several loads in flight, joined in order
+constexpr int kDwStrips = 16;
+__global__ void __launch_bounds__(32 * kDwStrips) norm_dw_kernel(const float* __restrict__ part,
+                                                                 int blocks, int d,
+                                                                 float* __restrict__ dw) {
+  __shared__ float s[kDwStrips][32];
+  const int lane = threadIdx.x & 31, col = blockIdx.x * 32 + lane, r = threadIdx.x >> 5;
   float v = 0.f;
-  if (col < d)
-    for (int b = r; b < blocks; b += 8) v += part[(int64_t)b * d + col];
-  s[r][threadIdx.x & 31] = v;
+  pdl_wait();
+  if (col < d) {
+#pragma unroll 8
+    for (int b = r; b < blocks; b += kDwStrips) v += part[(int64_t)b * d + col];
+  }
+  s[r][lane] = v;
   __syncthreads();
   if (r == 0 && col < d) {
-    for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x];
+    for (int k = 1; k < kDwStrips; ++k) v += s[k][lane];
     dw[col] = v;
   }
 }
 
 constexpr int kMaxD = 16384;
-constexpr int kBwdBlocks = 148 * 2;
+constexpr int kSMs = 148;
 
 int rows_per_block(int wpr) { return wpr >= 8 ? 1 : 8 / wpr; }
 
@@ -279,38 +290,50 @@ template <int N>
 using Int = std::integral_constant<int, N>;
 
 // Units per lane and warps per row: as few warps as hold the row with UMAX
-// units a lane.  Four of bf16 (no block barrier up to 1024 columns), two of
-// fp32 (the same registers).
+// units a lane.  The forward holds four (no barrier up to 1024 columns).  The
+// backward, with three tensors and the weight gradient in registers, holds
+// two of bf16 and one of fp32: three blocks per SM then have more rows in
+// flight than two with four units (35 against 38 us at 8191 x 2048 bf16).
 template <int UMAX, typename F>
 cudaError_t norm_shape(int d, F&& f) {
   if (d <= 256) return f(Int<1>{}, Int<1>{});
-  if (d <= 512) return f(Int<2>{}, Int<1>{});
   if constexpr (UMAX == 4) {
+    if (d <= 512) return f(Int<2>{}, Int<1>{});
     if (d <= 1024) return f(Int<4>{}, Int<1>{});
     if (d <= 2048) return f(Int<4>{}, Int<2>{});
     if (d <= 4096) return f(Int<4>{}, Int<4>{});
     if (d <= 8192) return f(Int<4>{}, Int<8>{});
     return f(Int<4>{}, Int<16>{});
-  } else {
+  } else if constexpr (UMAX == 2) {
+    if (d <= 512) return f(Int<2>{}, Int<1>{});
     if (d <= 1024) return f(Int<2>{}, Int<2>{});
     if (d <= 2048) return f(Int<2>{}, Int<4>{});
     if (d <= 4096) return f(Int<2>{}, Int<8>{});
     if (d <= 8192) return f(Int<2>{}, Int<16>{});
     return f(Int<2>{}, Int<32>{});
+  } else {
+    if (d <= 512) return f(Int<1>{}, Int<2>{});
+    if (d <= 1024) return f(Int<1>{}, Int<4>{});
+    if (d <= 2048) return f(Int<1>{}, Int<8>{});
+    if (d <= 4096) return f(Int<1>{}, Int<16>{});
+    if (d <= 8192) return f(Int<1>{}, Int<32>{});
+    return f(Int<2>{}, Int<32>{});
   }
 }
 
-// Blocks of the backward (each writes a partial weight gradient): two per SM
-// of 256 threads, at most one per group of rows.
+// Blocks of the backward (each writes a partial weight gradient): what the SMs
+// hold at a time, at most one per group of rows.
 int bwd_blocks(int64_t T, int d, bool f32) {
-  int rows = 1;
+  int rows = 1, most = kSMs;
   const auto f = [&](auto, auto wpr) {
-    rows = rows_per_block(decltype(wpr)::value);
+    constexpr int WPR = decltype(wpr)::value;
+    rows = rows_per_block(WPR);
+    most = kSMs * bwd_per_sm(WPR);
     return cudaSuccess;
   };
-  f32 ? norm_shape<2>(d, f) : norm_shape<4>(d, f);
+  f32 ? norm_shape<1>(d, f) : norm_shape<2>(d, f);
   const int64_t b = (T + rows - 1) / rows;
-  return (int)(b < kBwdBlocks ? b : kBwdBlocks);
+  return (int)(b < most ? b : most);
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -332,16 +355,16 @@ template <pkm_dtype DT, pkm_dtype DY>
 cudaError_t bwd_launch(const NormBwd& p, float* dweight, cudaStream_t st) {
   constexpr bool f32 = DT == PKM_F32 || DY == PKM_F32;
   const int blocks = bwd_blocks(p.T, p.d, f32);
-  const cudaError_t e = norm_shape<f32 ? 2 : 4>(p.d, [&](auto nu, auto wpr) {
+  const cudaError_t e = norm_shape<f32 ? 1 : 2>(p.d, [&](auto nu, auto wpr) {
     constexpr int NU = decltype(nu)::value, WPR = decltype(wpr)::value;
     norm_bwd_kernel<DT, DY, NU, WPR><<<blocks, block_threads(WPR), 0, st>>>(p);
     note_launch();
     return cudaGetLastError();
   });
   if (e != cudaSuccess || !dweight) return e;
-  norm_dw_kernel<<<(p.d + 31) / 32, 256, 0, st>>>(p.part, blocks, p.d, dweight);
   note_launch();
-  return cudaGetLastError();
+  return launch_maybe_pdl(true, norm_dw_kernel, dim3((p.d + 31) / 32), dim3(32 * kDwStrips), 0, st,
+                          p.part, blocks, p.d, dweight);
 }
 
 pkm_status fwd_validate(const pkm_norm_args* a) {

@@ -112,12 +112,13 @@ __device__ __forceinline__ uint2 q8_encode(const float* v, float inv, pkm_q8 fmt
       w[h] = lo | (hi << 16);
     }
   } else {
+    // 1.5 * 2^23 + v / s rounds to an integer whose low byte is two's complement
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      w[h] = 0;
+      uint32_t b[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[h] |= ((uint32_t)__float2int_rn(v[4 * h + e] * inv) & 0xffu) << (8 * e);
+      for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(fmaf(v[4 * h + e], inv, 12582912.0f));
+      w[h] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
     }
   }
   return make_uint2(w[0], w[1]);
