@@ -30,6 +30,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "kernels.h"
 #include "tc_pair.cuh"
 #include "tmap.h"
 
@@ -378,6 +379,7 @@ __global__ void __launch_bounds__(gp::threads<E>(), 1)
                 "shared memory layout");
   static_assert(sizeof(PairCtl) <= 512 && smem_bytes<E>() <= 227 * 1024, "shared memory size");
   static_assert(kEpiWarps * E::kCols == 4 * kN && kEpiWarps <= kMaxWarps, "columns per warp");
+  pdl_launch_dependents();
   extern __shared__ unsigned char smem_raw[];
   unsigned char* stages = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -418,6 +420,7 @@ __global__ void __launch_bounds__(gp::threads<E>(), 1)
   cluster_sync_all();  // both CTAs' barriers and TMEM exist before any remote use
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  pdl_wait();  // operands and outputs belong to the kernel before until here
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
@@ -649,6 +652,8 @@ __global__ void __launch_bounds__(256) slice_sum_kernel(const float* __restrict_
                                                         typename Elem<GT>::T* __restrict__ out,
                                                         const float* __restrict__ part2,
                                                         typename Elem<GT>::T* __restrict__ out2) {
+  pdl_launch_dependents();
+  pdl_wait();
   if (blockIdx.y) {
     part = part2;
     out = out2;
@@ -682,14 +687,12 @@ inline cudaError_t launch_slice_sum(const float* part, int nz, int64_t n, void* 
                                     void* out2 = nullptr) {
   const int64_t n8 = n / 8, blocks = (n8 + 255) / 256;
   const dim3 grid((unsigned)(blocks < 148 * 8 ? blocks : 148 * 8), part2 ? 2 : 1);
-  if (dt == PKM_BF16)
-    slice_sum_kernel<PKM_BF16><<<grid, 256, 0, st>>>(part, nz, n8,
-                                                     static_cast<__nv_bfloat16*>(out), part2,
-                                                     static_cast<__nv_bfloat16*>(out2));
-  else
-    slice_sum_kernel<PKM_F32><<<grid, 256, 0, st>>>(part, nz, n8, static_cast<float*>(out), part2,
-                                                    static_cast<float*>(out2));
-  return cudaGetLastError();
+  return dt == PKM_BF16
+             ? launch_maybe_pdl(true, slice_sum_kernel<PKM_BF16>, grid, dim3(256), 0, st, part, nz,
+                                n8, static_cast<__nv_bfloat16*>(out), part2,
+                                static_cast<__nv_bfloat16*>(out2))
+             : launch_maybe_pdl(true, slice_sum_kernel<PKM_F32>, grid, dim3(256), 0, st, part, nz,
+                                n8, static_cast<float*>(out), part2, static_cast<float*>(out2));
 }
 
 // Tensor map of an operand with `rows` rows (M or N) and depth K, `ld`
@@ -853,13 +856,15 @@ cudaError_t launch_pair_gemm(const PairMaps<NP>& maps, PairProbs<NP> probs, cons
   cfg.blockDim = dim3(gp::threads<E>(), 1, 1);
   cfg.dynamicSmemBytes = gp::smem_bytes<E>();
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, pair_gemm_kernel<NP, E>, maps, probs, epi, status);
 }
 

@@ -30,6 +30,8 @@ template <pkm_dtype DT>
 __global__ void __launch_bounds__(kThreads) act8_store_kernel(
     const typename Elem<DT>::T* __restrict__ x, int64_t n_groups, int groups, int d, pkm_q8 fmt,
     uint8_t* __restrict__ q, float* __restrict__ scales) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int64_t g0 = (int64_t)blockIdx.x * (kHalves * kAtOnce) + threadIdx.x / kGroupLanes;
   int64_t at[kAtOnce];
   Raw8<DT> raw[kAtOnce];
@@ -54,6 +56,8 @@ template <pkm_dtype DT>
 __global__ void __launch_bounds__(kThreads) act8_load_kernel(
     const uint8_t* __restrict__ q, const float* __restrict__ scales, int64_t n_groups, int groups,
     int d, pkm_q8 fmt, typename Elem<DT>::T* __restrict__ out) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int64_t g0 = (int64_t)blockIdx.x * (kHalves * kAtOnce) + threadIdx.x / kGroupLanes;
   int64_t at[kAtOnce];
   uint2 raw[kAtOnce];
@@ -85,14 +89,15 @@ cudaError_t launch_act8_store(const void* x, int64_t T, int d, pkm_dtype dt, pkm
   const int g = q8_groups(d);
   const int64_t n = T * g;
   if (n <= 0) return cudaSuccess;
-  if (dt == PKM_BF16)
-    act8_store_kernel<PKM_BF16><<<group_grid(n), kThreads, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(x), n, g, d, fmt, static_cast<uint8_t*>(q), scales);
-  else
-    act8_store_kernel<PKM_F32><<<group_grid(n), kThreads, 0, stream>>>(
-        static_cast<const float*>(x), n, g, d, fmt, static_cast<uint8_t*>(q), scales);
+  const dim3 grid(group_grid(n)), block(kThreads);
   note_launch();
-  return cudaGetLastError();
+  return dt == PKM_BF16
+             ? launch_maybe_pdl(true, act8_store_kernel<PKM_BF16>, grid, block, 0, stream,
+                                static_cast<const __nv_bfloat16*>(x), n, g, d, fmt,
+                                static_cast<uint8_t*>(q), scales)
+             : launch_maybe_pdl(true, act8_store_kernel<PKM_F32>, grid, block, 0, stream,
+                                static_cast<const float*>(x), n, g, d, fmt,
+                                static_cast<uint8_t*>(q), scales);
 }
 
 cudaError_t launch_act8_load(const void* q, const float* scales, int64_t T, int d, pkm_q8 fmt,
@@ -100,14 +105,15 @@ cudaError_t launch_act8_load(const void* q, const float* scales, int64_t T, int 
   const int g = q8_groups(d);
   const int64_t n = T * g;
   if (n <= 0) return cudaSuccess;
-  if (dt == PKM_BF16)
-    act8_load_kernel<PKM_BF16><<<group_grid(n), kThreads, 0, stream>>>(
-        static_cast<const uint8_t*>(q), scales, n, g, d, fmt, static_cast<__nv_bfloat16*>(out));
-  else
-    act8_load_kernel<PKM_F32><<<group_grid(n), kThreads, 0, stream>>>(
-        static_cast<const uint8_t*>(q), scales, n, g, d, fmt, static_cast<float*>(out));
+  const dim3 grid(group_grid(n)), block(kThreads);
   note_launch();
-  return cudaGetLastError();
+  return dt == PKM_BF16
+             ? launch_maybe_pdl(true, act8_load_kernel<PKM_BF16>, grid, block, 0, stream,
+                                static_cast<const uint8_t*>(q), scales, n, g, d, fmt,
+                                static_cast<__nv_bfloat16*>(out))
+             : launch_maybe_pdl(true, act8_load_kernel<PKM_F32>, grid, block, 0, stream,
+                                static_cast<const uint8_t*>(q), scales, n, g, d, fmt,
+                                static_cast<float*>(out));
 }
 
 }  // namespace pkm

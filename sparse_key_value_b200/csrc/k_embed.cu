@@ -49,6 +49,8 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(
     const typename Elem<DT>::T* __restrict__ table, int64_t n_rows, int d, int lpr,
     const int32_t* __restrict__ ids, int64_t T, float scale, int has_pad, int32_t pad,
     typename Elem<DT>::T* __restrict__ out, int32_t* status) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / lpr;
   if (t >= T) return;
   const int l = threadIdx.x % lpr;
@@ -220,6 +222,8 @@ __device__ __forceinline__ void sort_clear(uint16_t* cnt, int bins) {
 template <int R>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedSort p,
                                                                   int32_t* status) {
+  pdl_launch_dependents();
+  pdl_wait();
   const uint32_t ncta = cluster_size(), rank = cluster_rank();
   if (sort_fills(p, ncta)) return;
   if (rank == 0 && threadIdx.x == 0) *p.n_cross = 0;
@@ -284,6 +288,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedSor
 // Longer lists, up to kSortMost tokens: the passes' lists in global memory.
 __global__ void __launch_bounds__(kSortThreads) embed_sort_long_kernel(const EmbedSort p,
                                                                        int32_t* status) {
+  pdl_launch_dependents();
+  pdl_wait();
   const uint32_t ncta = cluster_size(), rank = cluster_rank();
   if (sort_fills(p, ncta)) return;
   if (rank == 0 && threadIdx.x == 0) *p.n_cross = 0;
@@ -372,6 +378,8 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
     typename Elem<GT>::T* __restrict__ grad, float* __restrict__ first,
     float* __restrict__ last, int slices, int64_t n_sum, uint32_t* __restrict__ n_cross,
     uint32_t* __restrict__ cross, const EmbedFill fill) {
+  pdl_launch_dependents();
+  pdl_wait();
   if ((int64_t)blockIdx.x >= n_sum) {
     fill_rows<GT>(fill, blockIdx.x - n_sum, d, grad);
     return;
@@ -502,6 +510,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(
     const float* __restrict__ last, const uint32_t* __restrict__ n_cross,
     const uint32_t* __restrict__ cross) {
   __shared__ float part[kJoinWarps][32 * kUnit];
+  pdl_launch_dependents();
+  pdl_wait();
   const uint32_t n = *n_cross;
   for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
     join_one<GT>(cross[i], skey, T, d, scale, add, grad, first, last, part);
@@ -583,18 +593,18 @@ cudaError_t embed_sums(const pkm_embed_args* a, const EmbedLayout& L, char* ws,
   const int64_t n_fill = fill.bitmap ? (fill.n_rows - fill.first + 31) / 32 : 0;
   if (n_sum + n_fill > 0x7fffffff) return cudaErrorInvalidValue;
   uint32_t* cross = reinterpret_cast<uint32_t*>(ws + L.cross);
-  embed_sum_kernel<DT, GT><<<(unsigned)(n_sum + n_fill), kSumUnits, 0, st>>>(
+  note_launch();
+  const cudaError_t e = launch_maybe_pdl(
+      true, embed_sum_kernel<DT, GT>, dim3((unsigned)(n_sum + n_fill)), dim3(kSumUnits), 0, st,
       skey, spos, a->T, (uint32_t)a->n_rows, static_cast<const typename Elem<DT>::T*>(a->dout),
-      a->d, a->scale, a->accumulate, grad, first, last, slices, n_sum, cross,
-      cross + 1, fill);
+      a->d, a->scale, a->accumulate, grad, first, last, slices, n_sum, cross, cross + 1, fill);
+  // an id that the join sums covers three chunks
+  if (e != cudaSuccess || chunks < 3) return e;
+  const unsigned blocks = (unsigned)(chunks - 2 < kJoinBlocks ? chunks - 2 : kJoinBlocks);
   note_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || chunks < 2) return e;
-  const unsigned blocks = (unsigned)(chunks - 1 < kJoinBlocks ? chunks - 1 : kJoinBlocks);
-  embed_join_kernel<GT><<<dim3(blocks, (units + 31) / 32), 32 * kJoinWarps, 0, st>>>(
-      skey, a->T, a->d, a->scale, a->accumulate, grad, first, last, cross, cross + 1);
-  note_launch();
-  return cudaGetLastError();
+  return launch_maybe_pdl(true, embed_join_kernel<GT>, dim3(blocks, (units + 31) / 32),
+                          dim3(32 * kJoinWarps), 0, st, skey, a->T, a->d, a->scale, a->accumulate,
+                          grad, first, last, cross, cross + 1);
 }
 
 // The one-cluster sort; the rows below fill->first are zeroed beside it.
@@ -649,13 +659,15 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
   cfg.blockDim = dim3(kSortThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ncta;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, p, status);
   if (e == cudaSuccess) note_launch();
   return e;
@@ -697,11 +709,11 @@ cudaError_t embed_forward(const pkm_embed_args* a, int32_t* status, cudaStream_t
   using E = typename Elem<DT>::T;
   const int lpr = lanes_per_row(a->d);
   const int rows = kThreads / lpr;
-  embed_fwd_kernel<DT><<<(unsigned)((a->T + rows - 1) / rows), kThreads, 0, st>>>(
-      static_cast<const E*>(a->table), a->n_rows, a->d, lpr, a->ids, a->T, a->scale, a->has_pad,
-      a->pad_id, static_cast<E*>(a->out), status);
   note_launch();
-  return cudaGetLastError();
+  return launch_maybe_pdl(true, embed_fwd_kernel<DT>, dim3((unsigned)((a->T + rows - 1) / rows)),
+                          dim3(kThreads), 0, st, static_cast<const E*>(a->table), a->n_rows, a->d,
+                          lpr, a->ids, a->T, a->scale, a->has_pad, a->pad_id,
+                          static_cast<E*>(a->out), status);
 }
 
 }  // namespace

@@ -59,6 +59,8 @@ template <pkm_dtype DT, int NU, int WPR>
 __global__ void __launch_bounds__(block_threads(WPR)) norm_fwd_kernel(const NormFwd p) {
   using E = typename Elem<DT>::T;
   __shared__ float red[2 * block_threads(WPR) / 32];
+  pdl_launch_dependents();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kRows = block_threads(WPR) / 32 / WPR;
   const int64_t row = (int64_t)blockIdx.x * kRows + warp / WPR;
@@ -155,7 +157,8 @@ __global__ void __launch_bounds__(block_threads(WPR), bwd_per_sm(WPR))
   const int team = warp / WPR;
   const int col0 = ((warp % WPR) * 32 + lane) * kUnit;
   const int groups = q8_groups(p.d);
-  pdl_launch_dependents();  // the partials' sum waits for this kernel's end
+  pdl_launch_dependents();
+  pdl_wait();
   float dw[NU][8];
 #pragma unroll
   for (int c = 0; c < NU; ++c)
@@ -344,10 +347,10 @@ cudaError_t fwd_launch(const NormFwd& p, cudaStream_t st) {
   return norm_shape<4>(p.d, [&](auto nu, auto wpr) {
     constexpr int NU = decltype(nu)::value, WPR = decltype(wpr)::value;
     const int rows = rows_per_block(WPR);
-    norm_fwd_kernel<DT, NU, WPR>
-        <<<(unsigned)((p.T + rows - 1) / rows), block_threads(WPR), 0, st>>>(p);
     note_launch();
-    return cudaGetLastError();
+    return launch_maybe_pdl(true, norm_fwd_kernel<DT, NU, WPR>,
+                            dim3((unsigned)((p.T + rows - 1) / rows)), dim3(block_threads(WPR)), 0,
+                            st, p);
   });
 }
 
@@ -357,9 +360,9 @@ cudaError_t bwd_launch(const NormBwd& p, float* dweight, cudaStream_t st) {
   const int blocks = bwd_blocks(p.T, p.d, f32);
   const cudaError_t e = norm_shape<f32 ? 1 : 2>(p.d, [&](auto nu, auto wpr) {
     constexpr int NU = decltype(nu)::value, WPR = decltype(wpr)::value;
-    norm_bwd_kernel<DT, DY, NU, WPR><<<blocks, block_threads(WPR), 0, st>>>(p);
     note_launch();
-    return cudaGetLastError();
+    return launch_maybe_pdl(true, norm_bwd_kernel<DT, DY, NU, WPR>, dim3(blocks),
+                            dim3(block_threads(WPR)), 0, st, p);
   });
   if (e != cudaSuccess || !dweight) return e;
   note_launch();

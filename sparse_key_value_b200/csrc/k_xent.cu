@@ -144,6 +144,8 @@ __global__ void __launch_bounds__(kJoinThreads) xent_join_kernel(
     float* __restrict__ loss, float* __restrict__ lse, int32_t* status) {
   __shared__ float2 sm[kJoinThreads / 32][kJoinRows];
   constexpr int kStrips = kJoinThreads / kJoinRows, kAtOnce = 4;
+  pdl_launch_dependents();
+  pdl_wait();
   const int in = threadIdx.x % kJoinRows, strip = threadIdx.x / kJoinRows;
   const int64_t m = (int64_t)blockIdx.x * kJoinRows + in;
   MaxSum v{-INFINITY, 0.f};
@@ -386,10 +388,10 @@ cudaError_t xent_forward(const pkm_xent_args* a, int32_t* status, cudaStream_t s
   const PairProbs<1> p{{fwd_prob(a)}, 1, {}};
   const XentStats epi{a->T, a->V, p.p[0].tile_n, a->targets, part, picked};
   PKM_TRY((launch_pair_gemm<1>(maps, p, epi, status, st)));
-  xent_join_kernel<<<(unsigned)((a->T + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, st>>>(
-      part, p.p[0].tiles_n, a->T, a->V, a->targets, a->ignore_index, picked, a->loss, a->lse,
-      status);
-  PKM_TRY(cudaGetLastError());
+  PKM_TRY(launch_maybe_pdl(true, xent_join_kernel,
+                           dim3((unsigned)((a->T + kJoinRows - 1) / kJoinRows)),
+                           dim3(kJoinThreads), 0, st, part, p.p[0].tiles_n, a->T, a->V, a->targets,
+                           a->ignore_index, picked, a->loss, a->lse, status));
   return cudaSuccess;
 }
 
