@@ -287,6 +287,8 @@ struct EpiWarp {
 //   kBarArrivals          arrivals of the epilogue warps' own barriers (EpiWarp::bars)
 //   kDual                 two products over the same tile (see above)
 //   struct State          a warp's state over its tiles, zero-initialised
+//   setup(State&, w)      once, by all epilogue warps, before the first tile; they
+//                         may meet at named barrier 1 there
 //   begin(State&, w, prob, row0, n0, z)        before the buffer is ready
 //   tile(State&, w, prob, row0, n0, z, tmem, release)   by a whole warp: rows
 //       row0 + lane, columns n0 + kCols part .. at TMEM address `tmem` (lane
@@ -327,7 +329,7 @@ __device__ __forceinline__ void stage_out(const CUtensorMap* map, const EpiWarp&
 template <class Release>
 __device__ __forceinline__ void store_tile(const StoreOut& o, const CUtensorMap* map,
                                            const EpiWarp& w, int64_t row0, int n0, int z,
-                                           uint32_t tmem, Release release) {
+                                           uint32_t tmem, Release release, float scale = 1.f) {
   const int c0 = n0 + w.part * 64;
   if (row0 >= o.rows || c0 >= o.cols) {  // the whole warp
     release();
@@ -338,6 +340,8 @@ __device__ __forceinline__ void store_tile(const StoreOut& o, const CUtensorMap*
   tmem_ld_32x32b_x32(tmem + 32, r + 32);
   tmem_ld_wait();
   release();
+#pragma unroll
+  for (int j = 0; j < 64; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale);
   if (o.bf16) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -597,6 +601,7 @@ __global__ void __launch_bounds__(gp::threads<E>(), 1)
                     ctl->epi, &ctl->abort, status};
     const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + part * E::kCols;
     typename E::State state{};
+    epi.setup(state, w);
     uint32_t used[kBufs] = {0, 0};
     bool ok = true;
     for (int iter = 0; ok; ++iter) {

@@ -15,8 +15,12 @@
 //      rows that no token reads, so each row is written once.
 //   3. embed_join_kernel: the parts of an id that covers three chunks or more,
 //      joined in chunk order.
+// Lists of at most kRankMost tokens are sorted by counting, for each token, the
+// tokens before it in the sorted list (embed_rank_kernel): one pass without
+// barriers between blocks, and the filling blocks look into the list itself
+// instead of a bitmap.
 // No atomics on values: the same bits every run, and a frequent id spreads
-// over many blocks.  Bound by the gradient's write (n_rows * d), then by the
+// over many blocks (a short list's over the warps of a block).  Bound by the gradient's write (n_rows * d), then by the
 // launches' latency.  Lists of more than kSortMost tokens go through the
 // library's multi-block radix sort.
 #include "kernels.h"
@@ -30,6 +34,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 16;   // sorted tokens per block
 constexpr int kAhead = 8;    // rows of dout in flight per thread
+constexpr int kRankMost = 1024;   // tokens sorted by counting
 constexpr int kSortThreads = 1024;
 constexpr int kSortCluster = 8;
 constexpr int kSortRounds = 16;  // tokens per thread of the sorting cluster, at most
@@ -216,6 +221,51 @@ __device__ __forceinline__ void sort_clear(uint16_t* cnt, int bins) {
   __syncthreads();
 }
 
+// Sort by counting: token i's place is the number of tokens with a smaller key,
+// or the same key and an earlier position.  A block places 32 tokens, one per
+// lane, each warp counting over its eighth of the list.  The blocks after them
+// fill.
+constexpr int kRankWarps = 8;
+
+__global__ void __launch_bounds__(32 * kRankWarps) embed_rank_kernel(const EmbedSort p, int blocks,
+                                                                     int32_t* status) {
+  pdl_launch_dependents();
+  pdl_wait();
+  if ((int)blockIdx.x >= blocks) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int64_t i = (int64_t)(blockIdx.x - blocks) * 32 * kRankWarps + threadIdx.x;
+         i < p.fill_units; i += (int64_t)(gridDim.x - blocks) * 32 * kRankWarps)
+      __stcs(p.fill + i, zero);
+    return;
+  }
+  __shared__ __align__(16) uint32_t keys[kRankMost];
+  __shared__ int count[kRankWarps][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = (int)p.T;
+  if (blockIdx.x == 0 && tid == 0) *p.n_cross = 0;
+  for (int i = tid; i < kRankMost; i += 32 * kRankWarps)
+    keys[i] = i < T ? embed_key(p.ids[i], p.n_rows, p.has_pad, p.pad,
+                                blockIdx.x == 0 ? status : nullptr)
+                    : 0xffffffffu;  // after every key
+  __syncthreads();
+  const int me = blockIdx.x * 32 + lane;
+  const uint32_t k = keys[me < T ? me : 0];
+  const int each = ((T + kRankWarps - 1) / kRankWarps + 3) / 4 * 4;  // tokens per warp
+  int n = 0;
+  for (int j = warp * each; j < min(T, (warp + 1) * each); j += 4) {
+    const uint4 q = *reinterpret_cast<const uint4*>(keys + j);
+    n += (q.x < k) + (q.y < k) + (q.z < k) + (q.w < k);
+    n += (q.x == k && j < me) + (q.y == k && j + 1 < me) + (q.z == k && j + 2 < me) +
+         (q.w == k && j + 3 < me);
+  }
+  count[warp][lane] = n;
+  __syncthreads();
+  if (warp == 0 && me < T) {
+    for (int w = 1; w < kRankWarps; ++w) n += count[w][lane];
+    p.key[0][n] = k;
+    p.pos[0][n] = (uint32_t)me;
+  }
+}
+
 // Lists of at most R * kSortThreads tokens per CTA: tokens stay in registers
 // within a pass and pass to their next CTA through distributed shared memory,
 // so global memory (busy with the fill) is met only at both ends.
@@ -350,16 +400,33 @@ __device__ __forceinline__ void write_grad(typename Elem<GT>::T* g, const float*
 }
 
 struct EmbedFill {
-  const uint32_t* bitmap;  // null: nothing to fill
+  bool on;
+  const uint32_t* bitmap;  // rows that occur, or null: look into the sorted keys
   int64_t n_rows, first;   // rows first .. n_rows - 1; `first` is a multiple of 32
 };
 
-// Zeroes the rows of one bitmap word that no token reads.
+// Zeroes those of 32 rows that no token reads.
 template <pkm_dtype GT>
 __device__ __forceinline__ void fill_rows(const EmbedFill& f, int64_t block, int d,
+                                          const uint32_t* skey, int T,
                                           typename Elem<GT>::T* grad) {
   const int64_t r0 = f.first + block * 32;
-  const uint32_t used = f.bitmap[r0 >> 5];
+  uint32_t used;
+  if (f.bitmap) {
+    used = f.bitmap[r0 >> 5];
+  } else {
+    __shared__ uint32_t found;
+    if (threadIdx.x == 0) found = 0;
+    __syncthreads();
+    uint32_t mine = 0;
+    for (int i = threadIdx.x; i < T; i += kSumUnits) {
+      const int64_t r = (int64_t)skey[i] - r0;
+      if (r >= 0 && r < 32) mine |= 1u << r;
+    }
+    if (mine) atomicOr(&found, mine);
+    __syncthreads();
+    used = found;
+  }
   const uint32_t units = (uint32_t)(d / Elem<GT>::kVec);  // 16 bytes each
   const uint32_t rows = (uint32_t)min((int64_t)32, f.n_rows - r0);
   uint4* g = reinterpret_cast<uint4*>(grad + r0 * d);
@@ -381,7 +448,7 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
   pdl_launch_dependents();
   pdl_wait();
   if ((int64_t)blockIdx.x >= n_sum) {
-    fill_rows<GT>(fill, blockIdx.x - n_sum, d, grad);
+    fill_rows<GT>(fill, blockIdx.x - n_sum, d, skey, (int)T, grad);
     return;
   }
   // this chunk's keys and the next one's: [0] is the key before the chunk
@@ -509,7 +576,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(
     typename Elem<GT>::T* __restrict__ grad, const float* __restrict__ first,
     const float* __restrict__ last, const uint32_t* __restrict__ n_cross,
     const uint32_t* __restrict__ cross) {
-  __shared__ float part[kJoinWarps][32 * kUnit];
+  __shared__ __align__(16) float part[kJoinWarps][32 * kUnit];
   pdl_launch_dependents();
   pdl_wait();
   const uint32_t n = *n_cross;
@@ -549,7 +616,7 @@ EmbedLayout embed_layout(const pkm_embed_args* a) {
   L.skey = take(T * 4);
   L.spos = take(T * 4);
   L.radix = L.cluster ? 0 : take(radix_sort_workspace(a->T));
-  L.bitmap = L.cluster && !a->accumulate ? take((size_t)(a->n_rows + 31) / 32 * 4) : 0;
+  L.bitmap = L.cluster && a->T > kRankMost && !a->accumulate ? take((size_t)(a->n_rows + 31) / 32 * 4) : 0;
   L.cross = take((chunks + 1) * 4);  // count, then chunks
   L.first = take(chunks * d * 4);
   L.last = take(chunks * d * 4);
@@ -576,7 +643,7 @@ pkm_status embed_validate(const pkm_embed_args* a, bool backward) {
 
 // Rows that the sort's launch zeroes beside the sort: about as many bytes as
 // the memory takes in the sort's time.
-constexpr int64_t kFillBeside = int64_t(64) << 20;
+constexpr int64_t kFillBeside = int64_t(64) << 20, kFillBesideRank = int64_t(16) << 20;
 
 template <pkm_dtype DT, pkm_dtype GT>
 cudaError_t embed_sums(const pkm_embed_args* a, const EmbedLayout& L, char* ws,
@@ -590,7 +657,7 @@ cudaError_t embed_sums(const pkm_embed_args* a, const EmbedLayout& L, char* ws,
   const int units = a->d / kUnit;
   const int slices = (units + kSumUnits - 1) / kSumUnits;
   const int64_t n_sum = chunks * slices;
-  const int64_t n_fill = fill.bitmap ? (fill.n_rows - fill.first + 31) / 32 : 0;
+  const int64_t n_fill = fill.on ? (fill.n_rows - fill.first + 31) / 32 : 0;
   if (n_sum + n_fill > 0x7fffffff) return cudaErrorInvalidValue;
   uint32_t* cross = reinterpret_cast<uint32_t*>(ws + L.cross);
   note_launch();
@@ -619,8 +686,7 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
   const int bits = key_bits(a->n_rows);
   p.passes = (bits + kMaxDigit - 1) / kMaxDigit;
   p.digit = (bits + p.passes - 1) / p.passes;
-  // one CTA for lists that it holds in two rounds: no cluster barriers to wait for
-  const int ncta = a->T <= 2 * kSortThreads ? 1 : kSortCluster;
+  const int ncta = kSortCluster;
   p.rounds = (int)((a->T + (int64_t)ncta * kSortThreads - 1) / ((int64_t)ncta * kSortThreads));
   p.key[0] = reinterpret_cast<uint32_t*>(ws + L.skey);
   p.pos[0] = reinterpret_cast<uint32_t*>(ws + L.spos);
@@ -628,18 +694,29 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
   p.pos[1] = reinterpret_cast<uint32_t*>(ws + L.pos);
   p.n_cross = reinterpret_cast<uint32_t*>(ws + L.cross);
   int clusters = 1;
+  const bool by_rank = a->T <= kRankMost;
   if (!a->accumulate) {
-    p.bitmap = reinterpret_cast<uint32_t*>(ws + L.bitmap);
-    p.words = (a->n_rows + 31) / 32;
+    if (!by_rank) {
+      p.bitmap = reinterpret_cast<uint32_t*>(ws + L.bitmap);
+      p.words = (a->n_rows + 31) / 32;
+    }
     const int64_t row = (int64_t)a->d * (a->grad_dtype == PKM_F32 ? 4 : 2);
-    int64_t rows = kFillBeside / row / 32 * 32;
+    int64_t rows = (by_rank ? kFillBesideRank : kFillBeside) / row / 32 * 32;
     if (rows > a->n_rows) rows = a->n_rows / 32 * 32;
     p.fill = static_cast<uint4*>(a->grad);
     p.fill_units = rows * row / 16;
-    *fill = EmbedFill{p.bitmap, a->n_rows, rows};
+    *fill = EmbedFill{true, p.bitmap, a->n_rows, rows};
     const int64_t blocks = (p.fill_units + 4 * kSortThreads - 1) / (4 * kSortThreads);
     const int64_t want = (blocks + ncta - 1) / ncta, most = 136 / ncta;
     clusters += (int)(want < most ? want : most);
+  }
+  if (by_rank) {
+    const int blocks = (int)((a->T + 31) / 32);
+    const int64_t want = (p.fill_units + 8 * 256 - 1) / (8 * 256);
+    note_launch();
+    return launch_maybe_pdl(true, embed_rank_kernel,
+                            dim3((unsigned)(blocks + (want < 148 * 6 ? want : 148 * 6))),
+                            dim3(32 * kRankWarps), 0, st, p, blocks, status);
   }
   // rounds of the short sort: a power of two, the tokens of a CTA
   int short_rounds = 1;
@@ -674,6 +751,7 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
 }
 
 cudaError_t embed_backward(const pkm_embed_args* a, int32_t* status, cudaStream_t st) {
+  const bool b = a->dtype == PKM_BF16, gb = a->grad_dtype == PKM_BF16;
   const EmbedLayout L = embed_layout(a);
   char* ws = static_cast<char*>(a->workspace);
   EmbedFill fill{};
@@ -697,7 +775,6 @@ cudaError_t embed_backward(const pkm_embed_args* a, int32_t* status, cudaStream_
     e = launch_embed_sort(a, L, ws, &fill, status, st);
   }
   if (e != cudaSuccess) return e;
-  const bool b = a->dtype == PKM_BF16, gb = a->grad_dtype == PKM_BF16;
   return b ? (gb ? embed_sums<PKM_BF16, PKM_BF16>(a, L, ws, fill, st)
                  : embed_sums<PKM_BF16, PKM_F32>(a, L, ws, fill, st))
            : (gb ? embed_sums<PKM_F32, PKM_BF16>(a, L, ws, fill, st)

@@ -52,6 +52,7 @@ struct Memplus8Gate {
       if (m < T && col + 8 * u < dv)
         s.y[u] = *reinterpret_cast<const uint2*>(y8 + m * dv + col + 8 * u);
   }
+  __device__ __forceinline__ void setup(State&, const EpiWarp&) const {}
   __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int n0,
                                         int) const {
     const int c0 = n0 + w.part * kCols;
@@ -138,6 +139,7 @@ struct Memplus8Grads {
   static constexpr int kBarArrivals = 1;
   static constexpr bool kDual = false;
   struct State {};
+  __device__ __forceinline__ void setup(State&, const EpiWarp&) const {}
   __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
   template <class Release>

@@ -14,7 +14,10 @@
 // Backward: d for a piece of the vocabulary (recomputed logits, rounded to
 // bf16 once: the operand type of the products that read it, half a step of
 // each d), then both products in one launch; dx is summed over the pieces in
-// fp32, in piece order.
+// fp32, in piece order.  d is held over s = max |dloss| and the products are
+// multiplied by s in fp32: with equal weights the large terms are then near
+// -1, which bf16 holds, where all of -1 / n may sit on the same worst
+// rounding (2.6e-3 of dW's norm against 1.8e-3).
 // Bound by the tensor cores: 2 T V d operations forward, 6 T V d backward.
 #include <math.h>
 
@@ -55,6 +58,7 @@ struct XentStats {
     MaxSum v;
     int turn;
   };
+  __device__ __forceinline__ void setup(State&, const EpiWarp&) const {}
   __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int n0,
                                         int) const {
     if (n0 % tile_n) return;  // the tile's second buffer
@@ -185,22 +189,42 @@ struct XentDelta {
   const int32_t* target;
   int32_t ignore;
   const float *lse, *dloss;
+  float* scale;  // max |dloss| over the counted positions (1 if 0 or infinite): out
 
-  static constexpr int kWarps = 16, kCols = 64, kStages = 4, kSharedBytes = 0;
+  static constexpr int kWarps = 16, kCols = 64, kStages = 4, kSharedBytes = 64;
   static constexpr int kWarpBytes = kStageBytesPerWarp;
   static constexpr int kBarArrivals = 1;
   static constexpr bool kDual = false;
   struct State {
     int target;
-    float g, l2;
+    float g, l2, scale;
     bool counted;
   };
+  // Every CTA finds the same maximum while its first products run.
+  __device__ __forceinline__ void setup(State& s, const EpiWarp& w) const {
+    const int warp = w.part * 4 + w.quarter;
+    float m = 0.f;
+#pragma unroll 4
+    for (int64_t t = warp * 32 + w.lane; t < T; t += 32 * kWarps) {
+      const int32_t k = target[t];
+      if (k != ignore && k >= 0 && k < V) m = fmaxf(m, fabsf(dloss[t]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float* all = reinterpret_cast<float*>(w.shared);
+    if (w.lane == 0) all[warp] = m;
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) m = fmaxf(m, all[k]);
+    s.scale = m > 0.f && m < INFINITY ? m : 1.f;
+    if (blockIdx.x == 0 && warp == 0 && w.lane == 0) *scale = s.scale;
+  }
   __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int n0,
                                         int) const {
     const int64_t m = row0 + w.lane;
     s.target = m < T ? target[m] : ignore;
     s.counted = s.target != ignore && s.target >= 0 && s.target < V;
-    s.g = s.counted ? dloss[m] : 0.f;
+    s.g = s.counted ? dloss[m] / s.scale : 0.f;
     s.l2 = s.counted ? lse[m] * kLog2e : 0.f;
   }
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
@@ -259,18 +283,22 @@ struct XentDelta {
 struct XentGrads {
   CUtensorMap map[2];
   StoreOut out[2];
+  const float* scale;
 
   static constexpr int kWarps = 16, kCols = 64, kStages = 4, kSharedBytes = 0;
   static constexpr int kWarpBytes = kStageBytesPerWarp;
   static constexpr int kBarArrivals = 1;
   static constexpr bool kDual = false;
-  struct State {};
+  struct State {
+    float scale;
+  };
+  __device__ __forceinline__ void setup(State& s, const EpiWarp&) const { s.scale = *scale; }
   __device__ __forceinline__ void begin(State&, const EpiWarp&, int, int64_t, int, int) const {}
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
   template <class Release>
-  __device__ __forceinline__ void tile(State&, const EpiWarp& w, int prob, int64_t row0, int n0,
+  __device__ __forceinline__ void tile(State& s, const EpiWarp& w, int prob, int64_t row0, int n0,
                                        int z, uint32_t tmem, Release release) const {
-    store_tile(out[prob], &map[prob], w, row0, n0, z, tmem, release);
+    store_tile(out[prob], &map[prob], w, row0, n0, z, tmem, release, s.scale);
   }
 };
 
@@ -285,7 +313,7 @@ constexpr int kMaxSlices = 64;  // of dx
 
 struct XentLayout {  // of the backward
   int piece, ld, nz, tile_dx, tile_dw;
-  size_t delta, dx, total;
+  size_t delta, scale, dx, total;
 };
 
 PairProb fwd_prob(const pkm_xent_args* a) {
@@ -327,9 +355,10 @@ XentLayout xent_layout(const pkm_xent_args* a) {
   }
   L.ld = (L.piece + 63) / 64 * 64;
   L.delta = 0;
-  L.dx = rup(T * (size_t)L.ld * 2);
+  L.scale = rup((size_t)a->T * (size_t)L.ld * 2);
+  L.dx = L.scale + 256;
   const bool direct = L.nz == 1 && a->grad_dtype == PKM_F32;
-  L.total = L.dx + (direct ? 0 : rup((size_t)L.nz * T * (size_t)a->d * 4));
+  L.total = L.dx + (direct ? 0 : rup((size_t)L.nz * (size_t)a->T * (size_t)a->d * 4));
   return L;
 }
 
@@ -399,6 +428,7 @@ cudaError_t xent_backward(const pkm_xent_args* a, const XentLayout& L, int32_t* 
                           cudaStream_t st) {
   char* ws = static_cast<char*>(a->workspace);
   auto* delta = reinterpret_cast<__nv_bfloat16*>(ws + L.delta);
+  auto* scale = reinterpret_cast<float*>(ws + L.scale);
   const bool direct = L.nz == 1 && a->grad_dtype == PKM_F32;
   float* dx = direct ? static_cast<float*>(a->dx) : reinterpret_cast<float*>(ws + L.dx);
   const bool gb = a->grad_dtype == PKM_BF16;
@@ -410,7 +440,8 @@ cudaError_t xent_backward(const pkm_xent_args* a, const XentLayout& L, int32_t* 
         !pair_map(&m1.b[0], Wp, Vp, a->d, a->d, false))
       return cudaErrorInvalidValue;
     const PairProbs<1> p{{pair_prob(a->T, Vp, a->d, false, false, 1, 8)}, 1, {}};
-    XentDelta de{{}, a->T, Vp, v0, a->V, a->targets, a->ignore_index, a->lse, a->dloss};
+    XentDelta de{{}, a->T, Vp, v0, a->V, a->targets, a->ignore_index, a->lse, a->dloss,
+                 scale};
     if (!pair_out_map(&de.out, delta, Vp, a->T, 1, L.ld, PKM_BF16)) return cudaErrorInvalidValue;
     PKM_TRY((launch_pair_gemm<1>(m1, p, de, status, st)));
     PairMaps<2> m2;
@@ -422,7 +453,7 @@ cudaError_t xent_backward(const pkm_xent_args* a, const XentLayout& L, int32_t* 
     // a shorter last piece may fill fewer slices: the others keep their sums
     const PairProbs<2> q{{pair_prob(a->T, a->d, Vp, false, true, L.nz, 1, L.tile_dx),
                           pair_prob(Vp, a->d, (int)a->T, true, true, 1, 1, L.tile_dw)}, 1, {}};
-    XentGrads ge{{}, {{a->T, a->d, 0, v0 > 0}, {Vp, a->d, gb, 0}}};
+    XentGrads ge{{}, {{a->T, a->d, 0, v0 > 0}, {Vp, a->d, gb, 0}}, scale};
     if (!pair_out_map(&ge.map[0], dx, a->d, a->T, L.nz, a->d, PKM_F32) ||
         !pair_out_map(&ge.map[1], static_cast<char*>(a->dW) + (size_t)v0 * a->d * (gb ? 2 : 4),
                       a->d, Vp, 1, a->d, a->grad_dtype))

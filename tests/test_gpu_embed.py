@@ -65,12 +65,15 @@ def test_forward_and_backward(T, V, d, kind, dtype):
         _within(grad, ref, tol, f"grad {gdt}")
 
 
-@pytest.mark.parametrize("T,V,kind", [(4095, 131072, "zipf"), (4096, 300, "zipf"),
+@pytest.mark.parametrize("T,V,kind", [(1024, 131072, "zipf"), (1024, 2, "uniform"),
+                                      (1000, 40000, "same"), (1025, 3000, "zipf"),
+                                      (1030, 200, "same"), (2049, 7, "uniform"),
+                                      (4095, 131072, "zipf"), (4096, 300, "zipf"),
                                       (4097, 65536, "uniform"), (20000, 131071, "zipf"),
                                       (8300, 3, "uniform"), (5000, 70000, "same"),
                                       (131072, 700, "zipf"), (140001, 200000, "zipf")])
 def test_backward_many_tokens(T, V, kind):
-    """Long lists: several sort blocks, ids over many chunks, up to 18 key bits, and
+    """Both sides of the 1024 tokens that are sorted by counting; long lists: several sort blocks, ids over many chunks, up to 18 key bits, and
     more tokens than one cluster sorts."""
     d = 64
     g = torch.Generator().manual_seed(T)

@@ -99,8 +99,9 @@ def test_embed_refuses_by_direction(lib):
     assert bwd(dout=None) == 1 and bwd(grad=ODD) == 1 and bwd(grad_dtype=4) == 1
     assert bwd(T=0, grad=None) == 1
     assert bwd(workspace=None) == 6
-    need = lib.pkm_embed_workspace_size(ctypes.byref(_embed()))
-    assert need > 0 and bwd(workspace_bytes=need - 1) == 6
+    for T in (4, 1024, 1025, 200000):
+        need = lib.pkm_embed_workspace_size(ctypes.byref(_embed(T=T)))
+        assert need > 0 and bwd(T=T, workspace_bytes=need - 1) == 6
     assert fwd(T=0, ids=None) == 0
     assert fwd(T=0) == 0 and lib.pkm_embed_workspace_size(None) == 0
 
