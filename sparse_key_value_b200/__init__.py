@@ -439,14 +439,10 @@ def _embed_args(ids, n_rows, d, dtype, scale, pad_id) -> "_lib.EmbedArgs":
     _need_cuda(ids)
     if ids.dtype != torch.int32:
         raise TypeError("ids must be int32")
-    a = _lib.EmbedArgs()
-    a.T, a.n_rows, a.d, a.dtype, a.scale = ids.numel(), n_rows, d, dtype, scale
-    if pad_id is not None:
-        if not -2 ** 31 <= pad_id < 2 ** 31:  # ctypes would cut it silently
-            raise ValueError(f"pad_id {pad_id} is not an int32")
-        a.has_pad, a.pad_id = 1, pad_id
-    a.ids = _ptr(ids)
-    return a
+    if pad_id is not None and not -2 ** 31 <= pad_id < 2 ** 31:  # ctypes would cut it silently
+        raise ValueError(f"pad_id {pad_id} is not an int32")
+    return _lib.EmbedArgs(ids.numel(), n_rows, d, dtype, dtype, scale, pad_id is not None,
+                          pad_id or 0, 0, ids.data_ptr())
 
 
 def embedding_forward(table, ids, scale: float = 1.0, pad_id: Optional[int] = None, out=None,
