@@ -540,8 +540,10 @@ PKM_API pkm_status pkm_add_rmsnorm_backward(const pkm_norm_bwd_args *args, pkm_s
  * dout, grad and a workspace of pkm_embed_workspace_size bytes.
  * T = 0 is a valid empty call (the backward then zeroes grad unless it
  * accumulates).
- * Limits: d a multiple of 8, d <= 65536; T < 2^31 - 64 (PKM_ERR_UNSUPPORTED
- * above either); 1 <= n_rows < 2^31; scale not NaN.
+ * Limits: d a multiple of 8, d <= 65536; T < 2^31 - 64, and in the backward
+ * ceil(T / 16) * ceil(d / 1024) + n_rows / 32 < 2^31 (PKM_ERR_UNSUPPORTED
+ * above); 1 <= n_rows < 2^31; scale not NaN.  ids need only be 4-byte aligned
+ * (a slice of a token list).
  */
 typedef struct {
     int64_t T;
@@ -588,8 +590,9 @@ PKM_API pkm_status pkm_embed_backward(const pkm_embed_args *args, pkm_stream_t s
  * backward's holds one piece of d, at most 512 MiB or 1024 columns, and fp32
  * sums of dx).  Results are bitwise reproducible.
  * Limits: dtype PKM_BF16 (PKM_F32: PKM_ERR_UNSUPPORTED); d a multiple of 8,
- * d <= 65536; T <= 2^30; ceil(T / 256) * ceil(V / 256) < 2^30.  T = 0 is a
- * valid empty call (the backward then zeroes dW).
+ * d <= 65536; T, V <= 2^30; ceil(T / 256) * ceil(V / 256) < 2^30
+ * (PKM_ERR_UNSUPPORTED above).  T = 0 is a valid empty call (the backward then
+ * zeroes dW).  targets need only be 4-byte aligned.
  */
 typedef struct {
     int64_t T;

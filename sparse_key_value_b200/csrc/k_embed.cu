@@ -602,6 +602,11 @@ int key_bits(int64_t n_rows) {  // bits that hold the keys 0 .. n_rows
 
 size_t rup(size_t x) { return (x + 255) / 256 * 256; }
 bool need16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool need4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Blocks of the sums: chunks times column slices.
+int sum_slices(int d) { return (d / kUnit + kSumUnits - 1) / kSumUnits; }
+int64_t sum_blocks(int64_t T, int d) { return (T + kChunk - 1) / kChunk * sum_slices(d); }
 
 struct EmbedLayout {
   size_t keys, pos, skey, spos, radix, bitmap, cross, first, last, total;
@@ -639,9 +644,12 @@ pkm_status embed_validate(const pkm_embed_args* a, bool backward) {
   if (backward && a->grad_dtype != PKM_F32 && a->grad_dtype != PKM_BF16)
     return PKM_ERR_INVALID_ARG;
   if (a->T > (int64_t(1) << 31) - 64 || a->d > 65536) return PKM_ERR_UNSUPPORTED;
+  // the sums' grid and the blocks that zero rows share 31 bits
+  if (backward && sum_blocks(a->T, a->d) + (a->n_rows + 31) / 32 > 0x7fffffff)
+    return PKM_ERR_UNSUPPORTED;
   if (backward && !need16(a->grad)) return PKM_ERR_INVALID_ARG;
   if (a->T == 0) return PKM_OK;
-  if (!need16(a->ids)) return PKM_ERR_INVALID_ARG;
+  if (!need4(a->ids)) return PKM_ERR_INVALID_ARG;
   if (!backward) return need16(a->table) && need16(a->out) ? PKM_OK : PKM_ERR_INVALID_ARG;
   if (!need16(a->dout)) return PKM_ERR_INVALID_ARG;
   if (!need16(a->workspace) || a->workspace_bytes < embed_layout(a).total)
@@ -663,10 +671,9 @@ cudaError_t embed_sums(const pkm_embed_args* a, const EmbedLayout& L, char* ws,
   auto* grad = static_cast<typename Elem<GT>::T*>(a->grad);
   const int64_t chunks = (a->T + kChunk - 1) / kChunk;
   const int units = a->d / kUnit;
-  const int slices = (units + kSumUnits - 1) / kSumUnits;
-  const int64_t n_sum = chunks * slices;
+  const int slices = sum_slices(a->d);
+  const int64_t n_sum = sum_blocks(a->T, a->d);
   const int64_t n_fill = fill.on ? (fill.n_rows - fill.first + 31) / 32 : 0;
-  if (n_sum + n_fill > 0x7fffffff) return cudaErrorInvalidValue;
   uint32_t* cross = reinterpret_cast<uint32_t*>(ws + L.cross);
   note_launch();
   const cudaError_t e = launch_maybe_pdl(

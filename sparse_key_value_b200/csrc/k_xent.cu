@@ -6,18 +6,18 @@
 //   d[t, v] = (exp(logit[t, v] - lse[t]) - [v = target[t]]) dloss[t]
 //   dx = d W,  dW = d^T x
 //
-// Forward: the logits live in TMEM only.  Each tile's epilogue
-// reduces its columns to a running maximum and sum per row, a small kernel
-// joins the tiles' partials.  Base 2 throughout: with
-// s = logit log2(e), a term is 2^(s - max) -- one multiply-add and one ex2 --
-// and the rounding of log2(e) scales every term alike (1.3e-8 of the logit).
+// Forward: the logits live in TMEM only.  Each tile's epilogue reduces its
+// columns to a running maximum and sum per row, a small kernel joins the tiles'
+// partials.  Base 2 throughout: with s = logit log2(e), a term is 2^(s - max)
+// -- one multiply-add and one ex2 -- and the rounding of log2(e) scales every
+// term alike (1.3e-8 of the logit).
 // Backward: d for a piece of the vocabulary (recomputed logits, rounded to
 // bf16 once: the operand type of the products that read it, half a step of
 // each d), then both products in one launch; dx is summed over the pieces in
 // fp32, in piece order.  d is held over s = max |dloss| and the products are
 // multiplied by s in fp32: with equal weights the large terms are then near
 // -1, which bf16 holds, where all of -1 / n may sit on the same worst
-// rounding (2.6e-3 of dW's norm against 1.8e-3).
+// rounding (2.6e-3 of dW's norm against 1.7e-3).
 // Bound by the tensor cores: 2 T V d operations forward, 6 T V d backward.
 #include <math.h>
 
@@ -118,8 +118,9 @@ struct XentStats {
     }
     if (n0 % tile_n + gp::kN < tile_n && n0 + gp::kN < V) return;  // the second buffer follows
     __syncwarp();
-    // two sets of slots in turn: a set is written again only after the tile in
-    // between, whose buffers the joining warp has handed back after its reads
+    // two sets of slots in turn: a set is written again two tiles on, whose
+    // products need the buffers of the tile in between, and those the joining
+    // warp hands back only after it has read this set
     float2* slot = reinterpret_cast<float2*>(w.shared) + (st.turn & 1) * 4 * 128;
     slot[w.part * 128 + w.quarter * 32 + w.lane] = make_float2(st.v.mx, st.v.sum);
     __syncwarp();
@@ -305,6 +306,7 @@ struct XentGrads {
 // ------------------------------------------------------------ host side
 
 bool need16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool need4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 size_t rup(size_t x) { return (x + 255) / 256 * 256; }
 
 constexpr int64_t kPieceBytes = int64_t(512) << 20;  // most that a piece's d may take
@@ -368,7 +370,7 @@ pkm_status xent_sizes(const pkm_xent_args* a) {
     return a->dtype == PKM_F32 ? PKM_ERR_UNSUPPORTED : PKM_ERR_INVALID_ARG;
   if (a->grad_dtype != PKM_F32 && a->grad_dtype != PKM_BF16) return PKM_ERR_INVALID_ARG;
   // tile counts and tensor-map coordinates stay in 31 bits
-  if (a->T > (int64_t(1) << 30) || a->d > 65536 ||
+  if (a->T > (int64_t(1) << 30) || a->V > (1 << 30) || a->d > 65536 ||
       ((a->T + 255) / 256) * (((int64_t)a->V + 255) / 256) >= (int64_t(1) << 30))
     return PKM_ERR_UNSUPPORTED;
   return PKM_OK;
@@ -386,7 +388,7 @@ pkm_status xent_validate(const pkm_xent_args* a, XentLayout* L) {  // L: of the 
   if (s != PKM_OK) return s;
   if (backward && !need16(a->dW)) return PKM_ERR_INVALID_ARG;
   if (a->T == 0) return PKM_OK;
-  if (!need16(a->x) || !need16(a->W) || !need16(a->targets) || !need16(a->lse))
+  if (!need16(a->x) || !need16(a->W) || !need4(a->targets) || !need16(a->lse))
     return PKM_ERR_INVALID_ARG;
   if (!backward && !need16(a->loss)) return PKM_ERR_INVALID_ARG;
   if (backward && (!need16(a->dloss) || !need16(a->dx))) return PKM_ERR_INVALID_ARG;

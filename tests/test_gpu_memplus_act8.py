@@ -168,8 +168,8 @@ def _lm_step(p, ids, targets, dloss, w):
     over the tied table.  Returns (loss, activations, gradients)."""
     T = ids.numel()
     scale = w.d_model ** 0.5
-    h0 = skv.embedding_forward(p["E"], ids, scale=scale)
-    n1 = skv.add_rmsnorm_forward(h0, p["g1"], fmt="int8")
+    h0 = skv.embedding_forward(p["E"], ids, scale=scale, pad_id=-100)
+    n1 = skv.add_rmsnorm_forward(h0, p["g1"], fmt="int8")  # rows without a token stay zero
     x = n1["y"]
     q = skv.qproj_forward(x, p["Wq"]).view(T, w.H, 2, w.d_half)
     y = torch.empty(T, w.d_v, dtype=BF, device="cuda")
@@ -190,8 +190,8 @@ def _lm_step(p, ids, targets, dloss, w):
     gr["Wq"] = qp["dWq"]
     b1 = skv.add_rmsnorm_backward(qp["dx"], n1["sum"], p["g1"], n1["rstd"], dsum=b2["dx"])
     gr["g1"] = b1["dweight"]
-    skv.embedding_backward(b1["dx"], ids, p["E"].shape[0], scale=scale, grad=gr["E"],
-                           accumulate=True)
+    skv.embedding_backward(b1["dx"], ids, p["E"].shape[0], scale=scale, pad_id=-100,
+                           grad=gr["E"], accumulate=True)
     return loss, dict(idx=idx), gr
 
 
@@ -216,9 +216,9 @@ def test_language_model_training_step():
     p = dict(E=rn(V, 128, std=128 ** -0.5), g1=1 + rn(128, std=0.1), g2=1 + rn(128, std=0.1),
              Wq=rn(128, w.H * 2 * w.d_half, std=128 ** -0.5), K=inp["subkeys"],
              V=(inp["values"].float() * 50).to(BF), W1=inp["W1"], W2=inp["W2"])
-    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
-    targets = ids.roll(-1)
-    targets[-20:] = -100
+    text = torch.randint(0, V, (T + 1,), generator=g, device="cuda", dtype=torch.int32)
+    text[-20:] = -100                       # the end is padding: no token, no target
+    ids, targets = text[:-1], text[1:]      # slices of one list, the second 4-byte aligned
     n = int((targets != -100).sum())
     dloss = torch.full((T,), 1.0 / n, device="cuda")
     loss, act, gr = _lm_step(p, ids, targets, dloss, w)
@@ -228,10 +228,10 @@ def test_language_model_training_step():
     r["V"] = p["V"][rows.long()].to(F64).requires_grad_()
     pos = torch.searchsorted(rows, act["idx"].long())
     norm = lambda h, wt: h * (h.square().mean(1, keepdim=True) + 1e-6) ** -0.5 * wt  # noqa: E731
-    h0 = r["E"][ids.long()] * 128 ** 0.5
+    h0 = r["E"][ids.long().clamp(min=0)] * 128 ** 0.5 * (ids >= 0)[:, None]
     x = norm(h0, r["g1"])
     q = (x @ r["Wq"]).view(T, w.H, 2, w.d_half)
-    unit = lambda t: t / t.norm(dim=-1, keepdim=True)  # noqa: E731
+    unit = lambda t: t / t.norm(dim=-1, keepdim=True).clamp(min=1e-12)  # noqa: E731
     half = w.d_half ** 0.5 * torch.einsum("thcd,hcnd->thcn", unit(q), unit(r["K"]))
     i = act["idx"].long()
     S = half[:, :, 0].gather(2, i // w.n_sub) + half[:, :, 1].gather(2, i % w.n_sub)

@@ -17,6 +17,7 @@ def lib():
 
 F = ctypes.c_void_p(1 << 20)         # 16-byte aligned, never dereferenced on the host
 ODD = ctypes.c_void_p((1 << 20) + 8)
+ODD2 = ctypes.c_void_p((1 << 20) + 2)  # for the 4-byte aligned id lists
 
 
 def _norm(**kw):
@@ -86,7 +87,7 @@ def _embed(**kw):
 @pytest.mark.parametrize("bad,code", [
     (dict(T=-1), 1), (dict(n_rows=0), 1), (dict(n_rows=2 ** 31), 1), (dict(d=4), 1),
     (dict(d=20), 1), (dict(dtype=9), 1), (dict(scale=float("nan")), 1), (dict(ids=None), 1),
-    (dict(ids=ODD), 1), (dict(T=2 ** 31), 2), (dict(d=65544), 2)])
+    (dict(ids=ODD2), 1), (dict(T=2 ** 31), 2), (dict(d=65544), 2)])
 def test_embed_refuses(lib, bad, code):
     assert lib.pkm_embed_forward(ctypes.byref(_embed(**bad)), None) == code
     assert lib.pkm_embed_backward(ctypes.byref(_embed(**bad)), None) == code
@@ -98,6 +99,7 @@ def test_embed_refuses_by_direction(lib):
     assert fwd(table=None) == 1 and fwd(out=ODD) == 1
     assert bwd(dout=None) == 1 and bwd(grad=ODD) == 1 and bwd(grad_dtype=4) == 1
     assert bwd(T=0, grad=None) == 1
+    assert bwd(T=2 ** 31 - 64, d=65536) == 2  # more blocks than a grid has
     assert bwd(workspace=None) == 6
     for T in (4, 1024, 1025, 200000):
         need = lib.pkm_embed_workspace_size(ctypes.byref(_embed(T=T)))
@@ -128,7 +130,8 @@ def _xent(**kw):
 @pytest.mark.parametrize("bad,code", [
     (dict(T=-1), 1), (dict(V=0), 1), (dict(d=4), 1), (dict(d=60), 1), (dict(dtype=3), 1),
     (dict(dtype=0), 2), (dict(grad_dtype=2), 1), (dict(x=None), 1), (dict(x=ODD), 1),
-    (dict(W=ODD), 1), (dict(targets=None), 1), (dict(lse=ODD), 1), (dict(d=65544), 2),
+    (dict(W=ODD), 1), (dict(targets=None), 1), (dict(targets=ODD2), 1), (dict(lse=ODD), 1),
+    (dict(d=65544), 2), (dict(V=2 ** 30 + 8), 2),
     (dict(T=2 ** 30 + 1), 2), (dict(T=2 ** 28, V=2 ** 20), 2), (dict(workspace=None), 6)])
 def test_xent_refuses(lib, bad, code):
     assert lib.pkm_linear_xent_forward(ctypes.byref(_xent(**bad)), None) == code
