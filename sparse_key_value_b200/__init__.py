@@ -11,6 +11,8 @@ never allocates.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 from typing import Optional
 
 import torch
@@ -411,12 +413,33 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _enqueue(fn: str, args, dev: torch.device, stream):
-    """Call the entry point with ``args`` on the tensors' device and stream."""
+def _on_stream(f):
+    """Gives ``f`` the keyword ``stream``: the whole call then runs with that
+    stream current, so what it allocates comes from the memory that the
+    allocator keeps for it.  A workspace taken from another stream's memory
+    could be handed out again, when the call returns, before its kernels have
+    run."""
+    @functools.wraps(f)
+    def call(*args, stream: Optional[torch.cuda.Stream] = None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        tensors = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)]
+        _need_cuda(*tensors)
+        _same_device(stream.device, *tensors)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+
+    call.__signature__ = inspect.Signature(
+        [*inspect.signature(f).parameters.values(),
+         inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
+    return call
+
+
+def _enqueue(fn: str, args, dev: torch.device):
+    """Call the entry point with ``args`` on the tensors' device and its
+    current stream."""
     f = getattr(load(), fn)
-    if stream is not None:
-        s = stream.cuda_stream
-    elif _raw_stream is not None:
+    if _raw_stream is not None:
         s = _raw_stream(dev.index)
     else:
         s = torch.cuda.current_stream(dev).cuda_stream
@@ -445,8 +468,8 @@ def _embed_args(ids, n_rows, d, dtype, scale, pad_id) -> "_lib.EmbedArgs":
                           pad_id or 0, 0, ids.data_ptr())
 
 
-def embedding_forward(table, ids, scale: float = 1.0, pad_id: Optional[int] = None, out=None,
-                      stream=None):
+@_on_stream
+def embedding_forward(table, ids, scale: float = 1.0, pad_id: Optional[int] = None, out=None):
     """out[t] = scale * table[ids[t]] (see pkm_embed_forward in include/pkm.h).
 
     table [n_rows, d], ids int32 of any shape; out [*ids.shape, d].
@@ -460,13 +483,14 @@ def embedding_forward(table, ids, scale: float = 1.0, pad_id: Optional[int] = No
     _shape("out", out, (*ids.shape, d), table.dtype)
     _same_device(dev, ids, out)
     a.table, a.out = _ptr(table), _ptr(out)
-    _enqueue("pkm_embed_forward", (ctypes.byref(a),), dev, stream)
+    _enqueue("pkm_embed_forward", (ctypes.byref(a),), dev)
     return out
 
 
+@_on_stream
 def embedding_backward(dout, ids, n_rows: int, scale: float = 1.0, pad_id: Optional[int] = None,
                        grad=None, accumulate: bool = False, grad_dtype=torch.float32,
-                       workspace=None, stream=None):
+                       workspace=None):
     """Gradient of embedding_forward's table (see pkm_embed_backward in
     include/pkm.h): grad[r] = scale * the sum of dout over the positions of r.
 
@@ -488,7 +512,7 @@ def embedding_backward(dout, ids, n_rows: int, scale: float = 1.0, pad_id: Optio
     _same_device(dev, ids, grad)
     a.dout, a.grad, a.workspace, a.workspace_bytes = _ptr(dout), _ptr(grad), _ptr(workspace), \
         workspace.numel() * workspace.element_size()
-    _enqueue("pkm_embed_backward", (ctypes.byref(a),), dev, stream)
+    _enqueue("pkm_embed_backward", (ctypes.byref(a),), dev)
     return grad
 
 
@@ -523,18 +547,20 @@ def _q8_check(name: str, q, scales):
     return T, d, fmt
 
 
-def act8_store(x, fmt: str = "int8", stream=None):
+@_on_stream
+def act8_store(x, fmt: str = "int8"):
     """x [T, d] in 8 bits (see pkm_act8_store in include/pkm.h): returns
     (q [T, d] float8_e4m3fn or int8, scales fp32 [T, ceil(d / 128)])."""
     _need_cuda(x)
     code, dtype = _q8_name(fmt)
     T, d = x.shape
     q, scales = _q8_empty(T, d, dtype, x.device)
-    _enqueue("pkm_act8_store", (_ptr(x), T, d, _dt(x), code, _ptr(q), _ptr(scales)), x.device, stream)
+    _enqueue("pkm_act8_store", (_ptr(x), T, d, _dt(x), code, _ptr(q), _ptr(scales)), x.device)
     return q, scales
 
 
-def act8_load(q, scales, dtype=torch.bfloat16, out=None, stream=None):
+@_on_stream
+def act8_load(q, scales, dtype=torch.bfloat16, out=None):
     """The values act8_store's (or add_rmsnorm_forward's) 8 bits stand for,
     exact in bf16."""
     T, d, fmt = _q8_check("act8", q, scales)
@@ -543,13 +569,13 @@ def act8_load(q, scales, dtype=torch.bfloat16, out=None, stream=None):
         out = torch.empty(T, d, dtype=dtype, device=q.device)
     _shape("out", out, (T, d))
     _same_device(q.device, out)
-    _enqueue("pkm_act8_load", (_ptr(q), _ptr(scales), T, d, fmt, _ptr(out), _dt(out)), q.device, stream)
+    _enqueue("pkm_act8_load", (_ptr(q), _ptr(scales), T, d, fmt, _ptr(out), _dt(out)), q.device)
     return out
 
 
+@_on_stream
 def add_rmsnorm_forward(x, weight=None, residual=None, eps: float = 1e-6,
-                        fmt: Optional[str] = None, want_y: bool = True, sum_out=None,
-                        stream=None):
+                        fmt: Optional[str] = None, want_y: bool = True, sum_out=None):
     """h = x + residual, y = h / rms(h) * weight (see pkm_add_rmsnorm_forward
     in include/pkm.h).
 
@@ -576,12 +602,13 @@ def add_rmsnorm_forward(x, weight=None, residual=None, eps: float = 1e-6,
         q, scales = _q8_empty(T, d, qdt, dev)
     a = _lib.NormArgs(T, d, _dt(x), eps, code, _ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y),
                       _ptr(q), _ptr(scales), _ptr(rstd))
-    _enqueue("pkm_add_rmsnorm_forward", (ctypes.byref(a),), dev, stream)
+    _enqueue("pkm_add_rmsnorm_forward", (ctypes.byref(a),), dev)
     return dict(sum=x if h is None else h, y=y, rstd=rstd, q8=q, scales=scales)
 
 
+@_on_stream
 def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, scales=None, want_dweight: bool = True,
-                         workspace=None, stream=None):
+                         workspace=None):
     """Backward of add_rmsnorm_forward (see pkm_add_rmsnorm_backward in
     include/pkm.h).
 
@@ -613,7 +640,7 @@ def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, scales=None, want_dwe
         workspace = _workspace(workspace, need, dev)
         a.workspace, a.workspace_bytes = _ptr(workspace), \
             workspace.numel() * workspace.element_size()
-    _enqueue("pkm_add_rmsnorm_backward", (ctypes.byref(a),), dev, stream)
+    _enqueue("pkm_add_rmsnorm_backward", (ctypes.byref(a),), dev)
     return dict(dx=dx, dweight=dweight)
 
 
@@ -631,7 +658,8 @@ def _xent_args(x, W, targets, ignore_index: int) -> "_lib.XentArgs":
     return a
 
 
-def linear_xent_forward(x, W, targets, ignore_index: int = -100, workspace=None, stream=None):
+@_on_stream
+def linear_xent_forward(x, W, targets, ignore_index: int = -100, workspace=None):
     """Cross entropy of the output layer without keeping the logits (see
     pkm_linear_xent_forward in include/pkm.h).
 
@@ -645,12 +673,13 @@ def linear_xent_forward(x, W, targets, ignore_index: int = -100, workspace=None,
     need = int(load().pkm_linear_xent_forward_workspace_size(ctypes.byref(a)))
     workspace = _workspace(workspace, need, dev)
     a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    _enqueue("pkm_linear_xent_forward", (ctypes.byref(a),), dev, stream)
+    _enqueue("pkm_linear_xent_forward", (ctypes.byref(a),), dev)
     return loss, lse
 
 
+@_on_stream
 def linear_xent_backward(x, W, targets, lse, dloss, ignore_index: int = -100,
-                         grad_dtype=torch.float32, dx=None, dW=None, workspace=None, stream=None):
+                         grad_dtype=torch.float32, dx=None, dW=None, workspace=None):
     """Gradients of linear_xent_forward (see pkm_linear_xent_backward in
     include/pkm.h): lse as the forward gave it, dloss fp32 [T] the upstream
     gradient of each position's loss.  Returns (dx [T, d], dW [V, d]) in
@@ -672,12 +701,13 @@ def linear_xent_backward(x, W, targets, lse, dloss, ignore_index: int = -100,
     need = int(load().pkm_linear_xent_backward_workspace_size(ctypes.byref(a)))
     workspace = _workspace(workspace, need, dev)
     a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    _enqueue("pkm_linear_xent_backward", (ctypes.byref(a),), dev, stream)
+    _enqueue("pkm_linear_xent_backward", (ctypes.byref(a),), dev)
     return dx, dW
 
 
+@_on_stream
 def memplus_backward_act8(x8, x_scales, W1, W2, y8, y_scales, dout, grad_dtype=torch.float32,
-                          workspace=None, stream=None):
+                          workspace=None):
     """Backward of the Memory+ block from 8-bit activations (see
     pkm_memplus_backward_act8 in include/pkm.h).
 
@@ -706,5 +736,5 @@ def memplus_backward_act8(x8, x_scales, W1, W2, y8, y_scales, dout, grad_dtype=t
     need = int(load().pkm_memplus_backward_act8_workspace_size(ctypes.byref(a)))
     workspace = _workspace(workspace, need, dev)
     a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    _enqueue("pkm_memplus_backward_act8", (ctypes.byref(a),), dev, stream)
+    _enqueue("pkm_memplus_backward_act8", (ctypes.byref(a),), dev)
     return dict(dy=dy, dx=dx, dW1=dW1, dW2=dW2)

@@ -185,3 +185,22 @@ def test_memplus_act8_workspace(lib):
         lib.pkm_linear_xent_backward_workspace_size(ctypes.byref(_xent(T=T)))
         lib.pkm_linear_xent_forward_workspace_size(ctypes.byref(_xent(T=T)))
     assert lib.pkm_memplus_backward_act8(ctypes.byref(_mp8(T=0, dW1=None)), None) == 1
+
+
+def test_binding_refuses_tensors_of_another_device_than_the_stream():
+    """``stream`` is a keyword; its device has to be the tensors' one."""
+    import inspect
+
+    import sparse_key_value_b200 as skv
+
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    x = torch.zeros(4, 64)
+    for f in (skv.act8_store, skv.add_rmsnorm_forward):
+        assert inspect.signature(f).parameters["stream"].kind is inspect.Parameter.KEYWORD_ONLY
+        with pytest.raises(ValueError):
+            f(x, stream=Stream())
+    # what the check compares: no CPU call can hold a tensor of another GPU
+    with pytest.raises(ValueError):
+        skv._same_device(Stream.device, x)
