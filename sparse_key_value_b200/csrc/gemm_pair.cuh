@@ -167,12 +167,6 @@ struct PairCtl {
   volatile int abort;
 };
 
-// ---- staging: an epilogue warp's 32 rows in shared memory, in the swizzled
-// layout of a tensor copy, so that a lane writes its own row's 16-byte pieces
-// without bank conflicts and the copy writes whole lines.  (Row-per-lane
-// stores to global memory touch 32 lines an instruction: for a 128 x 256 fp32
-// tile that alone took as long as the products of K = 1024.)
-
 // 2^x and 1 / x, as the hardware approximates them (2^-22 and 2^-23 relative;
 // subnormals flushed)
 __device__ __forceinline__ float ex2(float x) {
@@ -187,6 +181,12 @@ __device__ __forceinline__ float rcp(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
+// ---- staging: an epilogue warp's 32 rows in shared memory, in the swizzled
+// layout of a tensor copy, so that a lane writes its own row's 16-byte pieces
+// without bank conflicts and the copy writes whole lines.  (Row-per-lane
+// stores to global memory touch 32 lines an instruction: for a 128 x 256 fp32
+// tile that alone took as long as the products of K = 1024.)
+//
 // Piece j (of four, 16 bytes) of the lane's row: 32 bf16 or 16 fp32 columns,
 // rows of 64 bytes, 2 KiB a warp
 __device__ __forceinline__ unsigned char* stage64_at(unsigned char* buf, int lane, int j) {
@@ -725,11 +725,25 @@ inline bool pair_out_map(CUtensorMap* m, const void* base, int64_t cols, int64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Columns of a tile: 512, or 256 where those still leave no pair of SMs more
-// than one item (twice the SMs at work on a short batch).
-inline int pair_tile_n(int64_t M, int N, int64_t nz) {
-  const int64_t items = (M + 2 * gp::kM - 1) / (2 * gp::kM) * ((N + gp::kN - 1) / gp::kN) * nz;
-  return items <= 74 ? gp::kN : gp::kTileN;
+// Pairs of SMs that the host's plans count on (148 SMs).
+constexpr int kPlanPairs = 74;
+
+// A problem's item in units of one 256-column k-block: its products, and about
+// six such steps of the epilogue that nothing covers.
+inline int64_t pair_len(int64_t kb, int tile_n) { return kb * (tile_n / gp::kN) + 6; }
+
+// Columns of a tile of a launch's only problem, 512 or 256: those whose longest
+// pair of SMs has less to do.  Measured as the loss (us, 512 and 256 columns):
+// 8192 x 32768 x 1024 413 and 426, 256 x 32768 x 1024 22.9 and 24.6, but 37 x
+// 50021 x 512 23.3 and 21.0 (98 tiles of 512 on 74 pairs are two rounds, 196 of
+// 256 three of half the length).
+inline int pair_tile_n(int64_t M, int N, int K, int64_t nz) {
+  const int64_t rows = (M + 2 * gp::kM - 1) / (2 * gp::kM) * nz;
+  const int64_t kb = ((K + gp::kKB - 1) / gp::kKB + nz - 1) / nz;
+  const auto span = [&](int tn) {
+    return (rows * ((N + tn - 1) / tn) + kPlanPairs - 1) / kPlanPairs * pair_len(kb, tn);
+  };
+  return span(gp::kN) < span(gp::kTileN) ? gp::kN : gp::kTileN;
 }
 
 inline PairProb pair_prob(int64_t M, int N, int K, bool amn, bool bmn, int nz = 1,
@@ -741,7 +755,7 @@ inline PairProb pair_prob(int64_t M, int N, int K, bool amn, bool bmn, int nz = 
   p.N = N;
   p.K = K;
   p.tiles_m = (int)((M + 2 * gp::kM - 1) / (2 * gp::kM));
-  p.tile_n = tile_n ? tile_n : pair_tile_n(M, N, nz);
+  p.tile_n = tile_n ? tile_n : pair_tile_n(M, N, K, nz);
   p.tiles_n = (N + p.tile_n - 1) / p.tile_n;
   p.kb_per = per;
   p.nz = (kb + per - 1) / per;
@@ -751,13 +765,6 @@ inline PairProb pair_prob(int64_t M, int N, int K, bool amn, bool bmn, int nz = 
   return p;
 }
 inline int64_t pair_items(const PairProb& p) { return (int64_t)p.tiles_m * p.tiles_n * p.nz; }
-
-// Pairs of SMs that the host's plans count on (148 SMs).
-constexpr int kPlanPairs = 74;
-
-// A problem's item in units of one 256-column k-block: its products, and about
-// six such steps of the epilogue that nothing covers.
-inline int64_t pair_len(int64_t kb, int tile_n) { return kb * (tile_n / gp::kN) + 6; }
 
 // The longest pair's work when n0 items of len0 and n1 of len1 are dealt out
 // as pair_item does; *extra receives the best evening-out.

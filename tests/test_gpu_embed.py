@@ -88,6 +88,23 @@ def test_backward_many_tokens(T, V, kind):
     assert (a.cpu()[n[:, 0] == 0] == 0).all()
 
 
+@pytest.mark.parametrize("T", [2047, 2048, 2049])
+@pytest.mark.parametrize("kind", ["zipf", "same", "uniform"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_backward_at_the_end_of_counting(T, kind, accumulate):
+    """Both sides of the longest list that is sorted by counting."""
+    V, d = 5000, 72
+    g = torch.Generator().manual_seed(T)
+    ids, dout = _ids(g, T, V, kind), torch.randn(T, d, generator=g).to(BF)
+    base = torch.randn(V, d, generator=g) if accumulate else torch.zeros(V, d)
+    a = skv.embedding_backward(dout.cuda(), ids.cuda(), V, grad=base.cuda(), accumulate=accumulate)
+    ref = base.double().index_add_(0, ids.long(), dout.double())
+    mag = base.double().abs().index_add_(0, ids.long(), dout.double().abs())
+    n = torch.bincount(ids.long(), minlength=V)[:, None]
+    _within(a, ref, (n + 4) * U32 * mag, "grad")
+    assert torch.equal(a.cpu()[n[:, 0] == 0], base[n[:, 0] == 0])
+
+
 def test_padding_and_batch_shape():
     g = torch.Generator().manual_seed(2)
     V, d, pad = 50, 48, 7
