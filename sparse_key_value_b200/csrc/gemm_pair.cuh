@@ -16,7 +16,8 @@
 // A or B may be held K-major ([M][K]) or MN-major ([K][M]); one launch takes up
 // to three problems, so that the tiles of several products fill the GPU
 // together.  A dual epilogue takes two products over the same tile at once,
-// 256 columns of each, one per buffer.
+// 256 columns of each, one per buffer; it takes the first into registers while
+// the second is worked on, so that the next tile's first can follow at once.
 //
 //   warp 0      TMA producer of this CTA's halves
 //   warp 1      TMEM; in the leader, the MMA issuer
@@ -48,9 +49,17 @@ template <class E>
 constexpr int stage_bytes() {
   return kABytes + (E::kDual ? 1 : kBufs) * kBBytes;
 }
+// Warps before the epilogue's.  A dual epilogue holds a buffer in registers: its
+// two warpgroups take over registers of the first (40 + 2 * 232 = 3 * 168, what
+// the block is launched with), which its roles then have for themselves.
+template <class E>
+constexpr int lead_warps() {
+  return E::kDual ? 4 : 2;
+}
+constexpr int kLeadRegs = 40, kDualRegs = 232;
 template <class E>
 constexpr int threads() {
-  return 64 + 32 * E::kWarps;
+  return 32 * (lead_warps<E>() + E::kWarps);
 }
 // ring, staging of the epilogue warps, what they share, control words; the
 // first kilobyte aligns the ring (the swizzle goes by the address)
@@ -167,6 +176,16 @@ struct PairCtl {
   volatile int abort;
 };
 
+// Registers a thread, for a whole warpgroup
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // 2^x and 1 / x, as the hardware approximates them (2^-22 and 2^-23 relative;
 // subnormals flushed)
 __device__ __forceinline__ float ex2(float x) {
@@ -209,15 +228,14 @@ __device__ __forceinline__ void bulk_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 // this thread's tensor stores have read their shared memory
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-// The warp's staging buffer may be written again (lane 0 issues the stores).
+// The warp's staging buffer may be written again (lane 0 issues the stores):
+// all but the last BEHIND groups of stores have read theirs.
+template <int BEHIND = 0>
 __device__ __forceinline__ void stage_free(int lane) {
-  if (lane == 0) bulk_wait_read();
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(BEHIND) : "memory");
   __syncwarp();
 }
 // The warp's writes are visible to the copy that lane 0 issues next.
@@ -426,178 +444,183 @@ __global__ void __launch_bounds__(gp::threads<E>(), 1)
   const uint32_t tmem = ctl->tmem;
   pdl_wait();  // operands and outputs belong to the kernel before until here
 
-  if (warp == 0) {
-    // ------------------------------------------------------ TMA producer
-    const bool issue = elect_one();
-    uint32_t issued_mask = 0, issued_par = 0;
-    bool ok = true;
-    int stage = 0;
-    uint32_t phase = 0;
-    for (int iter = 0; ok; ++iter) {
-      const PairItem it = pair_turn<E>(probs, pair, pairs, iter);
-      if (it.prob < 0) break;
-      const PairProb& p = probs.p[it.prob];
-      const CUtensorMap* ta = &maps.a[it.prob];
-      const CUtensorMap* tb = &maps.b[it.prob];
-      const PairTile tc = pair_tile(p, it.idx);
-      const int am = (int)(tc.m0 + (int64_t)rank * kM);  // this CTA's rows
-      const int bn = tc.n0 + (int)rank * kNh;  // this CTA's half of a buffer's columns
-      const int bufs = pair_bufs<E>(p, tc);
-      const bool amn = p.amn, bmn = p.bmn;
-      const int kb0 = tc.z * p.kb_per;
-      const int kb1 = min(kb0 + p.kb_per, (p.K + kKB - 1) / kKB);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!warp_wait(&ctl->empty[stage], phase ^ 1, &ctl->abort, status)) {
-          ok = false;
-          break;
-        }
-        if (issue) {
-          unsigned char* sa = stages + stage * kStageBytes;
-          const int kc = kb * kKB;
-          const uint32_t bar = map_to(&ctl->full[stage], 0);
-          // the leader registers the bytes of both CTAs' copies; a copy of
-          // the partner's that lands first only takes the count below zero
-          if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * (kABytes + bufs * kBBytes));
-          if (amn) {
-#pragma unroll
-            for (int j = 0; j < kM / kBox; ++j)
-              tma_load_2d_pair(sa + j * kBox * 128, ta, bar, am + j * kBox, kc);
-          } else {
-            tma_load_2d_pair(sa, ta, bar, kc, am);
-          }
-          for (int u = 0; u < bufs; ++u) {
-            unsigned char* sb = sa + kABytes + u * kBBytes;
-            const int n = bn + u * kN;
-            if (bmn) {
-#pragma unroll
-              for (int j = 0; j < kNh / kBox; ++j)
-                tma_load_2d_pair(sb + j * kBox * 128, tb, bar, n + j * kBox, kc);
-            } else {
-              tma_load_2d_pair(sb, tb, bar, kc, n);
-            }
-          }
-        }
-        __syncwarp();
-        issued_mask |= 1u << stage;
-        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-    }
-    // on an abort the leader lets every copy it was told about land
-    if (!ok && leader) {
-      for (int s = 0; s < kStages; ++s)
-        if (issued_mask & (1u << s))
-          for (unsigned long long i = 0; i < kSpinLimit; ++i)
-            if (mbar_try_wait(&ctl->full[s], (issued_par >> s) & 1)) break;
-    }
-  } else if (warp == 1) {
-    // ----------------------------------------------- MMA issuer (leader)
-    if (leader) {
+  constexpr int kLead = gp::lead_warps<E>();
+  if (warp < kLead) {
+    if constexpr (E::kDual) reg_dec<kLeadRegs>();
+    if (warp == 0) {
+      // ------------------------------------------------------ TMA producer
       const bool issue = elect_one();
+      uint32_t issued_mask = 0, issued_par = 0;
       bool ok = true;
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t used0 = 0, used1 = 0;  // times each buffer was filled
       for (int iter = 0; ok; ++iter) {
         const PairItem it = pair_turn<E>(probs, pair, pairs, iter);
         if (it.prob < 0) break;
         const PairProb& p = probs.p[it.prob];
-        const bool amn = p.amn, bmn = p.bmn;
-        const uint32_t idesc = idesc_bf16_f32(2 * kM, kN) | (amn ? (1u << 15) : 0u) |
-                               (bmn ? (1u << 16) : 0u);
-        // one 16-deep step inside a k-block: 32 bytes along a K-major row,
-        // 16 lines of 128 bytes of an MN-major tile
-        const uint32_t astep = amn ? 2048 >> 4 : 32 >> 4, bstep = bmn ? 2048 >> 4 : 32 >> 4;
+        const CUtensorMap* ta = &maps.a[it.prob];
+        const CUtensorMap* tb = &maps.b[it.prob];
         const PairTile tc = pair_tile(p, it.idx);
+        const int am = (int)(tc.m0 + (int64_t)rank * kM);  // this CTA's rows
+        const int bn = tc.n0 + (int)rank * kNh;  // this CTA's half of a buffer's columns
+        const int bufs = pair_bufs<E>(p, tc);
+        const bool amn = p.amn, bmn = p.bmn;
         const int kb0 = tc.z * p.kb_per;
-        const int nkb = min(p.kb_per, (p.K + kKB - 1) / kKB - kb0);
-        const bool wide = pair_bufs<E>(p, tc) > 1;
-        const int b0 = E::kDual ? it.prob : 0;  // the (first) buffer
-        auto products = [&](int st, int u, bool first) {  // k-block in stage st, buffer u
-          const uint32_t sa = smem_u32(stages + st * kStageBytes);
-          const uint32_t sb = sa + kABytes + (E::kDual ? 0 : u) * kBBytes;
-          const uint64_t ad = amn ? smem_desc_mn128(sa) : smem_desc_k128(sa);
-          const uint64_t bd = bmn ? smem_desc_mn128(sb) : smem_desc_k128(sb);
-#pragma unroll
-          for (int kk = 0; kk < kKB / 16; ++kk)
-            tc_mma_f16_pair(tmem + (uint32_t)(u * kN), ad + kk * astep, bd + kk * bstep, idesc,
-                            !(first && kk == 0));
-        };
-        // both epilogues have drained the buffer's last tile
-        const uint32_t n_used = E::kDual && b0 ? used1 : used0;
-        if (!warp_wait(&ctl->acce[b0], (n_used & 1) ^ 1, &ctl->abort, status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        int back = 0, back_stage = stage;  // k-blocks the second buffer has had, its next stage
-        bool open = !wide;                 // the second buffer may be written
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!warp_wait(&ctl->full[stage], phase, &ctl->abort, status)) {
+        const int kb1 = min(kb0 + p.kb_per, (p.K + kKB - 1) / kKB);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!warp_wait(&ctl->empty[stage], phase ^ 1, &ctl->abort, status)) {
             ok = false;
             break;
           }
-          tc_fence_after();
           if (issue) {
-            products(stage, b0, kb == 0);
-            if (kb == nkb - 1) tc_commit_pair_both(&ctl->accf[b0]);
-            if (!wide) tc_commit_pair_both(&ctl->empty[stage]);  // both CTAs may refill the stage
+            unsigned char* sa = stages + stage * kStageBytes;
+            const int kc = kb * kKB;
+            const uint32_t bar = map_to(&ctl->full[stage], 0);
+            // the leader registers the bytes of both CTAs' copies; a copy of
+            // the partner's that lands first only takes the count below zero
+            if (leader) mbar_arrive_expect_tx(&ctl->full[stage], 2 * (kABytes + bufs * kBBytes));
+            if (amn) {
+  #pragma unroll
+              for (int j = 0; j < kM / kBox; ++j)
+                tma_load_2d_pair(sa + j * kBox * 128, ta, bar, am + j * kBox, kc);
+            } else {
+              tma_load_2d_pair(sa, ta, bar, kc, am);
+            }
+            for (int u = 0; u < bufs; ++u) {
+              unsigned char* sb = sa + kABytes + u * kBBytes;
+              const int n = bn + u * kN;
+              if (bmn) {
+  #pragma unroll
+                for (int j = 0; j < kNh / kBox; ++j)
+                  tma_load_2d_pair(sb + j * kBox * 128, tb, bar, n + j * kBox, kc);
+              } else {
+                tma_load_2d_pair(sb, tb, bar, kc, n);
+              }
+            }
           }
           __syncwarp();
-          if (wide) {
-            if (!open) {
-              // wait only when the ring is full or the tile's last k-block is in
-              const uint32_t par = (used1 & 1) ^ 1;
-              if (kb + 1 - back == kStages || kb == nkb - 1) {
-                if (!warp_wait(&ctl->acce[1], par, &ctl->abort, status)) {
-                  ok = false;
-                  break;
-                }
-                open = true;
-              } else {
-                open = __all_sync(0xffffffffu, mbar_test_wait(&ctl->acce[1], par));
-              }
-              if (open) tc_fence_after();
-            }
-            if (open)
-              for (; back <= kb; ++back) {
-                if (issue) {
-                  products(back_stage, 1, back == 0);
-                  tc_commit_pair_both(&ctl->empty[back_stage]);
-                }
-                __syncwarp();
-                if (++back_stage == kStages) back_stage = 0;
-              }
-          }
+          issued_mask |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (!ok) break;
-        if (b0)
-          ++used1;
-        else
-          ++used0;
-        if (wide) {
-          if (issue) tc_commit_pair_both(&ctl->accf[1]);
-          __syncwarp();
-          ++used1;
-        }
       }
-      // every MMA issued must complete before either CTA frees TMEM or exits
-      if (issue) tc_commit_pair_local(&ctl->drain);
-      __syncwarp();
-      for (unsigned long long i = 0; i < kSpinLimit; ++i)
-        if (mbar_try_wait(&ctl->drain, 0)) break;
+      // on an abort the leader lets every copy it was told about land
+      if (!ok && leader) {
+        for (int s = 0; s < kStages; ++s)
+          if (issued_mask & (1u << s))
+            for (unsigned long long i = 0; i < kSpinLimit; ++i)
+              if (mbar_try_wait(&ctl->full[s], (issued_par >> s) & 1)) break;
+      }
+    } else if (warp == 1) {
+      // ----------------------------------------------- MMA issuer (leader)
+      if (leader) {
+        const bool issue = elect_one();
+        bool ok = true;
+        int stage = 0;
+        uint32_t phase = 0;
+        uint32_t used0 = 0, used1 = 0;  // times each buffer was filled
+        for (int iter = 0; ok; ++iter) {
+          const PairItem it = pair_turn<E>(probs, pair, pairs, iter);
+          if (it.prob < 0) break;
+          const PairProb& p = probs.p[it.prob];
+          const bool amn = p.amn, bmn = p.bmn;
+          const uint32_t idesc = idesc_bf16_f32(2 * kM, kN) | (amn ? (1u << 15) : 0u) |
+                                 (bmn ? (1u << 16) : 0u);
+          // one 16-deep step inside a k-block: 32 bytes along a K-major row,
+          // 16 lines of 128 bytes of an MN-major tile
+          const uint32_t astep = amn ? 2048 >> 4 : 32 >> 4, bstep = bmn ? 2048 >> 4 : 32 >> 4;
+          const PairTile tc = pair_tile(p, it.idx);
+          const int kb0 = tc.z * p.kb_per;
+          const int nkb = min(p.kb_per, (p.K + kKB - 1) / kKB - kb0);
+          const bool wide = pair_bufs<E>(p, tc) > 1;
+          const int b0 = E::kDual ? it.prob : 0;  // the (first) buffer
+          auto products = [&](int st, int u, bool first) {  // k-block in stage st, buffer u
+            const uint32_t sa = smem_u32(stages + st * kStageBytes);
+            const uint32_t sb = sa + kABytes + (E::kDual ? 0 : u) * kBBytes;
+            const uint64_t ad = amn ? smem_desc_mn128(sa) : smem_desc_k128(sa);
+            const uint64_t bd = bmn ? smem_desc_mn128(sb) : smem_desc_k128(sb);
+  #pragma unroll
+            for (int kk = 0; kk < kKB / 16; ++kk)
+              tc_mma_f16_pair(tmem + (uint32_t)(u * kN), ad + kk * astep, bd + kk * bstep, idesc,
+                              !(first && kk == 0));
+          };
+          // both epilogues have drained the buffer's last tile
+          const uint32_t n_used = E::kDual && b0 ? used1 : used0;
+          if (!warp_wait(&ctl->acce[b0], (n_used & 1) ^ 1, &ctl->abort, status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          int back = 0, back_stage = stage;  // k-blocks the second buffer has had, its next stage
+          bool open = !wide;                 // the second buffer may be written
+          for (int kb = 0; kb < nkb; ++kb) {
+            if (!warp_wait(&ctl->full[stage], phase, &ctl->abort, status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (issue) {
+              products(stage, b0, kb == 0);
+              if (kb == nkb - 1) tc_commit_pair_both(&ctl->accf[b0]);
+              if (!wide) tc_commit_pair_both(&ctl->empty[stage]);  // both CTAs may refill the stage
+            }
+            __syncwarp();
+            if (wide) {
+              if (!open) {
+                // wait only when the ring is full or the tile's last k-block is in
+                const uint32_t par = (used1 & 1) ^ 1;
+                if (kb + 1 - back == kStages || kb == nkb - 1) {
+                  if (!warp_wait(&ctl->acce[1], par, &ctl->abort, status)) {
+                    ok = false;
+                    break;
+                  }
+                  open = true;
+                } else {
+                  open = __all_sync(0xffffffffu, mbar_test_wait(&ctl->acce[1], par));
+                }
+                if (open) tc_fence_after();
+              }
+              if (open)
+                for (; back <= kb; ++back) {
+                  if (issue) {
+                    products(back_stage, 1, back == 0);
+                    tc_commit_pair_both(&ctl->empty[back_stage]);
+                  }
+                  __syncwarp();
+                  if (++back_stage == kStages) back_stage = 0;
+                }
+            }
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+          if (!ok) break;
+          if (b0)
+            ++used1;
+          else
+            ++used0;
+          if (wide) {
+            if (issue) tc_commit_pair_both(&ctl->accf[1]);
+            __syncwarp();
+            ++used1;
+          }
+        }
+        // every MMA issued must complete before either CTA frees TMEM or exits
+        if (issue) tc_commit_pair_local(&ctl->drain);
+        __syncwarp();
+        for (unsigned long long i = 0; i < kSpinLimit; ++i)
+          if (mbar_try_wait(&ctl->drain, 0)) break;
+      }
     }
   } else {
     // ----------------------------------------------------------- epilogue
-    const int quarter = warp & 3, part = (warp - 2) >> 2;
-    const EpiWarp w{lane, quarter, part, staging + (warp - 2) * E::kWarpBytes, shared,
+    if constexpr (E::kDual) reg_inc<kDualRegs>();
+    const int quarter = warp & 3, part = (warp - kLead) >> 2;
+    const EpiWarp w{lane, quarter, part, staging + (warp - kLead) * E::kWarpBytes, shared,
                     ctl->epi, &ctl->abort, status};
     const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + part * E::kCols;
     typename E::State state{};
@@ -617,8 +640,21 @@ __global__ void __launch_bounds__(gp::threads<E>(), 1)
         const int n0 = tc.n0 + u * kN;
         epi.begin(state, w, it.prob, row0, n0, tc.z);
         bool got = mbar_wait_or_abort(&ctl->accf[u], used[u] & 1, &ctl->abort, status);
-        if (E::kDual && got)
-          got = mbar_wait_or_abort(&ctl->accf[1], used[u] & 1, &ctl->abort, status);
+        const auto release = [&](int b) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive_local_scope(map_to(&ctl->acce[b], 0));
+          __syncwarp();
+        };
+        if constexpr (E::kDual) {
+          if (__all_sync(0xffffffffu, got)) {
+            tc_fence_after();
+            epi.first(state, w, row0, n0, mine, [&] { release(0); });
+            got = mbar_wait_or_abort(&ctl->accf[1], used[u] & 1, &ctl->abort, status);
+          } else {
+            got = false;
+          }
+        }
         if (!__all_sync(0xffffffffu, got)) {
           epi.abandon(state, w);
           ok = false;
@@ -626,15 +662,8 @@ __global__ void __launch_bounds__(gp::threads<E>(), 1)
         }
         ++used[u];
         tc_fence_after();
-        epi.tile(state, w, it.prob, row0, n0, tc.z, mine + u * kN, [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            remote_arrive_local_scope(map_to(&ctl->acce[u], 0));
-            if (E::kDual) remote_arrive_local_scope(map_to(&ctl->acce[1], 0));
-          }
-          __syncwarp();
-        });
+        epi.tile(state, w, it.prob, row0, n0, tc.z, mine + (E::kDual ? 1 : u) * kN,
+                 [&] { release(E::kDual ? 1 : u); });
       }
     }
     if (E::kWarpBytes > 0) stage_free(lane);  // no store reads shared memory any more

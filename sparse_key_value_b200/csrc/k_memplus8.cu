@@ -9,17 +9,17 @@
 // is decoded where it is used.  One launch computes a and dz of the same tile,
 // each in its own accumulator, and its epilogue writes dy, da and z: neither a
 // nor dz nor an elementwise pass touches HBM.  (Two launches of 512-column
-// tiles with dz in fp32 between them measured 39 + 40 us at best, against 70 at
+// tiles with dz in fp32 between them measured 39 + 40 us at best, against 62 at
 // 16384 x 1024 x 1024, and 67 MB of workspace.)  da and z are rounded to bf16
 // once, the operand type of the three products that follow; those run in one
 // launch, the weight gradients (few tiles, a long contraction over the tokens)
 // cut into slices that are summed in order.
 // Bound by the tensor cores for long batches (10 T d_model d_v operations),
-// by launches for short ones.  Measured on one B200: 16384 x 1024 x 1024 182-187
-// us (0.93 PFLOP/s): reading x back 8.5, a and dz 70 (operands from L2: 64 bytes
-// per SM and cycle where each accumulator has 256 columns), the three products
-// 63 (1.6 PFLOP/s), the slices' sum 7, and starts and ends that do not overlap.
-// 1000 x 640 x 520: 32 us, four dependent launches.
+// by launches for short ones.  Measured on one B200: 16384 x 1024 x 1024 179 us
+// back to back (0.96 PFLOP/s, at the power limit), alone: reading x back 8.5, a
+// and dz 62 (operands from L2: 64 bytes per SM and cycle where each accumulator
+// has 256 columns; 11 for writing dy, da and z), the three products 63 (1.6
+// PFLOP/s), the slices' sum 7.  1000 x 640 x 520: 32 us, four dependent launches.
 #include <math.h>
 
 #include "gemm_pair.cuh"
@@ -31,7 +31,14 @@ namespace pkm {
 namespace {
 
 // a and dz in TMEM, y from memory -> dy, da, z, 32 columns at a time through
-// the warp's staging rows.  The lane's bytes of y for the next columns are
+// the warp's staging rows.  A lane takes its 128 columns of a into registers
+// while dz is still being worked on, so that a of the next tile can follow; the
+// columns move down one place a turn, which keeps the loop short and its
+// registers fixed (against a and dz read together: 16384 x 1024 x 1024 184 -> 180
+// us in all, the launch alone 76 -> 66 from cold caches; unrolled four times 181,
+// and 1000 x 640 x 520 34 us for 32, the longer code's first pass).  Two sets of
+// staging rows: with one, and five ring stages, the short batch took 33 us.
+// The lane's bytes of y for the next columns are
 // loaded while these are worked on, the tile's first before its products are
 // done; a warp's columns lie in one quantisation group, so a lane has one scale.
 struct Memplus8Gate {
@@ -42,12 +49,14 @@ struct Memplus8Gate {
   const uint8_t* y8;
   const float* y_scales;
 
-  static constexpr int kWarps = 8, kCols = 128, kStages = 5, kWarpBytes = 3 * kStageBytesPerWarp;
+  static constexpr int kWarps = 8, kCols = 128, kStages = 4, kWarpBytes = 6 * kStageBytesPerWarp;
   static constexpr int kSharedBytes = 0, kBarArrivals = 1;
   static constexpr bool kDual = true;
   struct State {
+    uint32_t a[kCols / 32][32];
     uint2 y[4];
     float scale;
+    int half;  // of the staging rows, used in turn
   };
 
   __device__ __forceinline__ void fetch(State& s, int64_t m, int col) const {
@@ -67,6 +76,22 @@ struct Memplus8Gate {
   }
   __device__ __forceinline__ void abandon(State&, const EpiWarp&) const {}
 
+  // the lane's row of a, from buffer 0
+  template <class Release>
+  __device__ __forceinline__ void first(State& s, const EpiWarp& w, int64_t row0, int n0,
+                                        uint32_t tmem, Release release) const {
+    const int c0 = n0 + w.part * kCols;
+    if (row0 < T && c0 < dv) {  // the whole warp
+      __syncwarp();             // the loads are warp-aligned
+#pragma unroll
+      for (int q = 0; q < kCols / 32; ++q)
+        if (q == 0 || c0 + q * 32 < dv) tmem_ld_32x32b_x32(tmem + q * 32, s.a[q]);
+      __syncwarp();
+      tmem_ld_wait();
+    }
+    release();
+  }
+
   template <class Release>
   __device__ __forceinline__ void tile(State& s, const EpiWarp& w, int, int64_t row0, int n0, int,
                                        uint32_t tmem, Release release) const {
@@ -79,10 +104,10 @@ struct Memplus8Gate {
     for (int q = 0; q < kCols / 32; ++q) {
       const int col = c0 + q * 32;
       const bool last = q + 1 == kCols / 32 || col + 32 >= dv;
-      uint32_t a[32], d[32];
-      __syncwarp();  // the loads are warp-aligned
-      tmem_ld_32x32b_x32(tmem + q * 32, a);
-      tmem_ld_32x32b_x32(tmem + gp::kN + q * 32, d);
+      const uint32_t* a = s.a[0];
+      uint32_t d[32];
+      __syncwarp();
+      tmem_ld_32x32b_x32(tmem + q * 32, d);
       uint2 yq[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) yq[u] = s.y[u];
@@ -90,7 +115,9 @@ struct Memplus8Gate {
       __syncwarp();
       tmem_ld_wait();
       if (last) release();
-      stage_free(w.lane);
+      stage_free<1>(w.lane);  // the stores of the turn before last
+      unsigned char* const stage = w.stage + s.half * 3 * kStageBytesPerWarp;
+      s.half ^= 1;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         float y[8], o[3][8];
@@ -117,18 +144,22 @@ struct Memplus8Gate {
         }
 #pragma unroll
         for (int k = 0; k < 3; ++k)
-          *reinterpret_cast<uint4*>(stage64_at(w.stage + k * kStageBytesPerWarp, w.lane, u)) =
+          *reinterpret_cast<uint4*>(stage64_at(stage + k * kStageBytesPerWarp, w.lane, u)) =
               pack16<PKM_BF16>(o[k]);
       }
       stage_ready();
       if (w.lane == 0) {
-        tma_store_3d(&dy_map, w.stage, col, (int)row0, 0);
-        tma_store_3d(&da_map, w.stage + kStageBytesPerWarp, col, (int)row0, 0);
-        tma_store_3d(&z_map, w.stage + 2 * kStageBytesPerWarp, col, (int)row0, 0);
+        tma_store_3d(&dy_map, stage, col, (int)row0, 0);
+        tma_store_3d(&da_map, stage + kStageBytesPerWarp, col, (int)row0, 0);
+        tma_store_3d(&z_map, stage + 2 * kStageBytesPerWarp, col, (int)row0, 0);
         bulk_commit();
       }
       __syncwarp();
       if (last) break;
+#pragma unroll
+      for (int k = 0; k + 1 < kCols / 32; ++k)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s.a[k][e] = s.a[k + 1][e];
     }
   }
 };
