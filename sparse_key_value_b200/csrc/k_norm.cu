@@ -15,10 +15,8 @@
 // quantisation group.
 // Measured on one B200: forward of 16384 x 1024 bf16 with a residual, both
 // outputs and the 8-bit copy 24 us (151 MB: 6.2 TB/s); backward of 8191 x 2048
-// bf16 with a second gradient 30.9 us with the weight gradient's join (134 MB:
-// 4.3 TB/s; the main kernel 24 us, held back by the row's sum between its loads
-// and its stores).  A backward with its loads by asynchronous copies into
-// shared memory took 45 us where the packed registers took 38.
+// bf16 with a second gradient 27.1 us with the weight gradient's join (134 MB:
+// 5.0 TB/s; the join and its launch take 3).
 #include <type_traits>
 
 #include "kernels.h"
@@ -35,12 +33,12 @@ constexpr int block_threads(int wpr) { return wpr * 32 > kNormThreads ? wpr * 32
 // Sum over the row's WPR warps (consecutive ones, a named barrier of their
 // own; `red` [2][warps], used in turn: the barrier of the next sum follows
 // every read of this one).  Fixed order: the same bits every run.
-template <int WPR>
+template <int WPR, int WARPS = block_threads(WPR) / 32>
 __device__ __forceinline__ float row_sum(float v, float* red, int turn) {
   v = warp_sum(v);
   if constexpr (WPR > 1) {
     const int warp = threadIdx.x >> 5;
-    float* r = red + (turn & 1) * (block_threads(WPR) / 32);
+    float* r = red + (turn & 1) * WARPS;
     if ((threadIdx.x & 31) == 0) r[warp] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WPR), "n"(32 * WPR) : "memory");
     v = 0.f;
@@ -48,6 +46,13 @@ __device__ __forceinline__ float row_sum(float v, float* red, int turn) {
     for (int w = 0; w < WPR; ++w) v += r[warp / WPR * WPR + w];
   }
   return v;
+}
+
+__device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(smem_u32(to)), "l"(from), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
 struct NormFwd {
@@ -268,6 +273,167 @@ __global__ void __launch_bounds__(block_threads(WPR), bwd_per_sm(WPR))
   }
 }
 
+// The backward of long batches of 16- or 32-bit h: a row's tensors come by bulk
+// copies into a ring of shared memory, so that up to 200 KB per SM are on their
+// way while rows are summed and written; registers hold a row only while it is
+// worked on.  One block per SM, kRingWarps / WPR teams of a row each, a ring of
+// up to kRingStages rows per team; the team's leader refills a place after the
+// row's sum, whose barrier follows the team's last read of it.
+// Against the rows straight into registers (bf16, second gradient, us): 8191 x
+// 2048 27.1 and 30.7, 4096 x 4096 27.2 and 34.8, 2048 x 8192 27.6 and 38.4, 30000
+// x 512 26.6 and 29.9; 40000 x 256 20.6 and 21.1, 100000 x 64 39.1 and 38.9.  20
+// warps took 28.9 at the first, 12 with a deeper ring 27.1 but 38.4 at the third.
+constexpr int kRingWarps = 16, kRingStages = 4;
+constexpr int kRingBytes = 200 * 1024;
+constexpr int ring_teams(int wpr) { return kRingWarps / wpr; }
+
+template <pkm_dtype DT, pkm_dtype DY, int NU, int WPR>
+__global__ void __launch_bounds__(32 * WPR * ring_teams(WPR), 1)
+    norm_bwd_ring_kernel(const NormBwd p, int stages, int32_t* status) {
+  using E = typename Elem<DT>::T;
+  using Ey = typename Elem<DY>::T;
+  constexpr int kTeams = ring_teams(WPR), kWarps = WPR * kTeams;
+  extern __shared__ __align__(128) unsigned char ring_raw[];
+  __shared__ __align__(8) uint64_t full[kTeams][kRingStages];
+  __shared__ float red[2 * kWarps];
+  __shared__ volatile int abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = warp / WPR;
+  const int col0 = ((warp % WPR) * 32 + lane) * kUnit;
+  const bool leads = threadIdx.x == team * WPR * 32;
+  const int d = p.d;
+  const uint32_t ny = (uint32_t)d * sizeof(Ey), nh = (uint32_t)d * sizeof(E);
+  const uint32_t row_bytes = ny + nh + (p.dsum ? nh : 0);
+  unsigned char* ring = ring_raw + (size_t)team * stages * row_bytes;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < kTeams; ++t)
+      for (int i = 0; i < kRingStages; ++i) mbar_init(&full[t][i], 1);
+    abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t step = (int64_t)gridDim.x * kTeams;
+  const int64_t row0 = (int64_t)blockIdx.x * kTeams + team;
+  auto copy = [&](int64_t row, int place) {  // the leader's
+    unsigned char* to = ring + (size_t)place * row_bytes;
+    uint64_t* bar = &full[team][place];
+    mbar_arrive_expect_tx(bar, row_bytes);
+    bulk_load(to, static_cast<const Ey*>(p.dy) + row * d, ny, bar);
+    bulk_load(to + ny, static_cast<const E*>(p.h) + row * d, nh, bar);
+    if (p.dsum) bulk_load(to + ny + nh, static_cast<const E*>(p.dsum) + row * d, nh, bar);
+  };
+  if (leads)
+    for (int i = 0; i < stages && row0 + i * step < p.T; ++i) copy(row0 + i * step, i);
+  Raw8<DT> w[NU];
+#pragma unroll
+  for (int c = 0; c < NU; ++c) {
+    const int col = col0 + c * (WPR * 32 * kUnit);
+    if (p.w && col < d) w[c].load(static_cast<const E*>(p.w) + col);
+  }
+  float dw[NU][8];
+#pragma unroll
+  for (int c = 0; c < NU; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[c][e] = 0.f;
+  float rstd = row0 < p.T ? p.rstd[row0] : 0.f;
+  int place = 0, turn = 0;
+  uint32_t parity = 0;
+  bool ok = true;
+  for (int64_t row = row0; row < p.T; row += step) {
+    const float rs = rstd;
+    if (row + step < p.T) rstd = p.rstd[row + step];
+    ok = ok && mbar_wait_or_abort(&full[team][place], parity, &abort, status);
+    const unsigned char* at = ring + (size_t)place * row_bytes;
+    Raw8<DY> dy[NU];
+    Raw8<DT> h[NU], ds[NU];
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      const int col = col0 + c * (WPR * 32 * kUnit);
+      dy[c].zero();
+      h[c].zero();
+      ds[c].zero();
+      if (col < d) {
+        dy[c].load(reinterpret_cast<const Ey*>(at) + col);
+        h[c].load(reinterpret_cast<const E*>(at + ny) + col);
+        if (p.dsum) ds[c].load(reinterpret_cast<const E*>(at + ny + nh) + col);
+      }
+    }
+    auto weigh = [&](int c, float* g) {
+      if (p.w && col0 + c * (WPR * 32 * kUnit) < d) {
+        float f[8];
+        w[c].unpack(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] *= f[e];
+      }
+    };
+    float dot = 0.f;
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      float g[8], n[8];
+      h[c].unpack(n);
+      dy[c].unpack(g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        n[e] *= rs;
+        dw[c][e] = fmaf(g[e], n[e], dw[c][e]);
+      }
+      weigh(c, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dot = fmaf(g[e], n[e], dot);
+    }
+    const float mean = row_sum<WPR, kWarps>(dot, red, turn++) / (float)d;
+    if constexpr (WPR == 1) __syncwarp();
+    if (leads && ok && row + stages * step < p.T) copy(row + stages * step, place);
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      const int col = col0 + c * (WPR * 32 * kUnit);
+      float g[8], n[8], o[8];
+      h[c].unpack(n);
+      dy[c].unpack(g);
+      weigh(c, g);
+      ds[c].unpack(o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] += rs * (g[e] - n[e] * rs * mean);
+      if (ok && col < d) store8<DT>(static_cast<E*>(p.dx) + row * d + col, o);
+    }
+    if (++place == stages) {
+      place = 0;
+      parity ^= 1;
+    }
+  }
+  // a team that gave up lets the copies that it was told about land
+  if (leads && !ok)
+    for (int i = 0; i < stages; ++i)
+      for (unsigned long long k = 0; k < kSpinLimit; ++k)
+        if (mbar_try_wait(&full[team][i], i < place ? parity ^ 1 : parity)) break;
+  if (!p.part) return;
+  __syncthreads();  // the ring is free: the teams' sums in order, one row per block
+  float* acc = reinterpret_cast<float*>(ring_raw);
+  constexpr int kCols = NU * WPR * 32 * kUnit;
+  if (team > 0) {
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      const int col = col0 + c * (WPR * 32 * kUnit);
+      store8<PKM_F32>(acc + (team - 1) * kCols + col, dw[c]);
+    }
+  }
+  __syncthreads();
+  if (team == 0) {
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      const int col = col0 + c * (WPR * 32 * kUnit);
+      if (col >= d) continue;
+#pragma unroll 4
+      for (int t = 1; t < kTeams; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[c][e] += acc[(t - 1) * kCols + col + e];
+      store8<PKM_F32>(p.part + (int64_t)blockIdx.x * d + col, dw[c]);
+    }
+  }
+}
+
 // dweight[c] = sum over blocks of part[block][c]: 32 columns per block, 16
 // row strides of several loads in flight, joined in order
 constexpr int kDwStrips = 16;
@@ -302,8 +468,8 @@ using Int = std::integral_constant<int, N>;
 // units a lane.  The forward holds four (no barrier up to 1024 columns).  The
 // backward, with three tensors and the weight gradient in registers, holds
 // two of bf16 and one of fp32: three blocks per SM then have more rows in
-// flight than two with four units (8191 x 2048 bf16: 30.9 us, two blocks of two
-// units 34.0, two of four 34.8).
+// flight than two with four units (8191 x 2048 bf16, without the ring: 30.9 us,
+// two blocks of two units 34.0, two of four 34.8).
 template <int UMAX, typename F>
 cudaError_t norm_shape(int d, F&& f) {
   if (d <= 256) return f(Int<1>{}, Int<1>{});
@@ -331,19 +497,35 @@ cudaError_t norm_shape(int d, F&& f) {
   }
 }
 
-// Blocks of the backward (each writes a partial weight gradient): what the SMs
-// hold at a time, at most one per group of rows.
-int bwd_blocks(int64_t T, int d, bool f32) {
-  int rows = 1, most = kSMs;
+// The rows that a team's ring holds, or 0 where the backward takes its rows
+// straight into registers: 8-bit h (rows of odd multiples of 8 bytes), short rows
+// and those of more warps than the ring's block has, batches of fewer than kRingRows rows
+// per team (the other path spreads those over more blocks; at 1500 and 740 x 2048
+// both end before the call's host side does).
+constexpr int kRingRows = 4;
+struct NormPlan {
+  int stages, blocks;
+};
+NormPlan bwd_plan(int64_t T, int d, bool f32, pkm_q8 fmt, int row_bytes) {
+  NormPlan plan{0, 1};
   const auto f = [&](auto, auto wpr) {
     constexpr int WPR = decltype(wpr)::value;
-    rows = rows_per_block(WPR);
-    most = kSMs * bwd_per_sm(WPR);
+    if constexpr (WPR <= kRingWarps) {
+      constexpr int kTeams = ring_teams(WPR);
+      int stages = kRingBytes / (kTeams * row_bytes);
+      if (stages > kRingStages) stages = kRingStages;
+      if (fmt == PKM_Q8_NONE && d > 256 && stages >= 2 && T >= (int64_t)kSMs * kTeams * kRingRows) {
+        plan = NormPlan{stages, kSMs};
+        return cudaSuccess;
+      }
+    }
+    const int rows = rows_per_block(WPR);
+    const int64_t b = (T + rows - 1) / rows, most = kSMs * bwd_per_sm(WPR);
+    plan.blocks = (int)(b < most ? b : most);
     return cudaSuccess;
   };
   f32 ? norm_shape<1>(d, f) : norm_shape<2>(d, f);
-  const int64_t b = (T + rows - 1) / rows;
-  return (int)(b < most ? b : most);
+  return plan;
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -361,13 +543,34 @@ cudaError_t fwd_launch(const NormFwd& p, cudaStream_t st) {
   });
 }
 
+int row_bytes(int d, pkm_dtype dt, pkm_dtype dy, bool dsum) {
+  const int b = dt == PKM_F32 ? 4 : 2, y = dy == PKM_F32 ? 4 : 2;
+  return d * (y + b + (dsum ? b : 0));
+}
+
 template <pkm_dtype DT, pkm_dtype DY>
-cudaError_t bwd_launch(const NormBwd& p, float* dweight, cudaStream_t st) {
+cudaError_t bwd_launch(const NormBwd& p, float* dweight, int32_t* status, cudaStream_t st) {
   constexpr bool f32 = DT == PKM_F32 || DY == PKM_F32;
-  const int blocks = bwd_blocks(p.T, p.d, f32);
+  const int bytes = row_bytes(p.d, DT, DY, p.dsum != nullptr);
+  const NormPlan plan = bwd_plan(p.T, p.d, f32, p.fmt, bytes);
+  const int blocks = plan.blocks;
   const cudaError_t e = norm_shape<f32 ? 1 : 2>(p.d, [&](auto nu, auto wpr) {
     constexpr int NU = decltype(nu)::value, WPR = decltype(wpr)::value;
     note_launch();
+    if constexpr (WPR <= kRingWarps) {
+      if (plan.stages) {
+        constexpr int kTeams = ring_teams(WPR);
+        const size_t ring = (size_t)kTeams * plan.stages * bytes;
+        const size_t sums = (size_t)(kTeams - 1) * NU * WPR * 32 * kUnit * 4;
+        const size_t smem = ring > sums ? ring : sums;
+        const cudaError_t set =
+            cudaFuncSetAttribute(norm_bwd_ring_kernel<DT, DY, NU, WPR>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        if (set != cudaSuccess) return set;
+        return launch_maybe_pdl(true, norm_bwd_ring_kernel<DT, DY, NU, WPR>, dim3(blocks),
+                                dim3(32 * WPR * kTeams), smem, st, p, plan.stages, status);
+      }
+    }
     return launch_maybe_pdl(true, norm_bwd_kernel<DT, DY, NU, WPR>, dim3(blocks),
                             dim3(block_threads(WPR)), 0, st, p);
   });
@@ -396,7 +599,8 @@ pkm_status fwd_validate(const pkm_norm_args* a) {
 size_t bwd_bytes(const pkm_norm_bwd_args* a) {
   if (a->T <= 0 || a->d < 8 || a->d > kMaxD) return 0;
   const bool f32 = a->dtype == PKM_F32 || a->dy_dtype == PKM_F32;
-  return (size_t)bwd_blocks(a->T, a->d, f32) * (size_t)a->d * 4;
+  // of the register path, whose blocks are the more: the same for every fmt and dsum
+  return (size_t)bwd_plan(a->T, a->d, f32, PKM_Q8_E4M3, 1).blocks * (size_t)a->d * 4;
 }
 
 pkm_status bwd_validate(const pkm_norm_bwd_args* a) {
@@ -450,13 +654,15 @@ PKM_API pkm_status pkm_add_rmsnorm_backward(const pkm_norm_bwd_args* a, pkm_stre
   const NormBwd p{a->T, a->d,      a->fmt,  a->dy, a->sum, a->weight, a->dsum,
                   a->scales, a->rstd, a->dx,
                   a->dweight ? static_cast<float*>(a->workspace) : nullptr};
+  int32_t* status = status_ptr();
+  if (!status) return PKM_ERR_CUDA;
   cudaError_t e;
   if (a->dtype == PKM_BF16)
-    e = a->dy_dtype == PKM_BF16 ? bwd_launch<PKM_BF16, PKM_BF16>(p, a->dweight, st)
-                                : bwd_launch<PKM_BF16, PKM_F32>(p, a->dweight, st);
+    e = a->dy_dtype == PKM_BF16 ? bwd_launch<PKM_BF16, PKM_BF16>(p, a->dweight, status, st)
+                                : bwd_launch<PKM_BF16, PKM_F32>(p, a->dweight, status, st);
   else
-    e = a->dy_dtype == PKM_BF16 ? bwd_launch<PKM_F32, PKM_BF16>(p, a->dweight, st)
-                                : bwd_launch<PKM_F32, PKM_F32>(p, a->dweight, st);
+    e = a->dy_dtype == PKM_BF16 ? bwd_launch<PKM_F32, PKM_BF16>(p, a->dweight, status, st)
+                                : bwd_launch<PKM_F32, PKM_F32>(p, a->dweight, status, st);
   return e == cudaSuccess ? PKM_OK : PKM_ERR_CUDA;
 }
 

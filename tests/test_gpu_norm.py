@@ -174,6 +174,28 @@ def test_backward_many_rows():
         _check_bwd(T, d, BF, BF, True, True, None, T)
 
 
+@pytest.mark.parametrize("T,d,dtype,dy_dtype,res,weight", [
+    (11900, 264, BF, BF, True, True), (11841, 512, BF, F32, False, True),
+    (5921, 1000, BF, BF, True, False), (2959, 2048, BF, BF, True, True),
+    (2963, 2048, BF, BF, False, True), (1300, 4096, BF, BF, True, True),
+    (600, 8192, BF, BF, True, True), (11845, 256 + 8, F32, F32, True, True),
+    (3001, 1024, F32, BF, True, True), (1201, 2040, F32, F32, False, True),
+    (700, 4096, F32, F32, True, True)])
+def test_backward_of_long_batches(T, d, dtype, dy_dtype, res, weight):
+    """Batches whose rows come through shared memory, and one just below; ends
+    that leave some of a block's teams without a row."""
+    a = _check_bwd(T, d, dtype, dy_dtype, res, weight, None, T + d)
+    b = _check_bwd(T, d, dtype, dy_dtype, res, weight, None, T + d)
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dweight"], b["dweight"])
+
+
+@pytest.mark.parametrize("T,d,dtype", [(2367, 2048, BF), (2368, 2048, BF), (9471, 64, BF),
+                                       (9472, 64, BF), (9473, 8, F32), (592, 4096, F32),
+                                       (593, 16384, BF)])
+def test_backward_where_the_path_changes(T, d, dtype):
+    _check_bwd(T, d, dtype, dtype, True, True, None, T)
+
+
 def test_backward_against_differences():
     """dx and dweight against central differences of the 64-bit forward."""
     g = torch.Generator().manual_seed(9)
