@@ -5,14 +5,15 @@
 // the distinct rows and the output.
 //
 // Backward: grad[r] = scale * sum of dout[t] over the tokens t with ids[t] = r,
-// every row of the table's gradient written.  Three launches:
+// every row of the table's gradient written.  Launches:
 //   1. embed_sort_kernel: one cluster sorts the tokens by id (stable radix
 //      sort, counts and tokens exchanged through distributed shared memory) and
-//      marks the rows that occur in a bitmap, while the other clusters already
-//      zero the first rows of the gradient.
+//      marks the rows that occur in a bitmap;
+//      embed_zero_kernel: meanwhile zeroes the first rows of the gradient on
+//      the other SMs (started early by programmatic dependent launch).
 //   2. embed_sum_kernel: the sorted list is cut into chunks of kChunk entries,
 //      one block sums a chunk's parts in order; the blocks after those zero the
-//      rows that no token reads, so each row is written once.
+//      other rows that no token reads.
 //   3. embed_join_kernel: the parts of an id that covers three chunks or more,
 //      joined in chunk order.
 // Lists of at most kRankMost tokens are sorted by counting, for each token, the
@@ -25,10 +26,9 @@
 // over many blocks (a short list's over the warps of a block).
 // Measured on one B200: forward of 16384 x 1024 bf16 9.7 us (48 MB distinct:
 // 4.9 TB/s, the rest in L2); gradient of those tokens over 131072 x 1024 fp32
-// 113 us, bound by the write of its 537 MB (5.0 TB/s over all three launches:
-// the sort's 17 us go beside the first 64 MiB of zeros, sum and fill run at 6.3
-// TB/s, the join takes 4); 509 tokens over 32003 x 520 17 us, bound by the
-// launches' latency.
+// 98 us, bound by the write of its 537 MB (5.8 TB/s with reading dout, over all
+// launches: the sort's 17 us go beside the first 112 MiB of zeros); 65536 tokens
+// 172 us; 509 tokens over 32003 x 520 17 us, bound by the launches.
 #include "kernels.h"
 #include "q8.cuh"
 #include "tc_pair.cuh"
@@ -42,14 +42,15 @@ constexpr int kChunk = 16;   // sorted tokens per block
 constexpr int kAhead = 8;    // rows of dout in flight per thread
 // Tokens sorted by counting, at most.  The whole gradient over 32768 x 1024
 // fp32, by counting and by the cluster: 512 tokens 28.6 and 36.8 us, 1024 32.2
-// and 38.6, 2048 35.0 and 38.4, 4096 48.3 and 39.9 (counting is quadratic).
+// and 38.6, 2048 35.0 and 38.4, 4096 48.3 and 39.9 (counting is quadratic; all of
+// these before the rows were zeroed by warps).
 constexpr int kRankMost = 2048;
 constexpr int kSortThreads = 1024;
 constexpr int kSortCluster = 8;
 // Tokens per thread of the sorting cluster, at most.  The whole gradient over
 // 131072 x 1024 fp32, by the cluster and by the multi-block sort: 2048 tokens 89
 // and 167 us, 65536 213 and 260, 131072 339 and 344; twice as many over 131072 x
-// 512 476 and 380.
+// 512 476 and 380 (before the rows were zeroed by warps).
 constexpr int kSortRounds = 16;
 constexpr int64_t kSortMost = (int64_t)kSortThreads * kSortRounds * kSortCluster;
 constexpr int kMaxDigit = 9;     // bits per pass
@@ -141,7 +142,7 @@ struct EmbedSort {
   uint32_t* bitmap;           // rows that occur, or null
   int64_t words;
   uint32_t* n_cross;          // ids that cross chunks, counted by the sums; zeroed here
-  uint4* fill;                // zeroed by the clusters after the first, or null
+  uint4* fill;                // zeroed beside the sort, or null
   int64_t fill_units;
 };
 
@@ -225,16 +226,6 @@ __device__ __forceinline__ uint32_t digit_rank(uint16_t* mine, uint32_t d, bool 
   return before + __popc(peers & lt);
 }
 
-// Zeroes the fill region (clusters after the first).
-__device__ __forceinline__ bool sort_fills(const EmbedSort& p, uint32_t ncta) {
-  if (blockIdx.x < ncta) return false;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int64_t i = (int64_t)(blockIdx.x - ncta) * kSortThreads + threadIdx.x; i < p.fill_units;
-       i += (int64_t)(gridDim.x - ncta) * kSortThreads)
-    __stcs(p.fill + i, zero);
-  return true;
-}
-
 __device__ __forceinline__ void sort_clear(uint16_t* cnt, int bins) {
   uint4* c = reinterpret_cast<uint4*>(cnt);
   for (int b = threadIdx.x; b < 4 * bins; b += kSortThreads) c[b] = make_uint4(0, 0, 0, 0);
@@ -286,16 +277,31 @@ __global__ void __launch_bounds__(32 * kRankWarps) embed_rank_kernel(const Embed
   }
 }
 
+// Zeroes the first rows of the gradient while the sort before it runs, which
+// touches none of them; ends after it, so that who waits for this kernel has
+// waited for both.
+constexpr int kZeroUnits = 1024;  // of 16 bytes, per block and turn
+constexpr int kZeroBlocks = 4 * 140;  // at work at a time, beside the sort's eight
+__global__ void __launch_bounds__(kThreads) embed_zero_kernel(uint4* fill, int64_t units) {
+  pdl_launch_dependents();
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int64_t i0 = (int64_t)blockIdx.x * kZeroUnits + threadIdx.x; i0 < units;
+       i0 += (int64_t)gridDim.x * kZeroUnits)
+#pragma unroll
+    for (int u = 0; u < kZeroUnits / kThreads; ++u)
+      if (i0 + u * kThreads < units) __stcs(fill + i0 + u * kThreads, zero);
+  pdl_wait();
+}
+
 // Lists of at most R * kSortThreads tokens per CTA: tokens stay in registers
 // within a pass and pass to their next CTA through distributed shared memory,
 // so global memory (busy with the fill) is met only at both ends.
 template <int R>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedSort p,
                                                                   int32_t* status) {
+  pdl_wait();  // first: the zeros that start now touch what earlier kernels may use
   pdl_launch_dependents();
-  pdl_wait();
   const uint32_t ncta = cluster_size(), rank = cluster_rank();
-  if (sort_fills(p, ncta)) return;
   if (rank == 0 && threadIdx.x == 0) *p.n_cross = 0;
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int kOwn = R * kSortThreads;  // tokens of a CTA
@@ -359,10 +365,9 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const EmbedSor
 // Longer lists, up to kSortMost tokens: the passes' lists in global memory.
 __global__ void __launch_bounds__(kSortThreads) embed_sort_long_kernel(const EmbedSort p,
                                                                        int32_t* status) {
+  pdl_wait();  // first: the zeros that start now touch what earlier kernels may use
   pdl_launch_dependents();
-  pdl_wait();
   const uint32_t ncta = cluster_size(), rank = cluster_rank();
-  if (sort_fills(p, ncta)) return;
   if (rank == 0 && threadIdx.x == 0) *p.n_cross = 0;
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -448,12 +453,23 @@ __device__ __forceinline__ void fill_rows(const EmbedFill& f, int64_t block, int
     __syncthreads();
     used = found;
   }
-  const uint32_t units = (uint32_t)(d / Elem<GT>::kVec);  // 16 bytes each
-  const uint32_t rows = (uint32_t)min((int64_t)32, f.n_rows - r0);
-  uint4* g = reinterpret_cast<uint4*>(grad + r0 * d);
+  const int units = d / Elem<GT>::kVec;  // 16 bytes each
+  const int rows = (int)min((int64_t)32, f.n_rows - r0);
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (uint32_t i = threadIdx.x; i < rows * units; i += kSumUnits)
-    if (!(used >> (i / units) & 1)) __stcs(g + i, zero);
+  // a warp per row where its last turn leaves few lanes idle, else the rows as
+  // if they were one (with a division per store)
+  if ((units + 31) / 32 * 32 - units > units / 8) {
+    uint4* g = reinterpret_cast<uint4*>(grad + r0 * d);
+    for (int i = threadIdx.x; i < rows * units; i += kSumUnits)
+      if (!(used >> (i / units) & 1)) __stcs(g + i, zero);
+    return;
+  }
+  for (int r = threadIdx.x >> 5; r < rows; r += kSumUnits / 32) {
+    if (used >> r & 1) continue;
+    uint4* g = reinterpret_cast<uint4*>(grad + (r0 + r) * d);
+#pragma unroll 8
+    for (int i = threadIdx.x & 31; i < units; i += 32) __stcs(g + i, zero);
+  }
 }
 
 // The first n_sum blocks: one per chunk and slice of 8 * kSumUnits columns, a
@@ -465,7 +481,7 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
     uint32_t mark, const typename Elem<DT>::T* __restrict__ dout, int d, float scale, int add,
     typename Elem<GT>::T* __restrict__ grad, float* __restrict__ first,
     float* __restrict__ last, int slices, int64_t n_sum, uint32_t* __restrict__ n_cross,
-    uint32_t* __restrict__ cross, const EmbedFill fill) {
+    uint4* __restrict__ cross, const EmbedFill fill) {
   pdl_launch_dependents();
   pdl_wait();
   if ((int64_t)blockIdx.x >= n_sum) {
@@ -483,6 +499,10 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
     keys[j] = in ? skey[i] : mark;
     if (in && j >= 1 && j <= 2 * kChunk) rows[j - 1] = spos[i];
   }
+  // what the 32 chunks after this one begin with
+  const int64_t chunks = (T + kChunk - 1) / kChunk;
+  uint32_t ahead = mark;
+  if (threadIdx.x < 32 && c + 1 + threadIdx.x < chunks) ahead = skey[(c + 1 + threadIdx.x) * kChunk];
   // the key before the last chunk (mark sorts last, so it is no earlier key)
   const uint32_t before = i0 > kChunk ? skey[i0 - kChunk - 1] : mark;
   __syncthreads();
@@ -499,25 +519,38 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
                          !(keys[0] == tail && keys[1] == tail);
   if (goes_over && keys[2 * kChunk + 1] != tail)
     while (e1 < 2 * kChunk && keys[e1 + 1] == tail) ++e1;
-  if (goes_over && e1 == len && threadIdx.x == 0 && blockIdx.x % slices == 0)
-    cross[atomicAdd(n_cross, 1u)] = (uint32_t)c;  // entries stand for themselves: any order
+  if (goes_over && e1 == len && threadIdx.x < 32 && blockIdx.x % slices == 0) {
+    // chunks c + 1 .. stop - 1 hold the rest: 32 chunks looked at at a time
+    int64_t stop = c + 1;
+    uint32_t m = __ballot_sync(0xffffffffu, ahead == tail);
+    while (m == 0xffffffffu) {
+      stop += 32;
+      const int64_t q = stop + threadIdx.x;
+      m = __ballot_sync(0xffffffffu, q < chunks && skey[q * kChunk] == tail);
+    }
+    stop += __ffs(~m) - 1;
+    if (threadIdx.x == 0)  // entries stand for themselves: any order
+      cross[atomicAdd(n_cross, 1u)] = make_uint4((uint32_t)c, (uint32_t)stop, tail, 0);
+  }
   const int col = ((int)(blockIdx.x % slices) * kSumUnits + threadIdx.x) * kUnit;
   if (col >= d) return;
   float acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
   for (int j0 = e0; j0 < e1 && keys[j0 + 1] != mark; j0 += kAhead) {
-    float f[kAhead][8];
+    Raw8<DT> raw[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       if (j0 + u < e1 && keys[j0 + u + 1] != mark)
-        load8<DT>(dout + (int64_t)rows[j0 + u] * d + col, f[u]);
+        raw[u].load(dout + (int64_t)rows[j0 + u] * d + col);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int j = j0 + u;
       if (j >= e1 || keys[j + 1] == mark) break;
+      float f[8];
+      raw[u].unpack(f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += f[u][e];
+      for (int e = 0; e < 8; ++e) acc[e] += f[e];
       const uint32_t key = keys[j + 1];
       const bool goes_on = keys[j + 2] == key;
       if (goes_on && j + 1 < e1) continue;
@@ -534,30 +567,19 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
   }
 }
 
-// An id that begins in chunk c and goes on past the next: its parts in chunk
-// order, cut into a run of chunks per warp (a frequent id has many), the runs
+// An id that begins in chunk x and goes on past the next, to chunk y - 1: its
+// parts in chunk order, cut into a run of chunks per warp (a frequent id has many), the runs
 // joined in order.  The blocks share the sums' list of such ids.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinBlocks = 148;
 
 template <pkm_dtype GT>
-__device__ __forceinline__ void join_one(int64_t c, const uint32_t* skey, int64_t T, int d,
-                                         float scale, int add, typename Elem<GT>::T* grad,
-                                         const float* first, const float* last,
-                                         float (*part)[32 * kUnit]) {
-  const uint32_t key = skey[(c + 1) * kChunk];
+__device__ __forceinline__ void join_one(const uint4& id, int d, float scale, int add,
+                                         typename Elem<GT>::T* grad, const float* first,
+                                         const float* last, float (*part)[32 * kUnit]) {
+  const int64_t c = id.x, stop = id.y;
+  const uint32_t key = id.z;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // chunks c + 1 .. stop - 1 hold the rest: 32 chunks looked at at a time
-  const int64_t chunks = (T + kChunk - 1) / kChunk;
-  int64_t stop = c + 1;
-  for (;; stop += 32) {
-    const int64_t q = stop + lane;  // chunk q begins with the id
-    const uint32_t m = __ballot_sync(0xffffffffu, q < chunks && skey[q * kChunk] == key);
-    if (m != 0xffffffffu) {
-      stop += __ffs(~m) - 1;
-      break;
-    }
-  }
   const int64_t run = (stop - c - 1 + kJoinWarps - 1) / kJoinWarps;
   const int64_t q1 = c + 1 + warp * run, q2 = min(stop, q1 + run);
   const int col = (blockIdx.y * 32 + lane) * kUnit;
@@ -593,16 +615,18 @@ __device__ __forceinline__ void join_one(int64_t c, const uint32_t* skey, int64_
 
 template <pkm_dtype GT>
 __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(
-    const uint32_t* __restrict__ skey, int64_t T, int d, float scale, int add,
-    typename Elem<GT>::T* __restrict__ grad, const float* __restrict__ first,
-    const float* __restrict__ last, const uint32_t* __restrict__ n_cross,
-    const uint32_t* __restrict__ cross) {
+    int d, float scale, int add, typename Elem<GT>::T* __restrict__ grad,
+    const float* __restrict__ first, const float* __restrict__ last,
+    const uint32_t* __restrict__ n_cross, const uint4* __restrict__ cross) {
   __shared__ __align__(16) float part[kJoinWarps][32 * kUnit];
   pdl_launch_dependents();
   pdl_wait();
+  // the block's first entry (there are as many places as blocks) beside the count
+  uint4 id = cross[blockIdx.x];
   const uint32_t n = *n_cross;
   for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
-    join_one<GT>(cross[i], skey, T, d, scale, add, grad, first, last, part);
+    if (i != blockIdx.x) id = cross[i];
+    join_one<GT>(id, d, scale, add, grad, first, last, part);
     __syncthreads();  // `part` may be written again
   }
 }
@@ -643,7 +667,7 @@ EmbedLayout embed_layout(const pkm_embed_args* a) {
   L.spos = take(T * 4);
   L.radix = L.cluster ? 0 : take(radix_sort_workspace(a->T));
   L.bitmap = L.cluster && a->T > kRankMost && !a->accumulate ? take((size_t)(a->n_rows + 31) / 32 * 4) : 0;
-  L.cross = take((chunks + 1) * 4);  // count, then chunks
+  L.cross = take((chunks + 1) * 16);  // count, then ids over three chunks or more
   L.first = take(chunks * d * 4);
   L.last = take(chunks * d * 4);
   L.total = off;
@@ -670,9 +694,11 @@ pkm_status embed_validate(const pkm_embed_args* a, bool backward) {
   return PKM_OK;
 }
 
-// Rows that the sort's launch zeroes beside the sort: about as many bytes as
-// the memory takes in the sort's time.
-constexpr int64_t kFillBeside = int64_t(64) << 20, kFillBesideRank = int64_t(16) << 20;
+// Rows zeroed beside the sort: about as many bytes as the memory takes in the
+// sort's time (16384 tokens over 131072 x 1024: 64 MiB 104 us, 96 101.2, 128
+// 100.4; 4096 over 32768 x 1024 33.8, 31.0, 31.5, all before the join got its
+// ids' ends from the sums).
+constexpr int64_t kFillBeside = int64_t(112) << 20, kFillBesideRank = int64_t(16) << 20;
 
 template <pkm_dtype DT, pkm_dtype GT>
 cudaError_t embed_sums(const pkm_embed_args* a, const EmbedLayout& L, char* ws,
@@ -687,19 +713,20 @@ cudaError_t embed_sums(const pkm_embed_args* a, const EmbedLayout& L, char* ws,
   const int slices = sum_slices(a->d);
   const int64_t n_sum = sum_blocks(a->T, a->d);
   const int64_t n_fill = fill.on ? (fill.n_rows - fill.first + 31) / 32 : 0;
-  uint32_t* cross = reinterpret_cast<uint32_t*>(ws + L.cross);
+  uint32_t* n_cross = reinterpret_cast<uint32_t*>(ws + L.cross);
+  uint4* cross = reinterpret_cast<uint4*>(ws + L.cross) + 1;
   note_launch();
   const cudaError_t e = launch_maybe_pdl(
       true, embed_sum_kernel<DT, GT>, dim3((unsigned)(n_sum + n_fill)), dim3(kSumUnits), 0, st,
       skey, spos, a->T, (uint32_t)a->n_rows, static_cast<const typename Elem<DT>::T*>(a->dout),
-      a->d, a->scale, a->accumulate, grad, first, last, slices, n_sum, cross, cross + 1, fill);
+      a->d, a->scale, a->accumulate, grad, first, last, slices, n_sum, n_cross, cross, fill);
   // an id that the join sums covers three chunks
   if (e != cudaSuccess || chunks < 3) return e;
   const unsigned blocks = (unsigned)(chunks - 2 < kJoinBlocks ? chunks - 2 : kJoinBlocks);
   note_launch();
   return launch_maybe_pdl(true, embed_join_kernel<GT>, dim3(blocks, (units + 31) / 32),
-                          dim3(32 * kJoinWarps), 0, st, skey, a->T, a->d, a->scale, a->accumulate,
-                          grad, first, last, cross, cross + 1);
+                          dim3(32 * kJoinWarps), 0, st, a->d, a->scale, a->accumulate, grad, first, last,
+                          n_cross, cross);
 }
 
 // The one-cluster sort; the rows below fill->first are zeroed beside it.
@@ -721,7 +748,6 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
   p.key[1] = reinterpret_cast<uint32_t*>(ws + L.keys);
   p.pos[1] = reinterpret_cast<uint32_t*>(ws + L.pos);
   p.n_cross = reinterpret_cast<uint32_t*>(ws + L.cross);
-  int clusters = 1;
   const bool by_rank = a->T <= kRankMost;
   if (!a->accumulate) {
     if (!by_rank) {
@@ -734,9 +760,6 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
     p.fill = static_cast<uint4*>(a->grad);
     p.fill_units = rows * row / 16;
     *fill = EmbedFill{true, p.bitmap, a->n_rows, rows};
-    const int64_t blocks = (p.fill_units + 4 * kSortThreads - 1) / (4 * kSortThreads);
-    const int64_t want = (blocks + ncta - 1) / ncta, most = 136 / ncta;
-    clusters += (int)(want < most ? want : most);
   }
   if (by_rank) {
     const int blocks = (int)((a->T + 31) / 32);
@@ -760,7 +783,7 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
                                                       is_short));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * ncta), 1, 1);
+  cfg.gridDim = dim3((unsigned)ncta, 1, 1);
   cfg.blockDim = dim3(kSortThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -774,8 +797,14 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, p, status);
-  if (e == cudaSuccess) note_launch();
-  return e;
+  if (e != cudaSuccess) return e;
+  note_launch();
+  if (p.fill_units == 0) return cudaSuccess;
+  note_launch();
+  const int64_t zero = (p.fill_units + kZeroUnits - 1) / kZeroUnits;
+  return launch_maybe_pdl(true, embed_zero_kernel,
+                          dim3((unsigned)(zero < kZeroBlocks ? zero : kZeroBlocks)),
+                          dim3(kThreads), 0, st, p.fill, p.fill_units);
 }
 
 cudaError_t embed_backward(const pkm_embed_args* a, int32_t* status, cudaStream_t st) {
