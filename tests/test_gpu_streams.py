@@ -1,6 +1,7 @@
 """The operators around a memory layer called with ``stream=``: a call on a busy
 side stream must not have its workspace or outputs handed out to the current
-stream before its kernels have run."""
+stream before its kernels have run; calls on two streams at once, and longer
+batches captured and replayed, give the same bits as one after the other."""
 
 import pytest
 import torch
@@ -20,8 +21,8 @@ def _calls():
     E = (rnd(V, d) * d ** -0.5).to(BF).cuda()
     W1, W2 = (rnd(d, d) * d ** -0.5).to(BF).cuda(), (rnd(d, d) * d ** -0.5).to(BF).cuda()
     ids = torch.randint(0, V, (T,), generator=g, dtype=torch.int32).cuda()
-    many = torch.randint(0, V, (3 * T,), generator=g, dtype=torch.int32).cuda()
-    many_dy = rnd(3 * T, d).to(BF).cuda()
+    many = torch.randint(0, V, (5 * T,), generator=g, dtype=torch.int32).cuda()
+    many_dy = rnd(5 * T, d).to(BF).cuda()
     dl = torch.rand(T, generator=g).cuda()
     q, s = skv.act8_store(x)
     f = skv.add_rmsnorm_forward(x, w, r)
@@ -72,3 +73,63 @@ def test_side_stream_keeps_its_memory(name):
     del taken
     for a, b in zip(_tensors(got), want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_two_streams_at_once():
+    calls = list(_calls().items())
+    want = {n: [t.clone() for t in _tensors(f())] for n, f in calls}
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for turn in range(6):
+        for k, (n, f) in enumerate(calls):
+            for j, st in enumerate(streams):  # different operators side by side
+                m, h = calls[(k + 3 * j + turn) % len(calls)]
+                got.append((m, h(stream=st)))
+    torch.cuda.synchronize()
+    for n, r in got:
+        for a, b in zip(_tensors(r), want[n]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), n
+
+
+@pytest.mark.parametrize("T,V,d,accumulate", [
+    (5000, 40000, 520, False), (5000, 40000, 520, True), (40000, 3000, 64, False),
+    (140000, 3000, 64, False), (2048, 70000, 256, False)])
+def test_embedding_backward_captured(T, V, d, accumulate):
+    """Every way of sorting, replayed on other ids and over what earlier
+    replays left in the gradient."""
+    import sparse_key_value_b200 as skv
+    g = torch.Generator().manual_seed(T)
+    ids = torch.randint(0, V, (T,), generator=g, dtype=torch.int32).cuda()
+    dout = torch.randn(T, d, generator=g).to(BF).cuda()
+    grad = torch.full((V, d), 3.0, device="cuda")
+    skv.embedding_backward(dout, ids, V, grad=grad.clone(), accumulate=accumulate)  # warm
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        skv.embedding_backward(dout, ids, V, grad=grad, accumulate=accumulate)
+    for turn in range(3):
+        ids.copy_((torch.rand(T, generator=g) ** 3 * V).to(torch.int32))
+        base = torch.full((V, d), 3.0, device="cuda")
+        grad.copy_(base)
+        graph.replay()
+        want = skv.embedding_backward(dout, ids, V, grad=base, accumulate=accumulate)
+        assert torch.equal(grad, want), turn
+
+
+def test_long_norm_backward_captured():
+    import sparse_key_value_b200 as skv
+    g = torch.Generator().manual_seed(8)
+    T, d = 3000, 2048
+    x, dy, ds = (torch.randn(T, d, generator=g).to(BF).cuda() for _ in range(3))
+    w = torch.randn(d, generator=g).to(BF).cuda()
+    rstd = skv.add_rmsnorm_forward(x, w)["rstd"]
+    skv.add_rmsnorm_backward(dy, x, w, rstd, dsum=ds)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = skv.add_rmsnorm_backward(dy, x, w, rstd, dsum=ds)
+    for _ in range(2):
+        dy.copy_(torch.randn(T, d, generator=g).to(BF))
+        graph.replay()
+        want = skv.add_rmsnorm_backward(dy, x, w, rstd, dsum=ds)
+        assert torch.equal(kept["dx"], want["dx"])
+        assert torch.equal(kept["dweight"], want["dweight"])
