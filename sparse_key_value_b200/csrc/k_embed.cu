@@ -15,7 +15,7 @@
 //      one block sums a chunk's parts in order; the blocks after those zero the
 //      other rows that no token reads.
 //   3. embed_join_kernel: the parts of an id that covers three chunks or more,
-//      joined in chunk order.
+//      joined in chunk order (up to kJoinMost tokens by the sums' own blocks).
 // Lists of at most kRankMost tokens are sorted by counting, for each token, the
 // tokens before it in the sorted list (embed_rank_kernel): one pass without
 // barriers between blocks, and the filling blocks look into the list itself
@@ -28,7 +28,8 @@
 // 4.9 TB/s, the rest in L2); gradient of those tokens over 131072 x 1024 fp32
 // 98 us, bound by the write of its 537 MB (5.8 TB/s with reading dout, over all
 // launches: the sort's 17 us go beside the first 112 MiB of zeros); 65536 tokens
-// 172 us; 509 tokens over 32003 x 520 17 us, bound by the launches.
+// 172 us; 509 tokens over 32003 x 520 fp32 17 us and over
+// 8192 x 512 14, bound by the call's host side.
 #include "kernels.h"
 #include "q8.cuh"
 #include "tc_pair.cuh"
@@ -45,6 +46,11 @@ constexpr int kAhead = 8;    // rows of dout in flight per thread
 // and 38.6, 2048 35.0 and 38.4, 4096 48.3 and 39.9 (counting is quadratic; all of
 // these before the rows were zeroed by warps).
 constexpr int kRankMost = 2048;
+// Tokens whose long ids' parts are joined by the sums' own blocks, at most.  The
+// gradient of 100 and of 512 tokens over 8192 x 512 17.1 us with the join's
+// launch and 14.4 without, 1024 over 32768 x 1024 30.2 and 27.9; 2048 32.4 and
+// 32.9, and 17.1 and 27.5 where those are of two ids (one block joins 64 parts).
+constexpr int kJoinMost = 1024;
 constexpr int kSortThreads = 1024;
 constexpr int kSortCluster = 8;
 // Tokens per thread of the sorting cluster, at most.  The whole gradient over
@@ -142,6 +148,8 @@ struct EmbedSort {
   uint32_t* bitmap;           // rows that occur, or null
   int64_t words;
   uint32_t* n_cross;          // ids that cross chunks, counted by the sums; zeroed here
+  uint32_t* done;             // short lists: parts of such an id, counted; zeroed here
+  int n_done;
   uint4* fill;                // zeroed beside the sort, or null
   int64_t fill_units;
 };
@@ -253,6 +261,8 @@ __global__ void __launch_bounds__(32 * kRankWarps) embed_rank_kernel(const Embed
   __shared__ int count[kRankWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = (int)p.T;
   if (blockIdx.x == 0 && tid == 0) *p.n_cross = 0;
+  for (int i = blockIdx.x * 32 * kRankWarps + tid; i < p.n_done; i += blocks * 32 * kRankWarps)
+    p.done[i] = 0;
   for (int i = tid; i < kRankMost; i += 32 * kRankWarps)
     keys[i] = i < T ? embed_key(p.ids[i], p.n_rows, p.has_pad, p.pad,
                                 blockIdx.x == 0 ? status : nullptr)
@@ -425,6 +435,15 @@ __device__ __forceinline__ void write_grad(typename Elem<GT>::T* g, const float*
   store8<GT>(g, o);
 }
 
+// Eight columns of a part that another block wrote
+__device__ __forceinline__ void part_load(const float* p, float* f) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 4) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p + e));
+    f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
+  }
+}
+
 struct EmbedFill {
   bool on;
   const uint32_t* bitmap;  // rows that occur, or null: look into the sorted keys
@@ -475,13 +494,16 @@ __device__ __forceinline__ void fill_rows(const EmbedFill& f, int64_t block, int
 // The first n_sum blocks: one per chunk and slice of 8 * kSumUnits columns, a
 // thread owns 8 columns and walks the chunk's entries in order, kAhead rows in
 // flight.  The blocks after them zero the rows without tokens.
-template <pkm_dtype DT, pkm_dtype GT>
+// JOIN (short lists): the last block to finish a part of an id over three chunks
+// or more, counted in `done`, sums the parts in chunk order, instead of a launch
+// of its own.
+template <pkm_dtype DT, pkm_dtype GT, bool JOIN>
 __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
     const uint32_t* __restrict__ skey, const uint32_t* __restrict__ spos, int64_t T,
     uint32_t mark, const typename Elem<DT>::T* __restrict__ dout, int d, float scale, int add,
-    typename Elem<GT>::T* __restrict__ grad, float* __restrict__ first,
-    float* __restrict__ last, int slices, int64_t n_sum, uint32_t* __restrict__ n_cross,
-    uint4* __restrict__ cross, const EmbedFill fill) {
+    typename Elem<GT>::T* __restrict__ grad, float* __restrict__ first, float* __restrict__ last,
+    int slices, int64_t n_sum, uint32_t* __restrict__ n_cross, uint4* __restrict__ cross,
+    uint32_t* __restrict__ done, const EmbedFill fill) {
   pdl_launch_dependents();
   pdl_wait();
   if ((int64_t)blockIdx.x >= n_sum) {
@@ -519,25 +541,26 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
                          !(keys[0] == tail && keys[1] == tail);
   if (goes_over && keys[2 * kChunk + 1] != tail)
     while (e1 < 2 * kChunk && keys[e1 + 1] == tail) ++e1;
-  if (goes_over && e1 == len && threadIdx.x < 32 && blockIdx.x % slices == 0) {
-    // chunks c + 1 .. stop - 1 hold the rest: 32 chunks looked at at a time
-    int64_t stop = c + 1;
-    uint32_t m = __ballot_sync(0xffffffffu, ahead == tail);
+  const bool leads = !starts, trails = goes_over && e1 == len;  // parts for the join
+  // the end of a long id that this chunk ends with (the first warp's)
+  int64_t stop = c + 1;
+  if (threadIdx.x < 32 && (trails || (JOIN && leads && tail == keys[1]))) {
+    uint32_t m = __ballot_sync(0xffffffffu, ahead == tail);  // 32 chunks at a time
     while (m == 0xffffffffu) {
       stop += 32;
       const int64_t q = stop + threadIdx.x;
       m = __ballot_sync(0xffffffffu, q < chunks && skey[q * kChunk] == tail);
     }
     stop += __ffs(~m) - 1;
-    if (threadIdx.x == 0)  // entries stand for themselves: any order
+    if (!JOIN && threadIdx.x == 0 && blockIdx.x % slices == 0)  // any order: entries stand alone
       cross[atomicAdd(n_cross, 1u)] = make_uint4((uint32_t)c, (uint32_t)stop, tail, 0);
   }
   const int col = ((int)(blockIdx.x % slices) * kSumUnits + threadIdx.x) * kUnit;
-  if (col >= d) return;
+  if (!JOIN && col >= d) return;
   float acc[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  for (int j0 = e0; j0 < e1 && keys[j0 + 1] != mark; j0 += kAhead) {
+  for (int j0 = e0; (!JOIN || col < d) && j0 < e1 && keys[j0 + 1] != mark; j0 += kAhead) {
     Raw8<DT> raw[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
@@ -563,6 +586,56 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = 0.f;
       starts = true;
+    }
+  }
+  if constexpr (JOIN) {
+    if (leads || trails) __threadfence();  // the parts before the counts
+    __shared__ uint32_t ids[2][2];         // an id whose parts are all there: begin, end
+    const int slice = (int)(blockIdx.x % slices);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      for (int k = 0; k < 2; ++k) {
+        int64_t begin = c, end = stop;
+        if (k == 0 && leads) {
+          // back over the chunks that begin with the id, to the one it begins in
+          if (tail != keys[1]) end = c + 1;
+          for (int64_t q0 = c;; q0 -= 32) {
+            const int64_t q = q0 - threadIdx.x;
+            const uint32_t m = __ballot_sync(0xffffffffu, q >= 0 && skey[q * kChunk] == keys[1]);
+            if (m == 0xffffffffu) continue;
+            begin = q0 - (__ffs(~m) - 2);
+            break;
+          }
+          if (begin > 0 && skey[begin * kChunk - 1] == keys[1]) --begin;
+        }
+        if (threadIdx.x == 0) {
+          const bool part = k == 0 ? leads : trails;
+          const bool all = part && atomicAdd(done + begin * slices + slice, 1u) ==
+                                       (uint32_t)(end - begin - 1);
+          ids[k][0] = (uint32_t)begin;
+          ids[k][1] = all ? (uint32_t)end : 0u;
+        }
+      }
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+      const int64_t begin = ids[k][0], end = ids[k][1];
+      if (end == 0 || col >= d) continue;
+      __threadfence();
+      part_load(last + begin * d + col, acc);
+      for (int64_t q0 = begin + 1; q0 < end; q0 += kAhead) {
+        float f[kAhead][8];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (q0 + u < end) part_load(first + (q0 + u) * d + col, f[u]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (q0 + u < end) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += f[u][e];
+          }
+      }
+      write_grad<GT>(grad + (int64_t)skey[(begin + 1) * kChunk] * d + col, acc, scale, add);
     }
   }
 }
@@ -646,7 +719,7 @@ int sum_slices(int d) { return (d / kUnit + kSumUnits - 1) / kSumUnits; }
 int64_t sum_blocks(int64_t T, int d) { return (T + kChunk - 1) / kChunk * sum_slices(d); }
 
 struct EmbedLayout {
-  size_t keys, pos, skey, spos, radix, bitmap, cross, first, last, total;
+  size_t keys, pos, skey, spos, radix, bitmap, cross, done, first, last, total;
   bool cluster;  // the list fits the one-cluster sort
 };
 
@@ -668,6 +741,7 @@ EmbedLayout embed_layout(const pkm_embed_args* a) {
   L.radix = L.cluster ? 0 : take(radix_sort_workspace(a->T));
   L.bitmap = L.cluster && a->T > kRankMost && !a->accumulate ? take((size_t)(a->n_rows + 31) / 32 * 4) : 0;
   L.cross = take((chunks + 1) * 16);  // count, then ids over three chunks or more
+  L.done = a->T <= kJoinMost ? take(chunks * (size_t)sum_slices(a->d) * 4) : 0;
   L.first = take(chunks * d * 4);
   L.last = take(chunks * d * 4);
   L.total = off;
@@ -715,13 +789,16 @@ cudaError_t embed_sums(const pkm_embed_args* a, const EmbedLayout& L, char* ws,
   const int64_t n_fill = fill.on ? (fill.n_rows - fill.first + 31) / 32 : 0;
   uint32_t* n_cross = reinterpret_cast<uint32_t*>(ws + L.cross);
   uint4* cross = reinterpret_cast<uint4*>(ws + L.cross) + 1;
+  uint32_t* done = reinterpret_cast<uint32_t*>(ws + L.done);
+  const bool joins = a->T <= kJoinMost;
   note_launch();
   const cudaError_t e = launch_maybe_pdl(
-      true, embed_sum_kernel<DT, GT>, dim3((unsigned)(n_sum + n_fill)), dim3(kSumUnits), 0, st,
-      skey, spos, a->T, (uint32_t)a->n_rows, static_cast<const typename Elem<DT>::T*>(a->dout),
-      a->d, a->scale, a->accumulate, grad, first, last, slices, n_sum, n_cross, cross, fill);
+      true, joins ? embed_sum_kernel<DT, GT, true> : embed_sum_kernel<DT, GT, false>,
+      dim3((unsigned)(n_sum + n_fill)), dim3(kSumUnits), 0, st, skey, spos, a->T,
+      (uint32_t)a->n_rows, static_cast<const typename Elem<DT>::T*>(a->dout), a->d, a->scale,
+      a->accumulate, grad, first, last, slices, n_sum, n_cross, cross, done, fill);
   // an id that the join sums covers three chunks
-  if (e != cudaSuccess || chunks < 3) return e;
+  if (e != cudaSuccess || joins || chunks < 3) return e;
   const unsigned blocks = (unsigned)(chunks - 2 < kJoinBlocks ? chunks - 2 : kJoinBlocks);
   note_launch();
   return launch_maybe_pdl(true, embed_join_kernel<GT>, dim3(blocks, (units + 31) / 32),
@@ -748,6 +825,8 @@ cudaError_t launch_embed_sort(const pkm_embed_args* a, const EmbedLayout& L, cha
   p.key[1] = reinterpret_cast<uint32_t*>(ws + L.keys);
   p.pos[1] = reinterpret_cast<uint32_t*>(ws + L.pos);
   p.n_cross = reinterpret_cast<uint32_t*>(ws + L.cross);
+  p.done = reinterpret_cast<uint32_t*>(ws + L.done);
+  p.n_done = a->T <= kJoinMost ? (int)((a->T + kChunk - 1) / kChunk) * sum_slices(a->d) : 0;
   const bool by_rank = a->T <= kRankMost;
   if (!a->accumulate) {
     if (!by_rank) {

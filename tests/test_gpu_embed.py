@@ -88,12 +88,14 @@ def test_backward_many_tokens(T, V, kind):
     assert (a.cpu()[n[:, 0] == 0] == 0).all()
 
 
-@pytest.mark.parametrize("T", [2047, 2048, 2049])
+@pytest.mark.parametrize("T,d", [(2047, 72), (2048, 72), (2049, 72), (1023, 2056), (1024, 72),
+                                 (1025, 2056), (49, 1032), (64, 8)])
 @pytest.mark.parametrize("kind", ["zipf", "same", "uniform"])
 @pytest.mark.parametrize("accumulate", [False, True])
-def test_backward_at_the_end_of_counting(T, kind, accumulate):
-    """Both sides of the longest list that is sorted by counting."""
-    V, d = 5000, 72
+def test_backward_at_the_end_of_counting(T, d, kind, accumulate):
+    """Both sides of the longest list that is sorted by counting and of the
+    longest whose long ids are joined by the sums; several column slices."""
+    V = 5000 if T > 1000 else 40
     g = torch.Generator().manual_seed(T)
     ids, dout = _ids(g, T, V, kind), torch.randn(T, d, generator=g).to(BF)
     base = torch.randn(V, d, generator=g) if accumulate else torch.zeros(V, d)
