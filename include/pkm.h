@@ -630,8 +630,8 @@ PKM_API pkm_status pkm_linear_xent_backward(const pkm_xent_args *args, pkm_strea
  * da and y ⊙ g are rounded to bf16 once as the operands of the products that
  * give dx, dW1 and dW2.  Every sum runs in a fixed order.
  * Limits: d_model, d_v multiples of 8 and <= 65536, T <= 2^28 and
- * T * ceil(d_model / PKM_Q8_GROUP) < 2^34 (PKM_ERR_UNSUPPORTED above).  T = 0 is a valid empty call (dW1 and dW2 are
- * zeroed).
+ * T * ceil(d_model / PKM_Q8_GROUP) < 2^34 (PKM_ERR_UNSUPPORTED above).  T = 0
+ * is a valid empty call (dW1 and dW2 are zeroed).
  */
 typedef struct {
     int64_t T;

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(block_threads(WPR), bwd_per_sm(WPR))
   }
 }
 
-// The backward of long batches of 16- or 32-bit h: a row's tensors come by bulk
+// The backward of long batches: a row's tensors come by bulk
 // copies into a ring of shared memory, so that up to 200 KB per SM are on their
 // way while rows are summed and written; registers hold a row only while it is
 // worked on.  One block per SM, kRingWarps / WPR teams of a row each, a ring of
@@ -281,13 +281,15 @@ __global__ void __launch_bounds__(block_threads(WPR), bwd_per_sm(WPR))
 // row's sum, whose barrier follows the team's last read of it.
 // Against the rows straight into registers (bf16, second gradient, us): 8191 x
 // 2048 27.1 and 30.7, 4096 x 4096 27.2 and 34.8, 2048 x 8192 27.6 and 38.4, 30000
-// x 512 26.6 and 29.9; 40000 x 256 20.6 and 21.1, 100000 x 64 39.1 and 38.9.  20
-// warps took 28.9 at the first, 12 with a deeper ring 27.1 but 38.4 at the third.
+// x 512 26.6 and 29.9; 40000 x 256 20.6 and 21.1, 100000 x 64 39.1 and 38.9;
+// int8 h: 8191 x 2048 27.0 and 30.8, 4096 x 4096 27.0 and 34.7.  20 warps took
+// 28.9 at the first (12 rounds of rows for 11.1), 12 with a deeper ring 27.1 but
+// 38.4 at the third.
 constexpr int kRingWarps = 16, kRingStages = 4;
 constexpr int kRingBytes = 200 * 1024;
 constexpr int ring_teams(int wpr) { return kRingWarps / wpr; }
 
-template <pkm_dtype DT, pkm_dtype DY, int NU, int WPR>
+template <pkm_dtype DT, pkm_dtype DY, int NU, int WPR, bool Q8>
 __global__ void __launch_bounds__(32 * WPR * ring_teams(WPR), 1)
     norm_bwd_ring_kernel(const NormBwd p, int stages, int32_t* status) {
   using E = typename Elem<DT>::T;
@@ -302,8 +304,9 @@ __global__ void __launch_bounds__(32 * WPR * ring_teams(WPR), 1)
   const int col0 = ((warp % WPR) * 32 + lane) * kUnit;
   const bool leads = threadIdx.x == team * WPR * 32;
   const int d = p.d;
-  const uint32_t ny = (uint32_t)d * sizeof(Ey), nh = (uint32_t)d * sizeof(E);
-  const uint32_t row_bytes = ny + nh + (p.dsum ? nh : 0);
+  const uint32_t ny = (uint32_t)d * sizeof(Ey), ns = p.dsum ? (uint32_t)d * sizeof(E) : 0;
+  const uint32_t nh = Q8 ? (uint32_t)d : (uint32_t)d * sizeof(E);
+  const uint32_t row_bytes = ny + nh + ns;
   unsigned char* ring = ring_raw + (size_t)team * stages * row_bytes;
   if (threadIdx.x == 0) {
     for (int t = 0; t < kTeams; ++t)
@@ -321,8 +324,8 @@ __global__ void __launch_bounds__(32 * WPR * ring_teams(WPR), 1)
     uint64_t* bar = &full[team][place];
     mbar_arrive_expect_tx(bar, row_bytes);
     bulk_load(to, static_cast<const Ey*>(p.dy) + row * d, ny, bar);
-    bulk_load(to + ny, static_cast<const E*>(p.h) + row * d, nh, bar);
-    if (p.dsum) bulk_load(to + ny + nh, static_cast<const E*>(p.dsum) + row * d, nh, bar);
+    bulk_load(to + ny, static_cast<const uint8_t*>(p.h) + row * nh, nh, bar);
+    if (ns) bulk_load(to + ny + nh, static_cast<const E*>(p.dsum) + row * d, ns, bar);
   };
   if (leads)
     for (int i = 0; i < stages && row0 + i * step < p.T; ++i) copy(row0 + i * step, i);
@@ -337,13 +340,28 @@ __global__ void __launch_bounds__(32 * WPR * ring_teams(WPR), 1)
   for (int c = 0; c < NU; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[c][e] = 0.f;
+  // a row's rstd, with 8-bit h its scales too, are read a turn ahead
   float rstd = row0 < p.T ? p.rstd[row0] : 0.f;
+  const int groups = q8_groups(d);
+  auto scale_of = [&](int64_t row, int c) {
+    const int col = col0 + c * (WPR * 32 * kUnit);
+    return Q8 && row < p.T && col < d ? p.scales[row * groups + col / kQ8Group] : 0.f;
+  };
+  float next[NU];
+#pragma unroll
+  for (int c = 0; c < NU; ++c) next[c] = scale_of(row0, c);
   int place = 0, turn = 0;
   uint32_t parity = 0;
   bool ok = true;
   for (int64_t row = row0; row < p.T; row += step) {
     const float rs = rstd;
     if (row + step < p.T) rstd = p.rstd[row + step];
+    float hs[NU];
+#pragma unroll
+    for (int c = 0; c < NU; ++c) {
+      hs[c] = next[c];
+      next[c] = scale_of(row + step, c);
+    }
     ok = ok && mbar_wait_or_abort(&full[team][place], parity, &abort, status);
     const unsigned char* at = ring + (size_t)place * row_bytes;
     Raw8<DY> dy[NU];
@@ -356,10 +374,30 @@ __global__ void __launch_bounds__(32 * WPR * ring_teams(WPR), 1)
       ds[c].zero();
       if (col < d) {
         dy[c].load(reinterpret_cast<const Ey*>(at) + col);
-        h[c].load(reinterpret_cast<const E*>(at + ny) + col);
-        if (p.dsum) ds[c].load(reinterpret_cast<const E*>(at + ny + nh) + col);
+        if constexpr (Q8) {
+          const uint2 q = *reinterpret_cast<const uint2*>(at + ny + col);
+          h[c].v[0].x = q.x;
+          h[c].v[0].y = q.y;
+        } else {
+          h[c].load(reinterpret_cast<const E*>(at + ny) + col);
+        }
+        if (ns) ds[c].load(reinterpret_cast<const E*>(at + ny + nh) + col);
       }
     }
+    float hv[Q8 ? NU : 1][8];  // 8-bit h as numbers: decoded once, used twice
+    if constexpr (Q8) {
+#pragma unroll
+      for (int c = 0; c < NU; ++c)
+        q8_decode(make_uint2(h[c].v[0].x, h[c].v[0].y), hs[c], p.fmt, hv[c]);
+    }
+    auto value = [&](int c, float* n) {
+      if constexpr (Q8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) n[e] = hv[c][e];
+      } else {
+        h[c].unpack(n);
+      }
+    };
     auto weigh = [&](int c, float* g) {
       if (p.w && col0 + c * (WPR * 32 * kUnit) < d) {
         float f[8];
@@ -372,7 +410,7 @@ __global__ void __launch_bounds__(32 * WPR * ring_teams(WPR), 1)
 #pragma unroll
     for (int c = 0; c < NU; ++c) {
       float g[8], n[8];
-      h[c].unpack(n);
+      value(c, n);
       dy[c].unpack(g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -390,7 +428,7 @@ __global__ void __launch_bounds__(32 * WPR * ring_teams(WPR), 1)
     for (int c = 0; c < NU; ++c) {
       const int col = col0 + c * (WPR * 32 * kUnit);
       float g[8], n[8], o[8];
-      h[c].unpack(n);
+      value(c, n);
       dy[c].unpack(g);
       weigh(c, g);
       ds[c].unpack(o);
@@ -498,7 +536,7 @@ cudaError_t norm_shape(int d, F&& f) {
 }
 
 // The rows that a team's ring holds, or 0 where the backward takes its rows
-// straight into registers: 8-bit h (rows of odd multiples of 8 bytes), short rows
+// straight into registers: 8-bit h in rows of odd multiples of 8 bytes, short rows
 // and those of more warps than the ring's block has, batches of fewer than kRingRows rows
 // per team (the other path spreads those over more blocks; at 1500 and 740 x 2048
 // both end before the call's host side does).
@@ -514,7 +552,7 @@ NormPlan bwd_plan(int64_t T, int d, bool f32, pkm_q8 fmt, int row_bytes) {
       constexpr int kTeams = ring_teams(WPR);
       int stages = kRingBytes / (kTeams * row_bytes);
       if (stages > kRingStages) stages = kRingStages;
-      if (fmt == PKM_Q8_NONE && d > 256 && stages >= 2 && T >= (int64_t)kSMs * kTeams * kRingRows) {
+      if ((fmt == PKM_Q8_NONE || d % 16 == 0) && d > 256 && stages >= 2 && T >= (int64_t)kSMs * kTeams * kRingRows) {
         plan = NormPlan{stages, kSMs};
         return cudaSuccess;
       }
@@ -543,15 +581,15 @@ cudaError_t fwd_launch(const NormFwd& p, cudaStream_t st) {
   });
 }
 
-int row_bytes(int d, pkm_dtype dt, pkm_dtype dy, bool dsum) {
+int row_bytes(int d, pkm_dtype dt, pkm_dtype dy, pkm_q8 fmt, bool dsum) {
   const int b = dt == PKM_F32 ? 4 : 2, y = dy == PKM_F32 ? 4 : 2;
-  return d * (y + b + (dsum ? b : 0));
+  return d * (y + (fmt == PKM_Q8_NONE ? b : 1) + (dsum ? b : 0));
 }
 
 template <pkm_dtype DT, pkm_dtype DY>
 cudaError_t bwd_launch(const NormBwd& p, float* dweight, int32_t* status, cudaStream_t st) {
   constexpr bool f32 = DT == PKM_F32 || DY == PKM_F32;
-  const int bytes = row_bytes(p.d, DT, DY, p.dsum != nullptr);
+  const int bytes = row_bytes(p.d, DT, DY, p.fmt, p.dsum != nullptr);
   const NormPlan plan = bwd_plan(p.T, p.d, f32, p.fmt, bytes);
   const int blocks = plan.blocks;
   const cudaError_t e = norm_shape<f32 ? 1 : 2>(p.d, [&](auto nu, auto wpr) {
@@ -563,12 +601,13 @@ cudaError_t bwd_launch(const NormBwd& p, float* dweight, int32_t* status, cudaSt
         const size_t ring = (size_t)kTeams * plan.stages * bytes;
         const size_t sums = (size_t)(kTeams - 1) * NU * WPR * 32 * kUnit * 4;
         const size_t smem = ring > sums ? ring : sums;
-        const cudaError_t set =
-            cudaFuncSetAttribute(norm_bwd_ring_kernel<DT, DY, NU, WPR>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        auto kern = p.fmt == PKM_Q8_NONE ? norm_bwd_ring_kernel<DT, DY, NU, WPR, false>
+                                         : norm_bwd_ring_kernel<DT, DY, NU, WPR, true>;
+        const cudaError_t set = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
         if (set != cudaSuccess) return set;
-        return launch_maybe_pdl(true, norm_bwd_ring_kernel<DT, DY, NU, WPR>, dim3(blocks),
-                                dim3(32 * WPR * kTeams), smem, st, p, plan.stages, status);
+        return launch_maybe_pdl(true, kern, dim3(blocks), dim3(32 * WPR * kTeams), smem, st, p,
+                                plan.stages, status);
       }
     }
     return launch_maybe_pdl(true, norm_bwd_kernel<DT, DY, NU, WPR>, dim3(blocks),
@@ -600,7 +639,7 @@ size_t bwd_bytes(const pkm_norm_bwd_args* a) {
   if (a->T <= 0 || a->d < 8 || a->d > kMaxD) return 0;
   const bool f32 = a->dtype == PKM_F32 || a->dy_dtype == PKM_F32;
   // of the register path, whose blocks are the more: the same for every fmt and dsum
-  return (size_t)bwd_plan(a->T, a->d, f32, PKM_Q8_E4M3, 1).blocks * (size_t)a->d * 4;
+  return (size_t)bwd_plan(a->T, a->d, f32, PKM_Q8_NONE, kRingBytes).blocks * (size_t)a->d * 4;
 }
 
 pkm_status bwd_validate(const pkm_norm_bwd_args* a) {

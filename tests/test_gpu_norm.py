@@ -189,6 +189,17 @@ def test_backward_of_long_batches(T, d, dtype, dy_dtype, res, weight):
     assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dweight"], b["dweight"])
 
 
+@pytest.mark.parametrize("T,d,dtype,dy_dtype,fmt", [
+    (9500, 272, BF, BF, "int8"), (9475, 512, BF, F32, "e4m3"), (4750, 1000, BF, BF, "int8"),
+    (4740, 1008, F32, F32, "e4m3"), (2371, 2048, BF, BF, "int8"), (2371, 2040, BF, BF, "e4m3"),
+    (1190, 4096, F32, BF, "int8"), (595, 8192, BF, BF, "e4m3")])
+def test_backward_of_long_batches_from_8_bits(T, d, dtype, dy_dtype, fmt):
+    """8-bit rows through shared memory where they are multiples of 16 bytes."""
+    a = _check_bwd(T, d, dtype, dy_dtype, d % 512 == 0, True, fmt, T + d)
+    b = _check_bwd(T, d, dtype, dy_dtype, d % 512 == 0, True, fmt, T + d)
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dweight"], b["dweight"])
+
+
 @pytest.mark.parametrize("T,d,dtype", [(2367, 2048, BF), (2368, 2048, BF), (9471, 64, BF),
                                        (9472, 64, BF), (9473, 8, F32), (592, 4096, F32),
                                        (593, 16384, BF)])
