@@ -389,10 +389,34 @@ def check_wait_timeout(polls: int = 4096, device=None, stream=None) -> int:
     return code
 
 
-def _same_device(dev: torch.device, *ts):
+def _operands(dev: torch.device, *ts):
+    """Contiguous tensors of one GPU (or None)."""
+    index = dev.index
     for t in ts:
-        if t is not None and t.device != dev:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            _need_cuda(t)
             raise ValueError(f"tensors on different devices: {t.device} and {dev}")
+
+
+# Small calls take as long as their host side, a third of which is torch.empty
+# reading its arguments (1.6 us); the entry that generated code uses takes half.
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    _empty_strided_cuda = None
+
+
+def _new_here(dtype, n, d=None):
+    if d is None:
+        return _empty_strided_cuda((n,), (1,), dtype)
+    return _empty_strided_cuda((n, d), (d, 1), dtype)
+
+
+def _new(dev: torch.device):
+    """new(dtype, n[, d]): an uninitialised tensor on ``dev``."""
+    if _empty_strided_cuda is not None and torch.cuda.current_device() == dev.index:
+        return _new_here
+    return lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _shape(name: str, t: Optional[torch.Tensor], shape, dtype=None):
@@ -423,9 +447,8 @@ def _on_stream(f):
     def call(*args, stream: Optional[torch.cuda.Stream] = None, **kw):
         if stream is None:
             return f(*args, **kw)
-        tensors = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)]
-        _need_cuda(*tensors)
-        _same_device(stream.device, *tensors)
+        _operands(stream.device,
+                  *(t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)))
         with torch.cuda.stream(stream):
             return f(*args, **kw)
 
@@ -439,27 +462,30 @@ def _enqueue(fn: str, args, dev: torch.device):
     """Call the entry point with ``args`` on the tensors' device and its
     current stream."""
     f = getattr(load(), fn)
-    if _raw_stream is not None:
-        s = _raw_stream(dev.index)
-    else:
-        s = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        check(f(*args, s), fn)
+    index = dev.index
+    s = torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None else _raw_stream(index)
+    if torch.cuda.current_device() == index:
+        code = f(*args, s)
     else:
         with torch.cuda.device(dev):
-            check(f(*args, s), fn)
+            code = f(*args, s)
+    if code:
+        check(code, fn)
 
 
-def _workspace(workspace, need: int, dev: torch.device):
+def _workspace(a, workspace, need: int, dev: torch.device):
+    """Puts the workspace into ``a``; returns its tensor, to be kept until the call."""
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    _need_cuda(workspace)
-    _same_device(dev, workspace)
+        a.workspace_bytes = need = max(need, 16)
+        workspace = _new(dev)(torch.uint8, need)
+    else:
+        _operands(dev, workspace)
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+    a.workspace = workspace.data_ptr()
     return workspace
 
 
 def _embed_args(ids, n_rows, d, dtype, scale, pad_id) -> "_lib.EmbedArgs":
-    _need_cuda(ids)
     if ids.dtype != torch.int32:
         raise TypeError("ids must be int32")
     if pad_id is not None and not -2 ** 31 <= pad_id < 2 ** 31:  # ctypes would cut it silently
@@ -474,15 +500,17 @@ def embedding_forward(table, ids, scale: float = 1.0, pad_id: Optional[int] = No
 
     table [n_rows, d], ids int32 of any shape; out [*ids.shape, d].
     Positions holding ``pad_id`` give a zero row."""
-    _need_cuda(table, out)
-    n_rows, d = table.shape
     dev = table.device
+    _operands(dev, table, ids, out)
+    n_rows, d = table.shape
     a = _embed_args(ids, n_rows, d, _dt(table), scale, pad_id)
-    if out is None:
+    if out is not None:
+        _shape("out", out, (*ids.shape, d), table.dtype)
+    elif ids.ndim == 1:
+        out = _new(dev)(table.dtype, ids.shape[0], d)
+    else:
         out = torch.empty(*ids.shape, d, dtype=table.dtype, device=dev)
-    _shape("out", out, (*ids.shape, d), table.dtype)
-    _same_device(dev, ids, out)
-    a.table, a.out = _ptr(table), _ptr(out)
+    a.table, a.out = table.data_ptr(), out.data_ptr()
     _enqueue("pkm_embed_forward", (ctypes.byref(a),), dev)
     return out
 
@@ -496,22 +524,20 @@ def embedding_backward(dout, ids, n_rows: int, scale: float = 1.0, pad_id: Optio
 
     dout [*ids.shape, d]; returns grad [n_rows, d] (``grad_dtype``, or the
     given tensor), every row written, or added to with ``accumulate``."""
-    _need_cuda(dout, grad)
-    d = dout.shape[-1]
     dev = dout.device
+    _operands(dev, dout, ids, grad)
+    d = dout.shape[-1]
     _shape("dout", dout, (*ids.shape, d))
     if accumulate and grad is None:
         raise ValueError("accumulate needs grad")
     a = _embed_args(ids, n_rows, d, _dt(dout), scale, pad_id)
     if grad is None:
-        grad = torch.empty(n_rows, d, dtype=grad_dtype, device=dev)
-    _shape("grad", grad, (n_rows, d))
+        grad = _new(dev)(grad_dtype, n_rows, d)
+    else:
+        _shape("grad", grad, (n_rows, d))
     a.grad_dtype, a.accumulate = _dt(grad), 1 if accumulate else 0
-    need = int(load().pkm_embed_workspace_size(ctypes.byref(a)))
-    workspace = _workspace(workspace, need, dev)
-    _same_device(dev, ids, grad)
-    a.dout, a.grad, a.workspace, a.workspace_bytes = _ptr(dout), _ptr(grad), _ptr(workspace), \
-        workspace.numel() * workspace.element_size()
+    workspace = _workspace(a, workspace, load().pkm_embed_workspace_size(ctypes.byref(a)), dev)
+    a.dout, a.grad = dout.data_ptr(), grad.data_ptr()
     _enqueue("pkm_embed_backward", (ctypes.byref(a),), dev)
     return grad
 
@@ -532,18 +558,16 @@ def _q8_name(fmt: str):
     return _Q8[fmt]
 
 
-def _q8_empty(T: int, d: int, dtype, dev):
-    return (torch.empty(T, d, dtype=dtype, device=dev),
-            torch.empty(T, (d + Q8_GROUP - 1) // Q8_GROUP, dtype=torch.float32, device=dev))
+def _q8_empty(T: int, d: int, dtype, new):
+    return new(dtype, T, d), new(torch.float32, T, (d + Q8_GROUP - 1) // Q8_GROUP)
 
 
 def _q8_check(name: str, q, scales):
-    """Checks an 8-bit activation and its scales; returns (T, d, fmt)."""
-    _need_cuda(q, scales)
+    """Checks an 8-bit activation and its scales, called ``name``; returns (T, d, fmt)."""
+    _operands(q.device, q, scales)
     fmt = _q8_fmt(q)
     T, d = q.shape
-    _shape(f"{name} scales", scales, (T, (d + Q8_GROUP - 1) // Q8_GROUP), torch.float32)
-    _same_device(q.device, scales)
+    _shape(name, scales, (T, (d + Q8_GROUP - 1) // Q8_GROUP), torch.float32)
     return T, d, fmt
 
 
@@ -551,11 +575,13 @@ def _q8_check(name: str, q, scales):
 def act8_store(x, fmt: str = "int8"):
     """x [T, d] in 8 bits (see pkm_act8_store in include/pkm.h): returns
     (q [T, d] float8_e4m3fn or int8, scales fp32 [T, ceil(d / 128)])."""
-    _need_cuda(x)
+    dev = x.device
+    _operands(dev, x)
     code, dtype = _q8_name(fmt)
     T, d = x.shape
-    q, scales = _q8_empty(T, d, dtype, x.device)
-    _enqueue("pkm_act8_store", (_ptr(x), T, d, _dt(x), code, _ptr(q), _ptr(scales)), x.device)
+    q, scales = _q8_empty(T, d, dtype, _new(dev))
+    _enqueue("pkm_act8_store", (x.data_ptr(), T, d, _dt(x), code, q.data_ptr(),
+                                scales.data_ptr()), dev)
     return q, scales
 
 
@@ -563,13 +589,15 @@ def act8_store(x, fmt: str = "int8"):
 def act8_load(q, scales, dtype=torch.bfloat16, out=None):
     """The values act8_store's (or add_rmsnorm_forward's) 8 bits stand for,
     exact in bf16."""
-    T, d, fmt = _q8_check("act8", q, scales)
-    _need_cuda(out)
+    T, d, fmt = _q8_check("scales", q, scales)
+    dev = q.device
     if out is None:
-        out = torch.empty(T, d, dtype=dtype, device=q.device)
-    _shape("out", out, (T, d))
-    _same_device(q.device, out)
-    _enqueue("pkm_act8_load", (_ptr(q), _ptr(scales), T, d, fmt, _ptr(out), _dt(out)), q.device)
+        out = _new(dev)(dtype, T, d)
+    else:
+        _operands(dev, out)
+        _shape("out", out, (T, d))
+    _enqueue("pkm_act8_load", (q.data_ptr(), scales.data_ptr(), T, d, fmt, out.data_ptr(),
+                               _dt(out)), dev)
     return out
 
 
@@ -583,23 +611,23 @@ def add_rmsnorm_forward(x, weight=None, residual=None, eps: float = 1e-6,
     residual), y (None unless ``want_y``), rstd fp32 [T], and with ``fmt``
     ('e4m3' or 'int8') q8, scales: y in 8 bits).  ``sum_out`` may be x or
     residual, to add in place."""
-    _need_cuda(x, weight, residual, sum_out)
-    T, d = x.shape
     dev, dt = x.device, x.dtype
-    _shape("residual", residual, (T, d), dt)
+    _operands(dev, x, weight, residual, sum_out)
+    T, d = shape = x.shape
+    _shape("residual", residual, shape, dt)
     _shape("weight", weight, (d,), dt)
-    _shape("sum_out", sum_out, (T, d), dt)
-    _same_device(dev, weight, residual, sum_out)
+    _shape("sum_out", sum_out, shape, dt)
+    new = _new(dev)
     h = sum_out
     if h is None and residual is not None:
-        h = torch.empty_like(x)
-    y = torch.empty_like(x) if want_y else None
-    rstd = torch.empty(T, dtype=torch.float32, device=dev)
+        h = new(dt, T, d)
+    y = new(dt, T, d) if want_y else None
+    rstd = new(torch.float32, T)
     q = scales = None
     code = PKM_Q8_NONE
     if fmt is not None:
         code, qdt = _q8_name(fmt)
-        q, scales = _q8_empty(T, d, qdt, dev)
+        q, scales = _q8_empty(T, d, qdt, new)
     a = _lib.NormArgs(T, d, _dt(x), eps, code, _ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y),
                       _ptr(q), _ptr(scales), _ptr(rstd))
     _enqueue("pkm_add_rmsnorm_forward", (ctypes.byref(a),), dev)
@@ -616,46 +644,41 @@ def add_rmsnorm_backward(dy, sum, weight, rstd, dsum=None, scales=None, want_dwe
     copy together with ``scales`` (act8_store); dsum the gradient that
     reaches the stored sum from elsewhere.  Returns dict(dx: the gradient of
     x and of the residual, in the type of dsum, weight or dy; dweight fp32 [d])."""
-    _need_cuda(dy, sum, weight, rstd, dsum)
-    T, d = dy.shape
     dev = dy.device
+    _operands(dev, dy, sum, weight, rstd, dsum)
+    T, d = shape = dy.shape
     fmt = PKM_Q8_NONE
     if scales is not None:
-        _, _, fmt = _q8_check("sum", sum, scales)
+        _, _, fmt = _q8_check("scales", sum, scales)
         like = dsum if dsum is not None else weight if weight is not None else dy
         dt = like.dtype
     else:
         dt = sum.dtype
-    _shape("sum", sum, (T, d))
+    _shape("sum", sum, shape)
     _shape("weight", weight, (d,), dt)
     _shape("rstd", rstd, (T,), torch.float32)
-    _shape("dsum", dsum, (T, d), dt)
-    _same_device(dev, sum, scales, weight, rstd, dsum)
-    dx = torch.empty(T, d, dtype=dt, device=dev)
-    dweight = torch.empty(d, dtype=torch.float32, device=dev) if want_dweight else None
+    _shape("dsum", dsum, shape, dt)
+    new = _new(dev)
+    dx = new(dt, T, d)
+    dweight = new(torch.float32, d) if want_dweight else None
     a = _lib.NormBwdArgs(T, d, _dt(dx), _dt(dy), fmt, _ptr(dy), _ptr(sum), _ptr(scales), _ptr(weight),
                          _ptr(rstd), _ptr(dsum), _ptr(dx), _ptr(dweight), None, 0)
     if want_dweight:
-        need = int(load().pkm_add_rmsnorm_backward_workspace_size(ctypes.byref(a)))
-        workspace = _workspace(workspace, need, dev)
-        a.workspace, a.workspace_bytes = _ptr(workspace), \
-            workspace.numel() * workspace.element_size()
+        need = load().pkm_add_rmsnorm_backward_workspace_size(ctypes.byref(a))
+        workspace = _workspace(a, workspace, need, dev)
     _enqueue("pkm_add_rmsnorm_backward", (ctypes.byref(a),), dev)
     return dict(dx=dx, dweight=dweight)
 
 
 def _xent_args(x, W, targets, ignore_index: int) -> "_lib.XentArgs":
-    _need_cuda(x, W, targets)
+    _operands(x.device, x, W, targets)
     T, d = x.shape
     _shape("W", W, (W.shape[0], d), x.dtype)
     _shape("targets", targets, (T,), torch.int32)
-    _same_device(x.device, W, targets)
     if not -2 ** 31 <= ignore_index < 2 ** 31:
         raise ValueError(f"ignore_index {ignore_index} is not an int32")
-    a = _lib.XentArgs()
-    a.T, a.V, a.d, a.dtype, a.ignore_index = T, W.shape[0], d, _dt(x), ignore_index
-    a.x, a.W, a.targets = _ptr(x), _ptr(W), _ptr(targets)
-    return a
+    return _lib.XentArgs(T, W.shape[0], d, _dt(x), PKM_F32, ignore_index, x.data_ptr(),
+                         W.data_ptr(), targets.data_ptr())
 
 
 @_on_stream
@@ -667,12 +690,11 @@ def linear_xent_forward(x, W, targets, ignore_index: int = -100, workspace=None)
     [T]; positions whose target is ``ignore_index`` have loss 0."""
     a = _xent_args(x, W, targets, ignore_index)
     dev = x.device
-    loss = torch.empty(a.T, dtype=torch.float32, device=dev)
-    lse = torch.empty(a.T, dtype=torch.float32, device=dev)
-    a.loss, a.lse = _ptr(loss), _ptr(lse)
-    need = int(load().pkm_linear_xent_forward_workspace_size(ctypes.byref(a)))
-    workspace = _workspace(workspace, need, dev)
-    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    new = _new(dev)
+    loss, lse = new(torch.float32, a.T), new(torch.float32, a.T)
+    a.loss, a.lse = loss.data_ptr(), lse.data_ptr()
+    need = load().pkm_linear_xent_forward_workspace_size(ctypes.byref(a))
+    workspace = _workspace(a, workspace, need, dev)
     _enqueue("pkm_linear_xent_forward", (ctypes.byref(a),), dev)
     return loss, lse
 
@@ -686,7 +708,7 @@ def linear_xent_backward(x, W, targets, lse, dloss, ignore_index: int = -100,
     ``grad_dtype`` (or the given tensors, overwritten)."""
     a = _xent_args(x, W, targets, ignore_index)
     dev = x.device
-    _need_cuda(lse, dloss, dx, dW)
+    _operands(dev, lse, dloss, dx, dW)
     _shape("lse", lse, (a.T,), torch.float32)
     _shape("dloss", dloss, (a.T,), torch.float32)
     if dx is None:
@@ -695,12 +717,10 @@ def linear_xent_backward(x, W, targets, lse, dloss, ignore_index: int = -100,
         dW = torch.empty(W.shape, dtype=dx.dtype, device=dev)
     _shape("dx", dx, x.shape)
     _shape("dW", dW, W.shape, dx.dtype)
-    _same_device(dev, lse, dloss, dx, dW)
     a.grad_dtype = _dt(dx)
     a.lse, a.dloss, a.dx, a.dW = _ptr(lse), _ptr(dloss), _ptr(dx), _ptr(dW)
-    need = int(load().pkm_linear_xent_backward_workspace_size(ctypes.byref(a)))
-    workspace = _workspace(workspace, need, dev)
-    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    need = load().pkm_linear_xent_backward_workspace_size(ctypes.byref(a))
+    workspace = _workspace(a, workspace, need, dev)
     _enqueue("pkm_linear_xent_backward", (ctypes.byref(a),), dev)
     return dx, dW
 
@@ -715,26 +735,23 @@ def memplus_backward_act8(x8, x_scales, W1, W2, y8, y_scales, dout, grad_dtype=t
     output [T, d_v] as act8_store (or add_rmsnorm_forward) wrote them, in one
     format; W1 [d_model, d_v], W2 [d_v, d_model], dout [T, d_model] bf16.
     Returns dict(dy (bf16), dx, dW1, dW2 (``grad_dtype``))."""
-    T, dm, fmt = _q8_check("x8", x8, x_scales)
-    T2, dv, fmt2 = _q8_check("y8", y8, y_scales)
+    T, dm, fmt = _q8_check("x_scales", x8, x_scales)
+    T2, dv, fmt2 = _q8_check("y_scales", y8, y_scales)
     if T2 != T or fmt2 != fmt:
         raise ValueError("x8 and y8: one number of rows and one format")
-    _need_cuda(W1, W2, dout)
+    dev = x8.device
+    _operands(dev, y8, W1, W2, dout)
     bf = torch.bfloat16
     _shape("W1", W1, (dm, dv), bf)
     _shape("W2", W2, (dv, dm), bf)
     _shape("dout", dout, (T, dm), bf)
-    dev = x8.device
-    _same_device(dev, y8, W1, W2, dout)
-    dy = torch.empty(T, dv, dtype=bf, device=dev)
-    dx = torch.empty(T, dm, dtype=grad_dtype, device=dev)
-    dW1 = torch.empty(dm, dv, dtype=grad_dtype, device=dev)
-    dW2 = torch.empty(dv, dm, dtype=grad_dtype, device=dev)
+    new = _new(dev)
+    dy, dx = new(bf, T, dv), new(grad_dtype, T, dm)
+    dW1, dW2 = new(grad_dtype, dm, dv), new(grad_dtype, dv, dm)
     a = _lib.MemplusBwd8Args(T, dm, dv, fmt, _dt(dx), _ptr(x8), _ptr(x_scales), _ptr(W1), _ptr(W2),
                              _ptr(y8), _ptr(y_scales), _ptr(dout), _ptr(dy), _ptr(dx), _ptr(dW1), _ptr(dW2),
                              None, 0)
-    need = int(load().pkm_memplus_backward_act8_workspace_size(ctypes.byref(a)))
-    workspace = _workspace(workspace, need, dev)
-    a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    need = load().pkm_memplus_backward_act8_workspace_size(ctypes.byref(a))
+    workspace = _workspace(a, workspace, need, dev)
     _enqueue("pkm_memplus_backward_act8", (ctypes.byref(a),), dev)
     return dict(dy=dy, dx=dx, dW1=dW1, dW2=dW2)

@@ -203,4 +203,4 @@ def test_binding_refuses_tensors_of_another_device_than_the_stream():
             f(x, stream=Stream())
     # what the check compares: no CPU call can hold a tensor of another GPU
     with pytest.raises(ValueError):
-        skv._same_device(Stream.device, x)
+        skv._operands(Stream.device, x)
