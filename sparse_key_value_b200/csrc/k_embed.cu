@@ -28,8 +28,8 @@
 // 4.9 TB/s, the rest in L2); gradient of those tokens over 131072 x 1024 fp32
 // 98 us, bound by the write of its 537 MB (5.8 TB/s with reading dout, over all
 // launches: the sort's 17 us go beside the first 112 MiB of zeros); 65536 tokens
-// 172 us; 509 tokens over 32003 x 520 fp32 17 us and over
-// 8192 x 512 14, bound by the call's host side.
+// 172 us; 509 tokens over 32003 x 520 fp32 17 us and 512 over
+// 8192 x 512 14, two dependent launches.
 #include "kernels.h"
 #include "q8.cuh"
 #include "tc_pair.cuh"
@@ -170,8 +170,8 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t a, uint32_t b
 // of this CTA's tokens with digit d in the warps before w and total[d] the
 // first place of the CTA's tokens with digit d.  Three CTA barriers' worth of
 // work, two of them over the cluster.
-__device__ __forceinline__ void sort_places(uint16_t* cnt, uint32_t* total, uint32_t* scan, int bins,
-                                            uint32_t ncta, uint32_t rank) {
+__device__ __forceinline__ void sort_places(uint16_t* cnt, uint32_t* total, uint32_t* scan,
+                                            int bins, uint32_t ncta, uint32_t rank) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __syncthreads();
   if (tid < bins) {
@@ -524,7 +524,8 @@ __global__ void __launch_bounds__(kSumUnits) embed_sum_kernel(
   // what the 32 chunks after this one begin with
   const int64_t chunks = (T + kChunk - 1) / kChunk;
   uint32_t ahead = mark;
-  if (threadIdx.x < 32 && c + 1 + threadIdx.x < chunks) ahead = skey[(c + 1 + threadIdx.x) * kChunk];
+  if (threadIdx.x < 32 && c + 1 + threadIdx.x < chunks)
+    ahead = skey[(c + 1 + threadIdx.x) * kChunk];
   // the key before the last chunk (mark sorts last, so it is no earlier key)
   const uint32_t before = i0 > kChunk ? skey[i0 - kChunk - 1] : mark;
   __syncthreads();
@@ -739,7 +740,9 @@ EmbedLayout embed_layout(const pkm_embed_args* a) {
   L.skey = take(T * 4);
   L.spos = take(T * 4);
   L.radix = L.cluster ? 0 : take(radix_sort_workspace(a->T));
-  L.bitmap = L.cluster && a->T > kRankMost && !a->accumulate ? take((size_t)(a->n_rows + 31) / 32 * 4) : 0;
+  L.bitmap = L.cluster && a->T > kRankMost && !a->accumulate
+                 ? take((size_t)(a->n_rows + 31) / 32 * 4)
+                 : 0;
   L.cross = take((chunks + 1) * 16);  // count, then ids over three chunks or more
   L.done = a->T <= kJoinMost ? take(chunks * (size_t)sum_slices(a->d) * 4) : 0;
   L.first = take(chunks * d * 4);
@@ -802,8 +805,8 @@ cudaError_t embed_sums(const pkm_embed_args* a, const EmbedLayout& L, char* ws,
   const unsigned blocks = (unsigned)(chunks - 2 < kJoinBlocks ? chunks - 2 : kJoinBlocks);
   note_launch();
   return launch_maybe_pdl(true, embed_join_kernel<GT>, dim3(blocks, (units + 31) / 32),
-                          dim3(32 * kJoinWarps), 0, st, a->d, a->scale, a->accumulate, grad, first, last,
-                          n_cross, cross);
+                          dim3(32 * kJoinWarps), 0, st, a->d, a->scale, a->accumulate, grad, first,
+                          last, n_cross, cross);
 }
 
 // The one-cluster sort; the rows below fill->first are zeroed beside it.

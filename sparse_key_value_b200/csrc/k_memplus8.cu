@@ -197,7 +197,9 @@ struct Mp8Layout {
 // cut into slices of at least four k-blocks (a unit of the plan takes as long
 // as 2 MB of the slices' traffic).
 PairPlan grads_plan(int64_t T, int dm, int dv) {
-  const auto tiles = [](int64_t m, int64_t n, int tn) { return (m + 255) / 256 * ((n + tn - 1) / tn); };
+  const auto tiles = [](int64_t m, int64_t n, int tn) {
+    return (m + 255) / 256 * ((n + tn - 1) / tn);
+  };
   return pair_plan([&](int tn) { return tiles(dm, dv, tn) + tiles(dv, dm, tn); },
                    (T + gp::kKB - 1) / gp::kKB, 64, 4, 2.0 * dm * dv * 8 / (2 << 20),
                    [&](int tn) { return tiles(T, dm, tn); }, (dv + gp::kKB - 1) / gp::kKB);
@@ -241,7 +243,8 @@ pkm_status mp8_validate(const pkm_memplus_bwd8_args* g, Mp8Layout* L) {
   if (s != PKM_OK) return s;
   if (!need16(g->dW1) || !need16(g->dW2)) return PKM_ERR_INVALID_ARG;
   if (g->T == 0) return PKM_OK;
-  const void* need[] = {g->x8, g->x_scales, g->W1, g->W2, g->y8, g->y_scales, g->dout, g->dy, g->dx};
+  const void* need[] = {g->x8,       g->x_scales, g->W1, g->W2, g->y8,
+                        g->y_scales, g->dout,     g->dy, g->dx};
   for (const void* p : need)
     if (!need16(p)) return PKM_ERR_INVALID_ARG;
   *L = mp8_layout(g);
@@ -288,7 +291,8 @@ cudaError_t memplus8_backward(const pkm_memplus_bwd8_args* g, const Mp8Layout& L
   float* w2 = direct ? static_cast<float*>(g->dW2) : reinterpret_cast<float*>(ws + L.w2);
   {  // dW1 = x^T da, dW2 = z^T dout, dx = da W1^T
     PairMaps<3> m;
-    if (!pair_map(&m.a[0], xb, dm, (int)T, dm, true) || !pair_map(&m.b[0], da, dv, (int)T, dv, true) ||
+    if (!pair_map(&m.a[0], xb, dm, (int)T, dm, true) ||
+        !pair_map(&m.b[0], da, dv, (int)T, dv, true) ||
         !pair_map(&m.a[1], z, dv, (int)T, dv, true) ||
         !pair_map(&m.b[1], g->dout, dm, (int)T, dm, true) ||
         !pair_map(&m.a[2], da, T, dv, dv, false) || !pair_map(&m.b[2], g->W1, dm, dv, dv, false))

@@ -343,7 +343,9 @@ XentLayout xent_layout(const pkm_xent_args* a) {
   int64_t most = kPieceBytes / 2 / Tt / gp::kTileN * gp::kTileN;
   if (most < kMinPiece) most = kMinPiece;
   const int64_t fewest = (V + most - 1) / most;
-  const auto tiles = [](int64_t m, int64_t n, int tn) { return (m + 255) / 256 * ((n + tn - 1) / tn); };
+  const auto tiles = [](int64_t m, int64_t n, int tn) {
+    return (m + 255) / 256 * ((n + tn - 1) / tn);
+  };
   double best = -1;
   // (a short batch's products take less time than weighing more plans)
   for (int64_t n = fewest; n <= fewest + (Tt >= 1024 && V >= 8 * kMinPiece ? 3 : 0); ++n) {
