@@ -170,7 +170,7 @@ struct PairCtl {
   uint64_t empty[gp::kMaxStages];  // each CTA: the MMAs are done with a stage
   uint64_t accf[gp::kBufs];        // each CTA: a buffer is ready
   uint64_t acce[gp::kBufs];        // leader: both epilogues drained a buffer
-  uint64_t epi[4];                 // the epilogue warps' own, one per row quarter
+  uint64_t epi[2][4];              // the epilogue warps' own, two per row quarter
   uint64_t drain;
   uint32_t tmem;
   volatile int abort;
@@ -294,7 +294,7 @@ struct EpiWarp {
   int lane, quarter, part;  // rows 32 quarter .. + 31, columns kCols part .. of a buffer
   unsigned char* stage;     // E::kWarpBytes of shared memory, 1024-byte aligned
   unsigned char* shared;    // E::kSharedBytes for all epilogue warps
-  uint64_t* bars;           // one barrier per row quarter
+  uint64_t (*bars)[4];      // two barriers per row quarter
   volatile int* abort;
   int32_t* status;
 };
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(gp::threads<E>(), 1)
       mbar_init(&ctl->accf[b], 1);
       mbar_init(&ctl->acce[b], 2 * kEpiWarps);
     }
-    for (int q = 0; q < 4; ++q) mbar_init(&ctl->epi[q], E::kBarArrivals);
+    for (int q = 0; q < 8; ++q) mbar_init(&ctl->epi[q >> 2][q & 3], E::kBarArrivals);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     fence_barrier_init();

@@ -62,7 +62,7 @@ struct XentStats {
   struct State {
     int target;
     MaxSum v;
-    int turn;
+    uint32_t turn;  // tiles so far
   };
   __device__ __forceinline__ void setup(State&, const EpiWarp&) const {}
   __device__ __forceinline__ void begin(State& s, const EpiWarp& w, int, int64_t row0, int n0,
@@ -124,17 +124,24 @@ struct XentStats {
     }
     if (n0 % tile_n + gp::kN < tile_n && n0 + gp::kN < V) return;  // the second buffer follows
     __syncwarp();
-    // two sets of slots in turn: a set is written again two tiles on, whose
-    // products need the buffers of the tile in between, and those the joining
-    // warp hands back only after it has read this set
-    float2* slot = reinterpret_cast<float2*>(w.shared) + (st.turn & 1) * 4 * 128;
+    // Two sets of slots, each with a barrier per row quarter, in turn.  A warp
+    // hands TMEM back before it comes here, so a faster one may already be here
+    // with the next tile, but no further: the products of the tile after that
+    // need the buffer of the next one back from every warp, which each gives
+    // only after it has arrived (the joining warp: after it has read) for this
+    // one.  So a phase counts the four arrivals of one tile, and a slot is
+    // written again only after it was read.  (On one barrier a fast warp's
+    // second arrival would count for a slow warp's first.)
+    const int set = st.turn & 1;
+    const uint32_t parity = (st.turn >> 1) & 1;
+    ++st.turn;
+    float2* slot = reinterpret_cast<float2*>(w.shared) + set * 4 * 128;
     slot[w.part * 128 + w.quarter * 32 + w.lane] = make_float2(st.v.mx, st.v.sum);
     __syncwarp();
-    if (w.lane == 0) mbar_arrive(&w.bars[w.quarter]);
-    const uint32_t parity = st.turn & 1;
-    st.turn ^= 1;
+    uint64_t* bar = &w.bars[set][w.quarter];
+    if (w.lane == 0) mbar_arrive(bar);
     if (w.part != 0) return;
-    if (mbar_wait_or_abort(&w.bars[w.quarter], parity, w.abort, w.status) && m < T) {
+    if (mbar_wait_or_abort(bar, parity, w.abort, w.status) && m < T) {
       for (int k = 1; k < 4; ++k) {
         const float2 q = slot[k * 128 + w.quarter * 32 + w.lane];
         st.v.join(q.x, q.y);

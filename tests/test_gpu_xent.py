@@ -208,3 +208,23 @@ def test_reproducible_captured_and_on_another_stream():
     graph.replay()
     for a, b in zip(kept, step()):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,V,d", [(65536, 150, 64), (65536, 70, 8), (40000, 200, 128),
+                                   (30000, 650, 64), (5000, 4648, 64), (3001, 9000, 128)])
+def test_many_tiles_a_pair_with_warps_out_of_step(T, V, d):
+    """Pairs of SMs that go through many tiles, some of whose column warps have
+    fewer columns than the others or none: those run ahead of the rest, and
+    the join of the four must still take each tile's own maximum and sum."""
+    x, W, t, _ = _case(T + V, T, V, d)
+    loss, lse = skv.linear_xent_forward(x, W, t, ignore_index=IGN)
+    for i in range(0, T, 8192):
+        rows = slice(i, i + 8192)
+        _, e, lse64, loss64, tol = _ref_forward(x[rows], W, t[rows])
+        bad = (lse[rows].to(F64) - lse64).abs() > tol
+        assert not bad.any(), f"lse: {int(bad.sum())}"
+        bad = (loss[rows].to(F64) - loss64).abs() > tol + e.amax(1) + U32 * loss64.abs()
+        assert not bad.any(), f"loss: {int(bad.sum())}"
+    for _ in range(20):
+        again = skv.linear_xent_forward(x, W, t, ignore_index=IGN)
+        assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
