@@ -94,7 +94,7 @@ __device__ __forceinline__ float q8_scale(uint32_t amax, pkm_q8 fmt) {
   k = max(k, kQ8MinExp);
   return __uint_as_float((uint32_t)(k + 127) << 23);
 }
-// 1 / scale (exact: -100 <= k <= 121)
+// 1 / scale (exact: -100 <= k <= 122, the largest for int8 near the top of fp32)
 __device__ __forceinline__ float q8_inverse(float scale) {
   const uint32_t b = __float_as_uint(scale);
   return b >= 0x7f800000u ? scale : __uint_as_float((254u << 23) - b);

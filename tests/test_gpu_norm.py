@@ -307,3 +307,28 @@ def test_act8_edges():
     q, s = skv.act8_store(torch.empty(0, 64, device="cuda"), "int8")
     assert q.shape == (0, 64) and skv.act8_load(q, s).shape == (0, 64)
     assert math.isfinite(float(s.sum()))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_act8_at_the_largest_values(fmt, dtype):
+    """The largest finite value of a type, alone and among others: the largest
+    scales that there are (2^120 and 2^122), the stored bytes as everywhere, and
+    what reads back is the exact product, infinite where it passes fp32."""
+    top = torch.finfo(dtype).max
+    x = torch.zeros(3, 136, dtype=torch.float64)
+    x[0, 3], x[0, 4], x[0, 130] = top, -top / 2, -top
+    x[1] = -top
+    x[2, :128] = torch.linspace(-1, 1, 128, dtype=torch.float64) * 2.0 ** 127
+    x = x.to(dtype)
+    q, s = skv.act8_store(x.cuda(), fmt)
+    ref_s = p64.scale_of(p64.group_amax(x.double()), fmt)
+    assert torch.equal(s.cpu().double(), ref_s)
+    assert float(ref_s.max()) == (2.0 ** 120 if fmt == "e4m3" else 2.0 ** 122)
+    u = x.double() / p64.expand_scales(ref_s, 136)
+    ref_q = u.float().to(torch.float8_e4m3fn) if fmt == "e4m3" else u.round().to(torch.int8)
+    assert torch.equal(q.cpu().view(torch.uint8), ref_q.view(torch.uint8))
+    v = p64.q8_values(ref_q, ref_s)
+    assert torch.isinf(v.float()).any() and torch.isfinite(v[2].float()).all()
+    for out in (BF, F32):
+        assert torch.equal(skv.act8_load(q, s, dtype=out).cpu(), v.to(out))
