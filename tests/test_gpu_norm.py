@@ -15,6 +15,7 @@ Tolerances, from the kernels' arithmetic (U = 2^-24, one fp32 rounding):
   magnitudes.
 """
 
+import ctypes
 import math
 
 import pytest
@@ -332,3 +333,65 @@ def test_act8_at_the_largest_values(fmt, dtype):
     assert torch.isinf(v.float()).any() and torch.isfinite(v[2].float()).all()
     for out in (BF, F32):
         assert torch.equal(skv.act8_load(q, s, dtype=out).cpu(), v.to(out))
+
+
+def _forward_through_abi(x, r, w, s, y, fmt):
+    """pkm_add_rmsnorm_forward with outputs of the caller's; returns (y8, scales, rstd)."""
+    T, d = x.shape
+    q = torch.empty(T, d, dtype=torch.int8, device="cuda")
+    sc = torch.empty(T, p64.q8_groups(d), device="cuda")
+    rstd = torch.empty(T, device="cuda")
+    a = skv._lib.NormArgs(T, d, skv._dt(x), 1e-6, fmt, *(skv._ptr(t) for t in (x, r, w, s, y)),
+                          *((q.data_ptr(), sc.data_ptr()) if fmt else (None, None)),
+                          rstd.data_ptr())
+    skv._enqueue("pkm_add_rmsnorm_forward", (ctypes.byref(a),), x.device)
+    return (q, sc, rstd) if fmt else (rstd,)
+
+
+@pytest.mark.parametrize("d", [8, 1000, 2048, 2056, 8192, 16384])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_forward_over_its_own_inputs(d, dtype):
+    """y over x or the residual, with the sum elsewhere or over the other one."""
+    g = torch.Generator().manual_seed(d)
+    x, r, w = (_rn(g, *s, dtype=dtype).cuda() for s in ((37, d), (37, d), (d,)))
+    for fmt in (skv.PKM_Q8_NONE, skv.PKM_Q8_INT8):
+        s0, y0 = torch.empty_like(x), torch.empty_like(x)
+        rest0 = _forward_through_abi(x, r, w, s0, y0, fmt)
+        for s_over, y_over in ((None, "x"), (None, "r"), ("x", "r"), ("r", "x"), ("x", None)):
+            t = dict(x=x.clone(), r=r.clone())
+            s = t[s_over] if s_over else torch.empty_like(x)
+            y = t[y_over] if y_over else torch.empty_like(x)
+            rest = _forward_through_abi(t["x"], t["r"], w, s, y, fmt)
+            for a, b in zip((s, y, *rest), (s0, y0, *rest0)):
+                assert torch.equal(a, b), (s_over, y_over)
+        alone = torch.empty_like(x)
+        _forward_through_abi(x, None, w, None, alone, fmt)
+        y = x.clone()
+        _forward_through_abi(y, None, w, None, y, fmt)
+        assert torch.equal(y, alone)
+
+
+@pytest.mark.parametrize("T,d", [(33, 72), (61, 1000), (3000, 2048), (610, 8192), (41, 16384)])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fmt", [None, "int8"])
+def test_backward_over_its_own_inputs(T, d, dtype, fmt):
+    """dx over dsum or dy, on both paths."""
+    g = torch.Generator().manual_seed(T)
+    h, dy, ds, w = (_rn(g, *s, dtype=dtype).cuda() for s in ((T, d), (T, d), (T, d), (d,)))
+    sc, code = None, skv.PKM_Q8_NONE
+    if fmt:
+        h, sc = skv.act8_store(h, fmt)
+        code = skv.PKM_Q8_INT8
+    rstd = torch.rand(T, generator=g).cuda() + 0.5
+    ref = skv.add_rmsnorm_backward(dy, h, w, rstd, dsum=ds, scales=sc)
+    for over in ("dy", "dsum"):
+        t = dict(dy=dy.clone(), dsum=ds.clone())
+        dw = torch.empty(d, device="cuda")
+        a = skv._lib.NormBwdArgs(T, d, skv._dt(dy), skv._dt(dy), code, skv._ptr(t["dy"]), skv._ptr(h),
+                                 skv._ptr(sc), skv._ptr(w), skv._ptr(rstd), skv._ptr(t["dsum"]),
+                                 skv._ptr(t[over]), skv._ptr(dw), None, 0)
+        need = skv.load().pkm_add_rmsnorm_backward_workspace_size(ctypes.byref(a))
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        a.workspace, a.workspace_bytes = ws.data_ptr(), need
+        skv._enqueue("pkm_add_rmsnorm_backward", (ctypes.byref(a),), dy.device)
+        assert torch.equal(t[over], ref["dx"]) and torch.equal(dw, ref["dweight"]), over
