@@ -142,3 +142,42 @@ def test_memplus_backward():
         part = skv.memplus_backward_act8(x8[e], xs[e], W1, W2, y8[e], ys[e], dout[e], grad_dtype=BF)
         _same(out["dy"][e], part["dy"])
         _same(out["dx"][e], part["dx"])
+
+
+def test_memplus_weight_gradients_over_many_tokens():
+    """dW1 and dW2, whose sums run over the tokens, at 8-bit activations of more
+    than 2^31 elements.  Every factor is positive and the last 100 tokens weigh
+    about as much as all others, so nothing cancels and no token may be lost.
+
+    Relative to the sums: da and z, half a bf16 step (2^-8) and their fp32
+    arithmetic: a and dz sums of 512 positive terms (2 * 512 U = 6e-5 each, U =
+    2^-24), the gate and its slope at a > 0 under three times that, the rest
+    some 32 U: under 1e-3 in all; the sums over T tokens, 16 products at a time
+    and at worst in one slice, T / 16 additions of 2 U, and 64 for the slices."""
+    T, dm, dv = 2_150_000, 512, 1024
+    g = torch.Generator(device="cuda").manual_seed(21)
+    W1 = _rn(dm, dv, seed=22, scale=2.0 / dm).abs()
+    W2 = _rn(dv, dm, seed=23, scale=2.0 / dm).abs()
+    x8 = torch.randint(1, 128, (T, dm), generator=g, device="cuda", dtype=torch.int8)
+    y8 = torch.randint(1, 128, (T, dv), generator=g, device="cuda", dtype=torch.int8)
+    xs = torch.full((T, dm // 128), 2.0 ** -6, device="cuda")
+    ys = torch.full((T, dv // 128), 2.0 ** -6, device="cuda")
+    dout = _rn(T, dm, seed=24).abs_()
+    dout[-100:] *= 2.0 ** 14
+    out = skv.memplus_backward_act8(x8, xs, W1, W2, y8, ys, dout)
+    # a quarter of the columns of each: the 64-bit products then take about a second
+    cv, cm = torch.arange(0, dv, 4, device="cuda"), torch.arange(0, dm, 4, device="cuda")
+    w1, w2 = W1[:, cv].double(), W2[cv].double()
+    dw1 = torch.zeros(dm, len(cv), dtype=F64, device="cuda")
+    dw2 = torch.zeros(len(cv), len(cm), dtype=F64, device="cuda")
+    for i in range(0, T, 50_000):
+        e = slice(i, i + 50_000)
+        x, y = x8[e].double() * 2.0 ** -6, y8[e][:, cv].double() * 2.0 ** -6
+        do = dout[e].double()
+        a, dz = x @ w1, do @ w2.t()
+        s = torch.sigmoid(a)
+        dw1 += x.t() @ (dz * y * s * (1 + a * (1 - s)))
+        dw2 += (y * a * s).t() @ do[:, cm]
+    rel = U16 + 1e-3 + 2 * (T / 16 + 64) * 2.0 ** -24
+    assert ((out["dW1"][:, cv].double() - dw1).abs() <= rel * dw1).all()
+    assert ((out["dW2"][cv][:, cm].double() - dw2).abs() <= rel * dw2).all()
