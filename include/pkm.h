@@ -587,8 +587,11 @@ PKM_API pkm_status pkm_embed_backward(const pkm_embed_args *args, pkm_stream_t s
  * operand type of its products: dx and dW carry that half step per term also
  * in fp32.  The forward reads x, W, targets; the backward also lse (the
  * forward's) and dloss.  Each direction has its own workspace size (the
- * backward's holds one piece of d, at most 512 MiB or 1024 columns, and fp32
- * sums of dx).  Results are bitwise reproducible.
+ * backward's holds one piece of d, at most 512 MiB or 1024 columns, and, but
+ * for a single slice with fp32 gradients, fp32 sums of dx: one [T, d] for each
+ * slice that a piece's columns are cut into, as many as fill the GPU, at most
+ * 64).  The sizes follow from T, V, d and grad_dtype; a smaller workspace is
+ * refused.  Results are bitwise reproducible.
  * Limits: dtype PKM_BF16 (PKM_F32: PKM_ERR_UNSUPPORTED); d a multiple of 8,
  * d <= 65536; T, V <= 2^30; ceil(T / 256) * ceil(V / 256) < 2^30
  * (PKM_ERR_UNSUPPORTED above).  T = 0 is a valid empty call (the backward then

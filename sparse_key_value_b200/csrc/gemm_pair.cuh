@@ -227,7 +227,7 @@ __device__ __forceinline__ void tma_add_3d(const void* map, const void* smem, in
 __device__ __forceinline__ void bulk_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// this thread's tensor stores have read their shared memory
+// this thread's writes to shared memory are visible to tensor copies issued after it
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }

@@ -24,12 +24,14 @@
 // radix sort.
 // No atomics on values: the same bits every run, and a frequent id spreads
 // over many blocks (a short list's over the warps of a block).
-// Measured on one B200: forward of 16384 x 1024 bf16 9.7 us (48 MB distinct:
-// 4.9 TB/s, the rest in L2); gradient of those tokens over 131072 x 1024 fp32
-// 98 us, bound by the write of its 537 MB (5.8 TB/s with reading dout, over all
+// Measured on one B200: forward of 16384 x 1024 bf16 9.2 us (48 MB distinct:
+// 5.2 TB/s, the rest in L2); gradient of those tokens over 131072 x 1024 fp32
+// 99.7 us, bound by the write of its 537 MB (5.7 TB/s with reading dout, over all
 // launches: the sort's 17 us go beside the first 112 MiB of zeros); 65536 tokens
-// 172 us; 509 tokens over 32003 x 520 fp32 17 us and 512 over
-// 8192 x 512 14, two dependent launches.
+// 170 us and 131072 tokens 254, bound by the sort, which eight SMs do through
+// global memory; added to an existing gradient, where no zeros hide the sort,
+// 16384 tokens 40 us and 65536 110; 509 tokens over 32003 x 520 fp32 17.5 us and
+// 512 over 8192 x 512 12.7, two dependent launches.
 #include "kernels.h"
 #include "q8.cuh"
 #include "tc_pair.cuh"
@@ -41,22 +43,27 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 16;   // sorted tokens per block
 constexpr int kAhead = 8;    // rows of dout in flight per thread
-// Tokens sorted by counting, at most.  The whole gradient over 32768 x 1024
-// fp32, by counting and by the cluster: 512 tokens 28.6 and 36.8 us, 1024 32.2
-// and 38.6, 2048 35.0 and 38.4, 4096 48.3 and 39.9 (counting is quadratic; all of
-// these before the rows were zeroed by warps).
+// Tokens sorted by counting, at most (counting is quadratic).  The whole
+// gradient, by counting and by the cluster: over 32768 x 1024 fp32 512 tokens
+// 24.6 and 28.4 us, 1024 27.2 and 29.6, 1536 35.3 and 29.3, 2048 32.6 and 30.0,
+// 4096 46.7 and 31.8; over 8192 x 512 512 12.7 and 16.9, 1024 16.7 and 17.7, 2048
+// 20.7 and 18.4; added to 131072 x 1024 512 11.4 and 18.0, 1024 16.8 and 19.9,
+// 1536 24.9 and 20.2, 2048 18.7 and 20.5.  Up to kJoinMost counting is ahead
+// everywhere; from there to this limit the cluster mostly is, by 2 to 6 us.
 constexpr int kRankMost = 2048;
 // Tokens whose long ids' parts are joined by the sums' own blocks, at most.  The
-// gradient of 100 and of 512 tokens over 8192 x 512 17.1 us with the join's
-// launch and 14.4 without, 1024 over 32768 x 1024 30.2 and 27.9; 2048 32.4 and
-// 32.9, and 17.1 and 27.5 where those are of two ids (one block joins 64 parts).
+// gradient with the join's launch and without: 100 tokens over 8192 x 512 13.5
+// and 11.4 us, 512 13.7 and 12.7, 1024 over 32768 x 1024 31.6 and 27.2; 2048 32.6
+// and 35.2.  Where all tokens are of two ids a block joins T / 32 parts: 1024
+// over 8192 x 512 13.7 and 17.9, 2048 19.9 and 28.1.
 constexpr int kJoinMost = 1024;
 constexpr int kSortThreads = 1024;
 constexpr int kSortCluster = 8;
 // Tokens per thread of the sorting cluster, at most.  The whole gradient over
-// 131072 x 1024 fp32, by the cluster and by the multi-block sort: 2048 tokens 89
-// and 167 us, 65536 213 and 260, 131072 339 and 344; twice as many over 131072 x
-// 512 476 and 380 (before the rows were zeroed by warps).
+// 131072 x 1024 fp32, by the cluster and by the multi-block sort: 40000 tokens 137
+// and 201 us, 65536 170 and 220, 131072 255 and 261; added to an existing one
+// 65536 110 and 156, 131072 193 and 207; twice as many over 131072 x 512 333 and
+// 242.
 constexpr int kSortRounds = 16;
 constexpr int64_t kSortMost = (int64_t)kSortThreads * kSortRounds * kSortCluster;
 constexpr int kMaxDigit = 9;     // bits per pass
@@ -772,9 +779,13 @@ pkm_status embed_validate(const pkm_embed_args* a, bool backward) {
 }
 
 // Rows zeroed beside the sort: about as many bytes as the memory takes in the
-// sort's time (16384 tokens over 131072 x 1024: 64 MiB 104 us, 96 101.2, 128
-// 100.4; 4096 over 32768 x 1024 33.8, 31.0, 31.5, all before the join got its
-// ids' ends from the sums).
+// time of the cluster's sort of up to 16384 tokens.  The gradient with 64, 96,
+// 112, 128 and 224 MiB: 4096 tokens over 32768 x 1024 32.8, 31.9, 31.8, 32.9 (all
+// 128) us, 16384 over 131072 x 1024 102.0, 100.1, 99.9, 99.9 and 101.7, 32768
+// 128.4, 124.7, 122.8, 121.3 and 119.9, 131072 256, 255, 254.5, 254 and 249: a longer
+// sort would take more.  By counting, with 4, 8, 16, 32 and 64 MiB: 509 over 32003
+// x 520 17.0, 17.1, 17.6, 17.6 and 20.6, 512 over 32768 x 1024 25.9, 25.9, 24.7,
+// 25.2 and 29.0.
 constexpr int64_t kFillBeside = int64_t(112) << 20, kFillBesideRank = int64_t(16) << 20;
 
 template <pkm_dtype DT, pkm_dtype GT>

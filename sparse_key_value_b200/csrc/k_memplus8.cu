@@ -15,11 +15,13 @@
 // launch, the weight gradients (few tiles, a long contraction over the tokens)
 // cut into slices that are summed in order.
 // Bound by the tensor cores for long batches (10 T d_model d_v operations),
-// by launches for short ones.  Measured on one B200: 16384 x 1024 x 1024 179 us
-// back to back (0.96 PFLOP/s, at the power limit), alone: reading x back 8.5, a
-// and dz 62 (operands from L2: 64 bytes per SM and cycle where each accumulator
-// has 256 columns; 11 for writing dy, da and z), the three products 63 (1.6
-// PFLOP/s), the slices' sum 7.  1000 x 640 x 520: 32 us, four dependent launches.
+// by launches for short ones.  Measured on one B200: 16384 x 1024 x 1024 181-184
+// us back to back (0.94 PFLOP/s; the power cap holds the SMs at 1451 MHz then),
+// alone and at full clock: reading x back 8.5, a and dz 62 (operands from L2: 64
+// bytes per SM and cycle where each accumulator has 256 columns, the tensor pipe
+// busy half the time; 11 for writing dy, da and z), the three products 63 (1.6
+// PFLOP/s), the slices' sum 7.  1000 x 640 x 520: 32 us, four dependent launches,
+// the longest (a and dz, 256 x 256 a pair of SMs) on 12 pairs of 74.
 #include <math.h>
 
 #include "gemm_pair.cuh"
@@ -34,13 +36,13 @@ namespace {
 // the warp's staging rows.  A lane takes its 128 columns of a into registers
 // while dz is still being worked on, so that a of the next tile can follow; the
 // columns move down one place a turn, which keeps the loop short and its
-// registers fixed (against a and dz read together: 16384 x 1024 x 1024 184 -> 180
-// us in all, the launch alone 76 -> 66 from cold caches; unrolled four times 181,
-// and 1000 x 640 x 520 34 us for 32, the longer code's first pass).  Two sets of
-// staging rows: with one, and five ring stages, the short batch took 33 us.
-// The lane's bytes of y for the next columns are
-// loaded while these are worked on, the tile's first before its products are
-// done; a warp's columns lie in one quantisation group, so a lane has one scale.
+// registers fixed (against a and dz read together, on one box: 16384 x 1024 x
+// 1024 184 -> 180 us in all, the launch alone 76 -> 66 from cold caches; unrolled
+// four times 181, and 1000 x 640 x 520 34 us for 32, the longer code's first
+// pass).  Two sets of staging rows: with one, and five ring stages, the short
+// batch took 33 us.  The lane's bytes of y for the next columns are loaded while
+// these are worked on, the tile's first before its products are done; a warp's
+// columns lie in one quantisation group, so a lane has one scale.
 struct Memplus8Gate {
   CUtensorMap dy_map, da_map, z_map;
   int64_t T;

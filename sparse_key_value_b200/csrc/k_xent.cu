@@ -22,9 +22,11 @@
 // Measured on one B200 at 8192 x 32768 x 1024: forward 395-420 us (1.31-1.39
 // PFLOP/s; the library's product of the same sizes, which writes the logits and
 // reads none back, 442-466), 340 us alone on a cool GPU; backward 1.27-1.32 ms
-// (1.25-1.30 PFLOP/s).  Back to back both run into the power limit, which holds
-// plain products at 1.42.  Short batches are bound by reading W: 37 x 50021 x
-// 512 20.7 us, 51 MB.
+// (1.25-1.30 PFLOP/s).  At 16384 x 131072 x 1024 3.27 ms (the library's product
+// 3.66) and 10.3 ms.  Back to back both run into the power cap (SMs at 1425 and
+// 1294 MHz), which holds plain products at 1.40-1.42.  Short
+// batches: 37 x 50021 x 512 20.4 us for the 51 MB of W, its gradients 62 us (W
+// read twice, dW written, 256 rows of a tile for 37 tokens).
 #include <math.h>
 
 #include "gemm_pair.cuh"
